@@ -539,6 +539,121 @@ PA_API pa_status pa_qk_norm_rope_kv_write(const void *q, const void *k, const vo
                                           void *q_out, const pa_kv_pool *pool, pa_stream_t stream);
 
 /*
+ * ---- long contexts --------------------------------------------------------------
+ * Rotary positions of any layout and scaling in front of the cache, and a cache
+ * that is held within a budget.  No counterpart on the pages beyond the rotary
+ * embedding of [P1] (apply_rope): library additions.
+ */
+
+/*
+ * Rotary embedding: the pair of dims i and i + rotary_dim / 2 (PA_ROPE_HALF) or
+ * 2 i and 2 i + 1 (PA_ROPE_INTERLEAVED), i < rotary_dim / 2, of a row at
+ * position p turns by the angle p * inv_freq[i]: with (c, s) =
+ * attention_factor * (cos, sin) of it, (a, b) becomes (a c - b s, b c + a s).
+ * Dims from rotary_dim on are left as they are.
+ */
+#define PA_ROPE_HALF 0
+#define PA_ROPE_INTERLEAVED 1
+typedef struct {
+  const double *inv_freq;   /* DEVICE [rotary_dim / 2], radians per position; finite */
+  int32_t rotary_dim;       /* even, 2 .. 128 */
+  int32_t layout;           /* PA_ROPE_HALF or PA_ROPE_INTERLEAVED */
+  float attention_factor;   /* multiplies cos and sin (1: none); finite */
+} pa_rope;
+
+/*
+ * rope_inv_freq — the inverse frequencies of a rotary embedding of base theta
+ * (> 1), scaled for contexts `factor` (>= 1) times the trained length, into the
+ * HOST array inv_freq [rotary_dim / 2], and its attention factor (host code; no
+ * GPU work).  With f_i = theta^(-2 i / rotary_dim):
+ *   PA_ROPE_PLAIN   f_i
+ *   PA_ROPE_LINEAR  f_i / factor (position interpolation)
+ *   PA_ROPE_NTK     the base theta * factor^(d / (d - 2)), d = rotary_dim
+ *   PA_ROPE_BANDS   f_i where it turns more than `fast` times over
+ *                   trained_length, f_i / factor where less than `slow` times,
+ *                   linearly mixed by the number of turns between
+ *   PA_ROPE_YARN    ("YaRN: Efficient Context Window Extension of Large
+ *                   Language Models", sections 3.2 and 3.4) f_i and f_i / factor mixed by
+ *                   a ramp over i between the (rounded) pairs that turn `fast`
+ *                   and `slow` times; attention factor 0.1 ln(factor) + 1
+ * The attention factor of the others is 1.  slow and fast (0 < slow < fast;
+ * e.g. 1 and 4 for BANDS, 1 and 32 for YARN) and trained_length are read by
+ * BANDS and YARN alone, factor by all but PLAIN.  A value out of range:
+ * PA_ERR_SHAPE; another scaling: PA_ERR_UNSUPPORTED.
+ */
+#define PA_ROPE_PLAIN 0
+#define PA_ROPE_LINEAR 1
+#define PA_ROPE_NTK 2
+#define PA_ROPE_BANDS 3
+#define PA_ROPE_YARN 4
+PA_API pa_status pa_rope_inv_freq(int32_t scaling, int32_t rotary_dim, double theta, double factor,
+                                  double trained_length, double slow, double fast, double *inv_freq,
+                                  float *attention_factor);
+
+/*
+ * rope_kv_write — for each new token t:
+ *   q_out[t][g] = rope(norm(q[t][g], q_norm_weight), positions[t])  (every query head g),
+ *   slot_mapping[t] receives K = rope(norm(k[t][h], k_norm_weight), positions[t]) and V = v[t][h].
+ * norm(x, w) = x / sqrt(mean(x^2) + eps) * w, or x where the weights are NULL
+ * (both or neither).  fp32 throughout, each output rounded once to the pool
+ * dtype (pa_qk_norm_rope_kv_write rounds after every step as the page's model
+ * does, and takes 16-bit tables).  Angles are exact to fp32 at any position:
+ * the fraction of a turn is taken in 64-bit fixed point.
+ *   q, q_out      [num_tokens][num_q_heads][128], pool dtype; q_out may be q.
+ *   k, v          [num_tokens][num_kv_heads][128], pool dtype.
+ *   rope          HOST descriptor, read during the call (its inv_freq is device memory).
+ *   positions     int32 [num_tokens]; the cache index of a token plays no part,
+ *                 so positions may run ahead of a cache that pa_kv_evict shortened.
+ *   slot_mapping  int64 [num_tokens] as for pa_kv_cache_write.
+ * A token with a negative position or a slot outside the pool records
+ * PA_ERR_RANGE (detail: the token) and nothing of it is written.  Two tokens
+ * with the same slot in one call race.  All pointers 16-byte aligned
+ * (positions 4; slot_mapping, inv_freq 8).
+ */
+PA_API pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, const pa_rope *rope,
+                                  const void *q_norm_weight, const void *k_norm_weight, float eps,
+                                  const int32_t *positions, const int64_t *slot_mapping, int32_t num_tokens,
+                                  int32_t num_q_heads, void *q_out, const pa_kv_pool *pool, pa_stream_t stream);
+
+/*
+ * kv_evict — shorten each sequence's cache to at most `budget` tokens, for
+ * every KV head by its own weights.  Of the ctx = context_lens[s] tokens of
+ * sequence s, for KV head h:
+ *   ctx <= budget   every token stays;
+ *   ctx >  budget   the first `sinks`, the last `recent`, and of those between
+ *                   the budget - sinks - recent of largest weights[s][h][j]
+ *                   (equal weights: the lower j first; a NaN below every number).
+ * With n = min(ctx, budget), the tokens that stay keep their order: the i-th
+ * of them, position j in the source, moves to position i of dst_block_tables[s]
+ * (its K and V rows, bit for bit), kept[s][h][i] = j and weights_out[s][h][i] =
+ * weights[s][h][j].  kept[s][h][n .. budget) = -1; weights_out[s][h][i] = 0 for
+ * n <= i < min(ctx, weights_out_stride), the rest of it is left; new_context_lens[s] = n.
+ *   weights           fp32 [num_seqs][num_kv_heads][weights_stride].
+ *   block_tables      int32 [num_seqs][max_blocks_per_seq].
+ *   dst_block_tables  int32 [num_seqs][dst_max_blocks].  In place: block_tables
+ *                     itself, or entries equal to its entries.  Apart: blocks that
+ *                     no sequence of the call reads.  Blocks that sequences share
+ *                     must not be rewritten in place (pa_sequence_unshare first).
+ *   weights_out       fp32 [num_seqs][num_kv_heads][weights_out_stride]: weights
+ *                     itself with the same stride (in place), or apart from it.
+ *   kept              int32 [num_seqs][num_kv_heads][budget].
+ *   new_context_lens  int32 [num_seqs], apart from context_lens.
+ * budget >= 1, recent, sinks >= 0, recent + sinks <= budget; num_seqs at most
+ * 16384.  A sequence whose length is 0, beyond its table or beyond
+ * weights_stride, or whose n does not fit dst_max_blocks or
+ * weights_out_stride, records PA_ERR_RANGE (detail: the sequence) and nothing
+ * of it is written.  A block id outside the pool, in either table, is recorded
+ * likewise and its rows are not moved.  The result does not depend on the
+ * order in which the GPU works.
+ */
+PA_API pa_status pa_kv_evict(const pa_kv_pool *pool, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                             const int32_t *context_lens, int32_t num_seqs, const float *weights,
+                             int32_t weights_stride, int32_t budget, int32_t recent, int32_t sinks,
+                             const int32_t *dst_block_tables, int32_t dst_max_blocks, float *weights_out,
+                             int32_t weights_out_stride, int32_t *kept, int32_t *new_context_lens,
+                             pa_stream_t stream);
+
+/*
  * ---- copy-on-write and the block-table builder [P1, qwen_serve/paged.py:
  * BlockAllocator, SequenceCache.fork_from / _cow_copy / adopt_prefix /
  * reserve / commit; task 12.1 worked examples and acceptance item 5] --------
@@ -627,6 +742,16 @@ PA_API pa_status pa_sequence_adopt_prefix(pa_sequence *seq, const int32_t *block
 /* Makes the empty sequence `seq` a copy of `other` (same allocator, nothing
  * reserved): every block is shared by reference, the length is copied. */
 PA_API pa_status pa_sequence_fork(pa_sequence *seq, const pa_sequence *other);
+/* Gives the sequence blocks of its own in place of those of its first n blocks
+ * (n <= the blocks held, else PA_ERR_SHAPE) that others share: each is replaced
+ * by a fresh block and the (src, dst) pair recorded for pa_kv_block_copy(), as
+ * by reserve() on a shared block.  For a call that rewrites blocks in place
+ * (pa_kv_evict).  All or nothing (PA_ERR_NO_BLOCKS). */
+PA_API pa_status pa_sequence_unshare(pa_sequence *seq, int32_t n);
+/* Shortens the sequence to its first n committed tokens (0 <= n <= length, else
+ * PA_ERR_SHAPE; nothing may be reserved: PA_ERR_STATE), releasing the blocks
+ * past them: after pa_kv_evict, n is the sequence's new length. */
+PA_API pa_status pa_sequence_truncate(pa_sequence *seq, int32_t n);
 /* Releases every block; the sequence is empty again. */
 PA_API pa_status pa_sequence_release(pa_sequence *seq);
 /* Committed tokens, reserved-but-uncommitted tokens, and blocks held. */

@@ -17,6 +17,9 @@ Calls (see include/pagedattn.h for the full contract):
   (``alloc_pool_f8``: the same layout with E4M3 codes held as uint8)
 * ``paged_attn_decode_window`` / ``paged_attn_prefill_chunk_window``: sliding window
 * ``qk_norm_rope_kv_write``: q/k RMSNorm + rotary embedding fused into the KV write
+* ``rope_kv_write``: rotary embedding of any layout, width and frequencies (``rope_inv_freq``
+  for the long-context scalings), with the KV write
+* ``kv_evict``: a cache shortened to a budget by accumulated attention weight
 * ``kv_block_copy(pools, pairs)``: copy-on-write block copy over every layer
 * ``BlockAllocator`` / ``Sequence`` / ``build_step_tables``: the host-side block
   allocator and block-table builder (native code in the same library; no GPU)
@@ -49,7 +52,8 @@ EXPORTS = ("pa_kv_cache_write", "pa_decode_workspace_bytes", "pa_paged_attn_deco
            "pa_qk_norm_rope_kv_write", "pa_paged_attn_decode_append", "pa_selftest_bounded_wait",
            "pa_paged_attn_decode_ex", "pa_paged_attn_decode_q8_ex", "pa_prefill_workspace_bytes",
            "pa_paged_attn_prefill_chunk_ex", "pa_paged_attn_prefill_chunk_q8", "pa_mixed_step",
-           "pa_mixed_step_workspace_bytes",
+           "pa_mixed_step_workspace_bytes", "pa_rope_inv_freq", "pa_rope_kv_write", "pa_kv_evict",
+           "pa_sequence_unshare", "pa_sequence_truncate",
            "pa_allocator_create", "pa_allocator_destroy", "pa_allocator_allocate", "pa_allocator_retain",
            "pa_allocator_release", "pa_allocator_refcount", "pa_allocator_stats_get", "pa_allocator_take_copies",
            "pa_sequence_create", "pa_sequence_destroy", "pa_sequence_reserve", "pa_sequence_commit",
@@ -75,6 +79,11 @@ class KVPoolQ8(ctypes.Structure):
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
                 ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("attention_factor", ctypes.c_float)]
 
 
 class AllocatorStats(ctypes.Structure):
@@ -149,6 +158,15 @@ def load_library(path: str = LIB_PATH):
         lib.pa_qk_norm_rope_kv_write.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, i32, P, P, i32, i32, P,
                                                  pool_p, P]
         lib.pa_qk_norm_rope_kv_write.restype = i32
+        f64 = ctypes.c_double
+        lib.pa_rope_inv_freq.argtypes = [i32, i32, f64, f64, f64, f64, f64, ctypes.POINTER(f64),
+                                         ctypes.POINTER(ctypes.c_float)]
+        lib.pa_rope_inv_freq.restype = i32
+        lib.pa_rope_kv_write.argtypes = [P, P, P, ctypes.POINTER(Rope), P, P, ctypes.c_float, P, P, i32, i32, P,
+                                         pool_p, P]
+        lib.pa_rope_kv_write.restype = i32
+        lib.pa_kv_evict.argtypes = [pool_p, P, i32, P, i32, P, i32, i32, i32, i32, P, i32, P, i32, P, P, P]
+        lib.pa_kv_evict.restype = i32
         lib.pa_selftest_bounded_wait.argtypes = [ctypes.c_uint32, P]
         lib.pa_selftest_bounded_wait.restype = i32
         lib.pa_kv_block_copy.argtypes = [pool_p, i32, P, i32, P]
@@ -162,6 +180,7 @@ def load_library(path: str = LIB_PATH):
                 ("pa_allocator_take_copies", [P, ip, i32, ip], i32),
                 ("pa_sequence_create", [P, ctypes.POINTER(P)], i32), ("pa_sequence_destroy", [P], None),
                 ("pa_sequence_reserve", [P, i32, ctypes.POINTER(i64)], i32),
+                ("pa_sequence_unshare", [P, i32], i32), ("pa_sequence_truncate", [P, i32], i32),
                 ("pa_sequence_commit", [P, i32], i32), ("pa_sequence_adopt_prefix", [P, ip, i32], i32),
                 ("pa_sequence_fork", [P, P], i32), ("pa_sequence_release", [P], i32),
                 ("pa_sequence_length", [P], i32), ("pa_sequence_reserved", [P], i32),
@@ -719,6 +738,139 @@ def qk_norm_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_n
     return q_out
 
 
+# ---- long contexts: rotary positions, eviction -------------------------------------------
+
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = range(5)
+
+
+def _here(**tensors) -> None:
+    """The library launches on the current device: its tensors must live there."""
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+
+
+def _hold(stream, *tensors) -> None:
+    """Tensors allocated here for a call on another stream than the current one:
+    the allocator must not hand their memory out before that stream is done with it."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def rope_inv_freq(rotary_dim: int, theta: float, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+                  trained_length: float = 1.0, slow: float = 1.0, fast: float = 32.0, device=None):
+    """Inverse frequencies (float64 [rotary_dim / 2], on ``device``, default the
+    current CUDA device) and attention factor of a rotary embedding scaled for
+    contexts ``factor`` times ``trained_length`` (see ``pa_rope_inv_freq``)."""
+    buf = (ctypes.c_double * max(int(rotary_dim) // 2, 1))()
+    att = ctypes.c_float()
+    _check(load_library().pa_rope_inv_freq(scaling, int(rotary_dim), float(theta), float(factor),
+                                           float(trained_length), float(slow), float(fast), buf, ctypes.byref(att)),
+           "pa_rope_inv_freq")
+    return torch.tensor(list(buf), dtype=torch.float64, device=device or "cuda"), float(att.value)
+
+
+def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: torch.Tensor,
+                  positions: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  interleaved: bool = False, attention_factor: float = 1.0,
+                  q_norm_weight: Optional[torch.Tensor] = None, k_norm_weight: Optional[torch.Tensor] = None,
+                  eps: float = 1e-6, q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rotate q [T, Hq, 128] (returned; ``q_out=q`` works in place) and k
+    [T, Hkv, 128] to ``positions``, after an RMSNorm where the weights are given,
+    and write the rotated k and the unchanged v into their slots.
+    ``inv_freq`` (float64 [rotary_dim / 2]) sets how much of the head turns."""
+    pool = make_pool(k_cache, v_cache)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _need(t, name, k_cache.dtype)
+    for name, t in (("q_norm_weight", q_norm_weight), ("k_norm_weight", k_norm_weight)):
+        if t is not None:
+            _need(t, name, k_cache.dtype)
+            if t.shape != (pool.head_dim,):
+                raise ValueError(f"{name} must be [{pool.head_dim}]")
+    _need(inv_freq, "inv_freq", torch.float64)
+    _need(positions, "positions", torch.int32)
+    _need(slot_mapping, "slot_mapping", torch.int64)
+    if q.dim() != 3 or inv_freq.dim() != 1:
+        raise ValueError("q must be [T, Hq, 128], inv_freq [rotary_dim / 2]")
+    T, hq, d = q.shape
+    if d != pool.head_dim or k.shape != (T, pool.num_kv_heads, d) or v.shape != k.shape or positions.shape != (T,) \
+            or slot_mapping.shape != (T,):
+        raise ValueError("q [T, Hq, 128], k/v [T, Hkv, 128], positions/slot_mapping [T]")
+    fresh = q_out is None
+    if fresh:
+        q_out = torch.empty_like(q)
+    _need(q_out, "q_out", q.dtype)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have the shape of q")
+    _here(q=q, k=k, v=v, inv_freq=inv_freq, positions=positions, slot_mapping=slot_mapping, k_cache=k_cache,
+          v_cache=v_cache, q_norm_weight=q_norm_weight, k_norm_weight=k_norm_weight, q_out=q_out)
+    rope = Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), ROPE_INTERLEAVED if interleaved else ROPE_HALF,
+                float(attention_factor))
+    wq, wk = (None if t is None else t.data_ptr() for t in (q_norm_weight, k_norm_weight))
+    _check(load_library().pa_rope_kv_write(q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(rope), wq, wk,
+                                           float(eps), positions.data_ptr(), slot_mapping.data_ptr(), T, hq,
+                                           q_out.data_ptr(), ctypes.byref(pool), _stream(stream)),
+           "pa_rope_kv_write")
+    if fresh:
+        _hold(stream, q_out)
+    return q_out
+
+
+def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+             weights: torch.Tensor, budget: int, recent: int = 0, sinks: int = 0,
+             dst_block_tables: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
+             kept: Optional[torch.Tensor] = None, new_context_lens: Optional[torch.Tensor] = None,
+             max_context_len: Optional[int] = None, stream=None):
+    """Shorten every sequence's cache to ``budget`` tokens, for each KV head by
+    its own ``weights`` (fp32 [S, Hkv, stride], as ``paged_attn_decode_weights``
+    accumulates them): the first ``sinks``, the last ``recent`` and the heaviest
+    of the rest stay, in order.  The rows move within the pool to
+    ``dst_block_tables`` (default: in place) and the weights to ``weights_out``
+    (default: in place).  Returns (kept int32 [S, Hkv, budget] with -1 past the
+    new length, new context lengths int32 [S]).  ``max_context_len`` is a host
+    bound on ``context_lens`` for the check that the weights cover it."""
+    pool = make_pool(k_cache, v_cache)
+    _need(block_tables, "block_tables", torch.int32)
+    _need(context_lens, "context_lens", torch.int32)
+    _need(weights, "weights", torch.float32)
+    dst = block_tables if dst_block_tables is None else dst_block_tables
+    w_out = weights if weights_out is None else weights_out
+    _need(dst, "dst_block_tables", torch.int32)
+    _need(w_out, "weights_out", torch.float32)
+    if block_tables.dim() != 2 or dst.dim() != 2 or weights.dim() != 3 or w_out.dim() != 3:
+        raise ValueError("block_tables and dst_block_tables must be [S, max_blocks], the weights [S, Hkv, stride]")
+    S, hkv = block_tables.shape[0], pool.num_kv_heads
+    if context_lens.shape != (S,) or dst.shape[0] != S or weights.shape[:2] != (S, hkv) or \
+            w_out.shape[:2] != (S, hkv):
+        raise ValueError(f"sizes disagree: {S} sequences, {hkv} KV heads")
+    if max_context_len is not None and int(max_context_len) > weights.shape[2]:
+        raise ValueError(f"weights hold {weights.shape[2]} tokens, max_context_len is {int(max_context_len)}")
+    budget = int(budget)
+    fresh = []
+    if kept is None:
+        kept = torch.empty((S, hkv, max(budget, 0)), dtype=torch.int32, device=k_cache.device)
+        fresh.append(kept)
+    if new_context_lens is None:
+        new_context_lens = torch.empty((S,), dtype=torch.int32, device=k_cache.device)
+        fresh.append(new_context_lens)
+    _need(kept, "kept", torch.int32)
+    _need(new_context_lens, "new_context_lens", torch.int32)
+    if kept.shape != (S, hkv, budget) or new_context_lens.shape != (S,):
+        raise ValueError(f"kept must be [{S}, {hkv}, {budget}], new_context_lens [{S}]")
+    _here(k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens, weights=weights,
+          dst_block_tables=dst, weights_out=w_out, kept=kept, new_context_lens=new_context_lens)
+    _check(load_library().pa_kv_evict(ctypes.byref(pool), block_tables.data_ptr(), block_tables.shape[1],
+                                      context_lens.data_ptr(), S, weights.data_ptr(), weights.shape[2], budget,
+                                      int(recent), int(sinks), dst.data_ptr(), dst.shape[1], w_out.data_ptr(),
+                                      w_out.shape[2], kept.data_ptr(), new_context_lens.data_ptr(),
+                                      _stream(stream)), "pa_kv_evict")
+    _hold(stream, *fresh)
+    return kept, new_context_lens
+
+
 # ---- copy-on-write block copy and the host-side block-table builder ---------------------
 
 def kv_block_copy(pools, pairs: torch.Tensor, stream=None) -> None:
@@ -825,6 +977,14 @@ class Sequence:
 
     def fork_from(self, other: "Sequence") -> None:
         _check(self._lib.pa_sequence_fork(self._h, other.handle), "pa_sequence_fork")
+
+    def unshare(self, n: int) -> None:
+        """Blocks of its own in place of the shared ones among the first n (copies recorded as by ``reserve``)."""
+        _check(self._lib.pa_sequence_unshare(self._h, n), "pa_sequence_unshare")
+
+    def truncate(self, n: int) -> None:
+        """Keep the first n committed tokens and release the blocks past them."""
+        _check(self._lib.pa_sequence_truncate(self._h, n), "pa_sequence_truncate")
 
     def release(self) -> None:
         _check(self._lib.pa_sequence_release(self._h), "pa_sequence_release")

@@ -218,6 +218,38 @@ pa_status pa_sequence_commit(pa_sequence *seq, int32_t n) {
   return PA_OK;
 }
 
+pa_status pa_sequence_unshare(pa_sequence *seq, int32_t n) {
+  if (!seq) return PA_ERR_NULL;
+  if (n < 0 || n > (int32_t)seq->blocks.size()) return PA_ERR_SHAPE;
+  pa_allocator *a = seq->alloc;
+  size_t fresh = 0;
+  for (int32_t i = 0; i < n; ++i) fresh += a->refcount[seq->blocks[i]] > 1;
+  if (fresh > a->free_list.size()) return PA_ERR_NO_BLOCKS;
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t src = seq->blocks[i];
+    if (a->refcount[src] <= 1) continue;
+    const int32_t dst = take_free(a);
+    a->copies.push_back(src);
+    a->copies.push_back(dst);
+    ref_down(a, src);
+    seq->blocks[i] = dst;
+    ++a->n_cow;
+  }
+  return PA_OK;
+}
+
+pa_status pa_sequence_truncate(pa_sequence *seq, int32_t n) {
+  if (!seq) return PA_ERR_NULL;
+  if (n < 0 || n > seq->length) return PA_ERR_SHAPE;
+  if (seq->reserved != 0) return PA_ERR_STATE;
+  while ((int32_t)seq->blocks.size() > blocks_for(n)) {
+    ref_down(seq->alloc, seq->blocks.back());
+    seq->blocks.pop_back();
+  }
+  seq->length = n;
+  return PA_OK;
+}
+
 pa_status pa_sequence_adopt_prefix(pa_sequence *seq, const int32_t *blocks, int32_t n) {
   if (!seq) return PA_ERR_NULL;
   if (n < 0) return PA_ERR_SHAPE;

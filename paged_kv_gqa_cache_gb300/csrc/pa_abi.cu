@@ -739,6 +739,144 @@ pa_status pa_qk_norm_rope_kv_write(const void *q, const void *k, const void *v, 
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
+pa_status pa_rope_inv_freq(int32_t scaling, int32_t rotary_dim, double theta, double factor, double trained_length,
+                           double slow, double fast, double *inv_freq, float *attention_factor) {
+  if (!inv_freq || !attention_factor) return PA_ERR_NULL;
+  if (rotary_dim < 2 || rotary_dim > kHeadDim || rotary_dim % 2 != 0) return PA_ERR_SHAPE;
+  if (scaling < PA_ROPE_PLAIN || scaling > PA_ROPE_YARN) return PA_ERR_UNSUPPORTED;
+  if (!(theta > 1.0) || !isfinite(theta)) return PA_ERR_SHAPE;
+  if (scaling != PA_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor))) return PA_ERR_SHAPE;
+  if ((scaling == PA_ROPE_BANDS || scaling == PA_ROPE_YARN) &&
+      (!(trained_length >= 1.0) || !isfinite(trained_length) || !(slow > 0.0) || !(fast > slow) || !isfinite(fast)))
+    return PA_ERR_SHAPE;
+  const double two_pi = 6.283185307179586477, d = rotary_dim;
+  double base = theta;
+  // the last pair's wavelength stretched by `factor`, the first pair's kept
+  if (scaling == PA_ROPE_NTK && rotary_dim > 2) base = theta * pow(factor, d / (d - 2.0));
+  double lo = 0.0, hi = 1.0;
+  if (scaling == PA_ROPE_YARN) {  // the pairs that turn `fast` and `slow` times over the trained length
+    lo = floor(d * log(trained_length / (fast * two_pi)) / (2.0 * log(theta)));
+    hi = ceil(d * log(trained_length / (slow * two_pi)) / (2.0 * log(theta)));
+    lo = lo < 0.0 ? 0.0 : lo;
+    hi = hi > d - 1.0 ? d - 1.0 : hi;
+    if (hi - lo < 1e-3) hi = lo + 1e-3;
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / d);
+    if (scaling == PA_ROPE_LINEAR) f /= factor;
+    if (scaling == PA_ROPE_BANDS) {
+      double keep = (trained_length * f / two_pi - slow) / (fast - slow);
+      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+      f = (1.0 - keep) * f / factor + keep * f;
+    }
+    if (scaling == PA_ROPE_YARN) {
+      double ramp = (i - lo) / (hi - lo);
+      ramp = ramp < 0.0 ? 0.0 : ramp > 1.0 ? 1.0 : ramp;
+      f = f / factor * ramp + f * (1.0 - ramp);
+    }
+    inv_freq[i] = f;
+  }
+  *attention_factor = scaling == PA_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.f;
+  return PA_OK;
+}
+
+pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, const pa_rope *rope, const void *q_norm_weight,
+                           const void *k_norm_weight, float eps, const int32_t *positions,
+                           const int64_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads, void *q_out,
+                           const pa_kv_pool *pool, pa_stream_t stream) {
+  pa_status st = check_pool(pool);
+  if (st != PA_OK) return st;
+  if (!rope || !rope->inv_freq) return PA_ERR_NULL;
+  if (rope->rotary_dim < 2 || rope->rotary_dim > kHeadDim || rope->rotary_dim % 2 != 0) return PA_ERR_SHAPE;
+  if (rope->layout != PA_ROPE_HALF && rope->layout != PA_ROPE_INTERLEAVED) return PA_ERR_UNSUPPORTED;
+  if (!isfinite(rope->attention_factor)) return PA_ERR_SHAPE;
+  if (num_tokens < 0) return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  if (!q || !k || !v || !positions || !slot_mapping || !q_out ||
+      (q_norm_weight == nullptr) != (k_norm_weight == nullptr))
+    return PA_ERR_NULL;
+  if (num_q_heads < 1 || num_q_heads > 1024) return PA_ERR_SHAPE;
+  if (q_norm_weight && (!(eps >= 0.f) || !isfinite(eps))) return PA_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(q_norm_weight) ||
+      !aligned16(k_norm_weight) || !aligned4(positions) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) ||
+      (reinterpret_cast<uintptr_t>(rope->inv_freq) & 7u))
+    return PA_ERR_ALIGN;
+  DeviceState *d = nullptr;
+  if ((st = device_state(&d)) != PA_OK) return st;
+  RopeKvParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_weight = q_norm_weight;
+  p.k_weight = k_norm_weight;
+  p.inv_freq = rope->inv_freq;
+  p.positions = positions;
+  p.slots = slot_mapping;
+  p.q_out = q_out;
+  p.k_cache = pool->k_cache;
+  p.v_cache = pool->v_cache;
+  p.err = d->err;
+  p.num_slots = (int64_t)pool->num_blocks * kBlock;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = pool->num_kv_heads;
+  p.rotary_dim = rope->rotary_dim;
+  p.interleaved = rope->layout == PA_ROPE_INTERLEAVED;
+  p.attention_factor = rope->attention_factor;
+  p.eps = eps;
+  cudaError_t e = launch_rope_kv(p, pool->dtype, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+pa_status pa_kv_evict(const pa_kv_pool *pool, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                      const int32_t *context_lens, int32_t num_seqs, const float *weights, int32_t weights_stride,
+                      int32_t budget, int32_t recent, int32_t sinks, const int32_t *dst_block_tables,
+                      int32_t dst_max_blocks, float *weights_out, int32_t weights_out_stride, int32_t *kept,
+                      int32_t *new_context_lens, pa_stream_t stream) {
+  pa_status st = check_pool(pool);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0) return PA_ERR_SHAPE;
+  if (num_seqs == 0) return PA_OK;
+  if (!block_tables || !context_lens || !weights || !dst_block_tables || !weights_out || !kept || !new_context_lens)
+    return PA_ERR_NULL;
+  if (max_blocks_per_seq < 1 || dst_max_blocks < 1 || weights_stride < 1 || weights_out_stride < 1) return PA_ERR_SHAPE;
+  if (budget < 1 || recent < 0 || sinks < 0 || (int64_t)recent + sinks > budget) return PA_ERR_SHAPE;
+  // the other heads of a sequence still read its length when one head has finished
+  if (new_context_lens == context_lens) return PA_ERR_SHAPE;
+  // in place, or apart: rows of another stride would overlap other rows of the source
+  if (weights_out == weights && weights_out_stride != weights_stride) return PA_ERR_SHAPE;
+  if (dst_block_tables == block_tables && dst_max_blocks != max_blocks_per_seq) return PA_ERR_SHAPE;
+  if (num_seqs > 16384) return PA_ERR_UNSUPPORTED;
+  if (!aligned4(block_tables) || !aligned4(context_lens) || !aligned4(weights) || !aligned4(dst_block_tables) ||
+      !aligned4(weights_out) || !aligned4(kept) || !aligned4(new_context_lens))
+    return PA_ERR_ALIGN;
+  DeviceState *d = nullptr;
+  if ((st = device_state(&d)) != PA_OK) return st;
+  EvictParams p{};
+  p.weights = weights;
+  p.context_lens = context_lens;
+  p.block_tables = block_tables;
+  p.dst_block_tables = dst_block_tables;
+  p.k_cache = pool->k_cache;
+  p.v_cache = pool->v_cache;
+  p.kept = kept;
+  p.weights_out = weights_out;
+  p.new_lens = new_context_lens;
+  p.err = d->err;
+  p.weights_stride = weights_stride;
+  p.out_stride = weights_out_stride;
+  p.num_seqs = num_seqs;
+  p.num_kv_heads = pool->num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.dst_max_blocks = dst_max_blocks;
+  p.num_blocks = pool->num_blocks;
+  p.budget = budget;
+  p.recent = recent;
+  p.sinks = sinks;
+  cudaError_t e = launch_evict(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
 pa_status pa_kv_block_copy(const pa_kv_pool *pools, int32_t num_layers, const int32_t *pairs, int32_t num_pairs,
                            pa_stream_t stream) {
   if (num_layers < 0 || num_pairs < 0) return PA_ERR_SHAPE;

@@ -75,6 +75,56 @@ struct RopeWriteParams {
 };
 cudaError_t launch_rope_write(const RopeWriteParams &p, int dtype, cudaStream_t stream);
 
+// ---- rotary embedding (any layout, part of the head) and the KV write ----------------------
+struct RopeKvParams {
+  const void *q;             // [T][Hq][128]
+  const void *k;             // [T][Hkv][128]
+  const void *v;
+  const void *q_weight;      // [128], null: no RMSNorm
+  const void *k_weight;
+  const double *inv_freq;    // [rotary_dim / 2]
+  const int32_t *positions;  // [T]
+  const int64_t *slots;      // [T]
+  void *q_out;               // [T][Hq][128]
+  void *k_cache;
+  void *v_cache;
+  int *err;
+  int64_t num_slots;
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float attention_factor;
+  float eps;
+};
+cudaError_t launch_rope_kv(const RopeKvParams &p, int dtype, cudaStream_t stream);
+
+// ---- eviction by accumulated attention weight ------------------------------------------------
+struct EvictParams {
+  const float *weights;             // [S][Hkv][weights_stride]
+  const int32_t *context_lens;
+  const int32_t *block_tables;      // [S][max_blocks_per_seq]
+  const int32_t *dst_block_tables;  // [S][dst_max_blocks]
+  void *k_cache;
+  void *v_cache;
+  int32_t *kept;                    // [S][Hkv][budget]
+  float *weights_out;               // [S][Hkv][out_stride]
+  int32_t *new_lens;                // [S]
+  int *err;
+  int32_t weights_stride;
+  int32_t out_stride;
+  int32_t num_seqs;
+  int32_t num_kv_heads;
+  int32_t max_blocks_per_seq;
+  int32_t dst_max_blocks;
+  int32_t num_blocks;
+  int32_t budget;
+  int32_t recent;
+  int32_t sinks;
+};
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
+
 // ---- self-test of the bounded waits --------------------------------------------------------
 cudaError_t launch_bounded_wait_selftest(int *err, uint64_t limit_ns, cudaStream_t stream);
 
