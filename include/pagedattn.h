@@ -616,6 +616,34 @@ PA_API pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, c
                                   int32_t num_q_heads, void *q_out, const pa_kv_pool *pool, pa_stream_t stream);
 
 /*
+ * paged_attn_decode_weights — pa_paged_attn_decode that also accumulates the
+ * attention weight every cached token received (what pa_kv_evict decides by):
+ *   weights_out[s][h][j] = weights_in[s][h][j] + sum over the query heads g of
+ *                          KV head h of softmax_j(scale * q[s][g] . K_j)
+ * for j < context_lens[s]; entries from context_lens[s] on are not touched.
+ *   weights_in, weights_out  fp32 [num_seqs][num_kv_heads][weights_stride],
+ *                 weights_stride >= max_context_len; weights_in NULL: zeros;
+ *                 weights_out may be weights_in, else they must not overlap.
+ *   max_context_len  also the longest sequence that is computed: a longer one
+ *                 records PA_ERR_RANGE as one beyond its block table does.
+ *   workspace     at least pa_decode_weights_workspace_bytes(...) bytes, 16-byte
+ *                 aligned; its contents need no initialisation and are
+ *                 clobbered.  Calls sharing one must not overlap on the GPU.
+ * Scores, weights and sums are fp32.  A page with a block id outside the pool is
+ * reported and its tokens get no weight.  16-bit pools; num_seqs * num_kv_heads
+ * at most 65535 (else PA_ERR_UNSUPPORTED).  Other arguments and errors as
+ * pa_paged_attn_decode.
+ */
+PA_API size_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                                int32_t max_context_len);
+PA_API pa_status pa_paged_attn_decode_weights(const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
+                                              int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                              int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
+                                              float scale, const float *weights_in, float *weights_out,
+                                              int32_t weights_stride, void *out, void *workspace,
+                                              size_t workspace_bytes, pa_stream_t stream);
+
+/*
  * kv_evict — shorten each sequence's cache to at most `budget` tokens, for
  * every KV head by its own weights.  Of the ctx = context_lens[s] tokens of
  * sequence s, for KV head h:

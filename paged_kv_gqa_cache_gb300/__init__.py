@@ -19,6 +19,7 @@ Calls (see include/pagedattn.h for the full contract):
 * ``qk_norm_rope_kv_write``: q/k RMSNorm + rotary embedding fused into the KV write
 * ``rope_kv_write``: rotary embedding of any layout, width and frequencies (``rope_inv_freq``
   for the long-context scalings), with the KV write
+* ``paged_attn_decode_weights``: decode that accumulates the attention weight of every cached token
 * ``kv_evict``: a cache shortened to a budget by accumulated attention weight
 * ``kv_block_copy(pools, pairs)``: copy-on-write block copy over every layer
 * ``BlockAllocator`` / ``Sequence`` / ``build_step_tables``: the host-side block
@@ -53,6 +54,7 @@ EXPORTS = ("pa_kv_cache_write", "pa_decode_workspace_bytes", "pa_paged_attn_deco
            "pa_paged_attn_decode_ex", "pa_paged_attn_decode_q8_ex", "pa_prefill_workspace_bytes",
            "pa_paged_attn_prefill_chunk_ex", "pa_paged_attn_prefill_chunk_q8", "pa_mixed_step",
            "pa_mixed_step_workspace_bytes", "pa_rope_inv_freq", "pa_rope_kv_write", "pa_kv_evict",
+           "pa_decode_weights_workspace_bytes", "pa_paged_attn_decode_weights",
            "pa_sequence_unshare", "pa_sequence_truncate",
            "pa_allocator_create", "pa_allocator_destroy", "pa_allocator_allocate", "pa_allocator_retain",
            "pa_allocator_release", "pa_allocator_refcount", "pa_allocator_stats_get", "pa_allocator_take_copies",
@@ -165,6 +167,11 @@ def load_library(path: str = LIB_PATH):
         lib.pa_rope_kv_write.argtypes = [P, P, P, ctypes.POINTER(Rope), P, P, ctypes.c_float, P, P, i32, i32, P,
                                          pool_p, P]
         lib.pa_rope_kv_write.restype = i32
+        lib.pa_decode_weights_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        lib.pa_decode_weights_workspace_bytes.restype = ctypes.c_size_t
+        lib.pa_paged_attn_decode_weights.argtypes = [P, pool_p, P, i32, P, i32, i32, i32, ctypes.c_float, P, P, i32,
+                                                     P, P, ctypes.c_size_t, P]
+        lib.pa_paged_attn_decode_weights.restype = i32
         lib.pa_kv_evict.argtypes = [pool_p, P, i32, P, i32, P, i32, i32, i32, i32, P, i32, P, i32, P, P, P]
         lib.pa_kv_evict.restype = i32
         lib.pa_selftest_bounded_wait.argtypes = [ctypes.c_uint32, P]
@@ -817,6 +824,75 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
     if fresh:
         _hold(stream, q_out)
     return q_out
+
+
+def decode_weights_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, max_context_len: int) -> int:
+    return int(load_library().pa_decode_weights_workspace_bytes(num_seqs, num_q_heads, num_kv_heads,
+                                                                max_context_len))
+
+
+def alloc_decode_weights_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, max_context_len: int,
+                                   device=None) -> torch.Tensor:
+    n = decode_weights_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, max_context_len)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def _decode_args(q, pool, k_cache, block_tables, context_lens, max_context_len):
+    """The checks the decode calls share; (sequences, query heads, table width, length bound)."""
+    _need(q, "q", k_cache.dtype)
+    _need(block_tables, "block_tables", torch.int32)
+    _need(context_lens, "context_lens", torch.int32)
+    if q.dim() != 3 or q.shape[2] != pool.head_dim:
+        raise ValueError(f"q must be [S, Hq, {pool.head_dim}]")
+    S, hq, _ = q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("block_tables must be [S, max_blocks], context_lens [S]")
+    mb = block_tables.shape[1]
+    return S, hq, mb, int(max_context_len) if max_context_len is not None else mb * pool.block_size
+
+
+def paged_attn_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                              weights_in: Optional[torch.Tensor], weights_out: torch.Tensor,
+                              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                              max_context_len: Optional[int] = None, stream=None):
+    """Decode attention (as :func:`paged_attn_decode`) that also accumulates the
+    attention weight of every cached token over the query heads of its KV head:
+    ``weights_out = weights_in + weight`` (fp32 [S, Hkv, stride >= the length
+    bound]; the same tensor: in place; ``weights_in`` None: zeros).  Entries from
+    a sequence's length on are not touched.  ``max_context_len`` defaults to what
+    both the block tables and the weights hold.  Returns (out, weights_out)."""
+    pool = make_pool(k_cache, v_cache)
+    S, hq, mb, mcl = _decode_args(q, pool, k_cache, block_tables, context_lens, max_context_len)
+    _need(weights_out, "weights_out", torch.float32)
+    if max_context_len is None and weights_out.dim() == 3:
+        mcl = min(mcl, weights_out.shape[2])
+    if weights_out.dim() != 3 or weights_out.shape[:2] != (S, pool.num_kv_heads):
+        raise ValueError(f"weights_out must be [{S}, {pool.num_kv_heads}, stride]")
+    if weights_in is not None:
+        _need(weights_in, "weights_in", torch.float32)
+        if weights_in.shape != weights_out.shape:
+            raise ValueError("weights_in and weights_out must have one shape")
+    fresh = []
+    if out is None:
+        out = torch.empty_like(q)
+        fresh.append(out)
+    _need(out, "out", q.dtype)
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if workspace is None:
+        workspace = alloc_decode_weights_workspace(S, hq, pool.num_kv_heads, mcl, q.device)
+        fresh.append(workspace)
+    _need(workspace, "workspace")
+    _here(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
+          weights_in=weights_in, weights_out=weights_out, out=out, workspace=workspace)
+    _check(load_library().pa_paged_attn_decode_weights(
+        q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq, mcl,
+        float(scale), None if weights_in is None else weights_in.data_ptr(), weights_out.data_ptr(),
+        weights_out.shape[2], out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(stream)), "pa_paged_attn_decode_weights")
+    _hold(stream, *fresh)
+    return out, weights_out
 
 
 def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,

@@ -1,0 +1,191 @@
+// Paged GQA decode that also accumulates the attention weight every cached
+// token received, for sm_103a (the decode: decode_kernel.cuh).
+//
+//   out[s][g]           = softmax_j(scale q[s][g] . K_j) V_j
+//   weights_out[s][h][j] = weights_in[s][h][j] + sum over the G query heads g of
+//                          KV head h of their softmax weight of token j
+//
+// A weight needs its row's final maximum and sum, which exist only after the
+// last page.  Reading K again would cost half of the decode; instead the split
+// pass leaves each key's G scores (log2 domain, fp32: 4 G bytes next to the 512
+// of its K and V rows) in the workspace, and the pass that joins the fragments
+// turns them into weights: CTA (item, 0) joins the outputs, CTA (item, c > 0)
+// takes kChunkKeys keys, first joining the (m, l) of the item's fragments
+// itself (a few hundred bytes), so that no CTA waits for another.
+// HBM-bound: K and V once; the scores and weights stream at 8 G + 8 bytes a key.
+#include "decode_kernel.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kChunkKeys = 4096;
+constexpr int kWeightThreads = 256;
+static_assert(kWeightThreads / 32 >= 8, "a warp per query head of a KV head");
+
+template <typename T, int G>
+__global__ void __launch_bounds__(NW * 32, 1)
+decode_scores_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const DecodeParams p, float *scores, int max_len) {
+  using Sm = SplitSmem<false, G, NW>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ int warp_tot[NW];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t *prefix = reinterpret_cast<int32_t *>(smem + Sm::kPrefixOff);
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  FormArgs fa;
+  fa.scores = scores;
+  fa.max_len = max_len;
+  griddep_wait();
+  scan_pages_n<NW * 32, kFormScores>(p, prefix, warp_tot, blockIdx.x == 0, fa);
+  const int64_t P = (int64_t)prefix[p.num_seqs] * p.num_kv_heads;
+  const int64_t W = P < p.num_workers ? P : p.num_workers;
+  const int w = blockIdx.x * NW + warp;
+  if (w >= W) {
+    if (blockIdx.x == 0 && warp == 0)  // only when no warp has pages (W = 0)
+      for (int i = lane; i <= p.num_seqs; i += 32) p.meta[i] = prefix[i];
+  } else {
+    decode_split_worker<T, G, false, false, NW, kFormScores>(kmap, vmap, p, smem, prefix, warp, w, P, W, fa);
+  }
+  griddep_launch_dependents();
+}
+
+template <typename T, int G>
+__global__ void __launch_bounds__(kWeightThreads)
+decode_weights_kernel(const DecodeParams p, const float *scores, const float *weights_in, float *weights_out,
+                      int64_t weights_stride) {
+  __shared__ float s_m[G], s_inv[G];
+  griddep_wait();
+  const int item = blockIdx.y, hkv = p.num_kv_heads;
+  const int s = item / hkv, h = item % hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t first = __ldg(p.meta + s), pages = __ldg(p.meta + s + 1) - first;
+  if (pages == 0) return;  // a bad length: reported, nothing written
+  const int64_t P = (int64_t)__ldg(p.meta + p.num_seqs) * hkv;
+  const int64_t W = P < p.num_workers ? P : p.num_workers;
+  const int64_t A = (int64_t)hkv * first + (int64_t)h * pages;
+  const int wf = worker_of(A, P, W), nf = worker_of(A + pages - 1, P, W) - wf + 1;
+  if (blockIdx.x == 0) {
+    if (warp < G) merge_fragments<T, G, 32>(p, s, h, warp, wf, nf, lane);
+    return;
+  }
+  const int ctx = __ldg(p.context_lens + s);
+  const int j0 = ((int)blockIdx.x - 1) * kChunkKeys;
+  if (j0 >= ctx) return;
+  if (warp < G) {  // head `warp`: the row's maximum and sum over its fragments
+    const int64_t slot0 = (int64_t)item + wf;
+    float m = -INFINITY, l = 0.f;
+    for (int f = lane; f < nf; f += 32) {
+      const float2 ml = *reinterpret_cast<const float2 *>(p.ws_ml + ((slot0 + f) * G + warp) * 2);
+      const float mn = fmaxf(m, ml.x);
+      if (mn > -INFINITY) l = l * exp2f(m - mn) + ml.y * exp2f(ml.x - mn);
+      m = mn;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const float m2 = __shfl_xor_sync(FULL, m, off), l2 = __shfl_xor_sync(FULL, l, off);
+      const float mn = fmaxf(m, m2);
+      if (mn > -INFINITY) l = l * exp2f(m - mn) + l2 * exp2f(m2 - mn);
+      m = mn;
+    }
+    if (lane == 0) {
+      s_m[warp] = m > -INFINITY ? m : 0.f;
+      s_inv[warp] = l == 0.f ? 0.f : 1.f / l;  // (no page could be read: no weight; a NaN stays one)
+    }
+  }
+  __syncthreads();
+  float m[G], inv[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    m[g] = s_m[g];
+    inv[g] = s_inv[g];
+  }
+  const float *sc = scores + A * (kBlock * G);
+  const int64_t row = (int64_t)item * weights_stride;
+  const int j1 = min(ctx, j0 + kChunkKeys);
+  constexpr int U = 4;  // keys per thread in flight
+  for (int j = j0 + (int)threadIdx.x; j < j1; j += kWeightThreads * U) {
+    float v[U][G], w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = j + u * kWeightThreads;
+      w[u] = 0.f;
+      if (k < j1) {
+        if (weights_in) w[u] = weights_in[row + k];
+        if constexpr (G == 1) {
+          v[u][0] = sc[k];
+        } else if constexpr (G == 2) {
+          const float2 x = *reinterpret_cast<const float2 *>(sc + (int64_t)k * G);
+          v[u][0] = x.x, v[u][1] = x.y;
+        } else {
+#pragma unroll
+          for (int g = 0; g < G; g += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(sc + (int64_t)k * G + g);
+            v[u][g] = x.x, v[u][g + 1] = x.y, v[u][g + 2] = x.z, v[u][g + 3] = x.w;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = j + u * kWeightThreads;
+      if (k < j1) {
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) sum = fmaf(exp2f(v[u][g] - m[g]), inv[g], sum);
+        weights_out[row + k] = w[u] + sum;
+      }
+    }
+  }
+}
+
+template <typename T, int G>
+cudaError_t launch_weights_typed(const DecodeParams &p0, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                 const DecodeWeightsParams &wp, cudaStream_t stream) {
+  DecodeParams p = p0;
+  const int smem = 1024 + NW * kStages * stage_stride<false>() + NW * kStages * 8 + NW * 16 * G * 8 +
+                   (p.num_seqs + 1) * 4;
+  static KernelSetup setup;
+  int per_sm = 0;
+  cudaError_t e = kernel_setup(setup, decode_scores_kernel<T, G>, smem, NW * 32, &per_sm);
+  if (e != cudaSuccess) return e;
+  int grid = sm_count() * per_sm;
+  const int64_t pages = (int64_t)p.num_seqs * p.num_kv_heads * ((wp.max_len + kBlock - 1) / kBlock);
+  const int64_t want = ((pages + 3) / 4 + NW - 1) / NW;  // at least 4 pages per warp
+  if (want < grid) grid = (int)want;
+  if (grid < 1) grid = 1;
+  if (grid * NW > kDecodeMaxWorkers) grid = kDecodeMaxWorkers / NW;
+  p.num_workers = grid * NW;
+  e = launch_pdl(decode_scores_kernel<T, G>, dim3(grid), dim3(NW * 32), smem, stream, kmap, vmap, p, wp.scores,
+                 wp.max_len);
+  if (e != cudaSuccess) return e;
+  const dim3 wgrid(1 + (wp.max_len + kChunkKeys - 1) / kChunkKeys, p.num_seqs * p.num_kv_heads);
+  return launch_pdl(decode_weights_kernel<T, G>, wgrid, dim3(kWeightThreads), 0, stream, p,
+                    (const float *)wp.scores, wp.weights_in, wp.weights_out, wp.weights_stride);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_weights(const DecodeParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap, int dtype,
+                                  int group, const DecodeWeightsParams &wp, cudaStream_t stream) {
+#define PA_WEIGHTS_CASE(T, G) \
+  if (group == G) return launch_weights_typed<T, G>(p, kmap, vmap, wp, stream);
+  if (dtype == PA_BF16) {
+    PA_WEIGHTS_CASE(__nv_bfloat16, 1)
+    PA_WEIGHTS_CASE(__nv_bfloat16, 2)
+    PA_WEIGHTS_CASE(__nv_bfloat16, 4)
+    PA_WEIGHTS_CASE(__nv_bfloat16, 8)
+  } else {
+    PA_WEIGHTS_CASE(__half, 1)
+    PA_WEIGHTS_CASE(__half, 2)
+    PA_WEIGHTS_CASE(__half, 4)
+    PA_WEIGHTS_CASE(__half, 8)
+  }
+#undef PA_WEIGHTS_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

@@ -828,6 +828,61 @@ pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, const pa
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
+size_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t max_context_len) {
+  if (num_seqs < 0 || num_kv_heads < 1 || num_q_heads < 1 || num_q_heads % num_kv_heads != 0 || max_context_len < 1)
+    return 0;
+  const size_t decode = (decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads) + 255) & ~(size_t)255;
+  const size_t pages = (size_t)num_seqs * (((size_t)max_context_len + kBlock - 1) / kBlock);
+  return decode + pages * kBlock * num_q_heads * sizeof(float);
+}
+
+pa_status pa_paged_attn_decode_weights(const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                                       int32_t num_q_heads, int32_t max_context_len, float scale,
+                                       const float *weights_in, float *weights_out, int32_t weights_stride, void *out,
+                                       void *workspace, size_t workspace_bytes, pa_stream_t stream) {
+  pa_status st = decode_check_args(q, pool, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                                   max_context_len, scale, out);
+  if (st != PA_OK || num_seqs == 0) return st;
+  if (!weights_out) return PA_ERR_NULL;
+  if (weights_stride < max_context_len) return PA_ERR_SHAPE;
+  if ((int64_t)num_seqs * pool->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;  // a launch's second dimension
+  if (!aligned4(weights_in) || !aligned4(weights_out)) return PA_ERR_ALIGN;
+  if (!workspace) return PA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return PA_ERR_ALIGN;
+  if (workspace_bytes < pa_decode_weights_workspace_bytes(num_seqs, num_q_heads, pool->num_kv_heads, max_context_len))
+    return PA_ERR_WORKSPACE;
+  DeviceState *d = nullptr;
+  if ((st = device_state(&d)) != PA_OK) return st;  // also readies the tensor-map encoder
+  CUtensorMap kmap, vmap;
+  if (!pool_map(&kmap, pool, pool->k_cache, true) || !pool_map(&vmap, pool, pool->v_cache, true)) return PA_ERR_CUDA;
+  DecodeParams p{};
+  if (!decode_workspace_carve(workspace, workspace_bytes, num_seqs, num_q_heads, pool->num_kv_heads, p))
+    return PA_ERR_WORKSPACE;
+  p.q = q;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.out = out;
+  p.err = d->err;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_kv_heads = pool->num_kv_heads;
+  p.num_q_heads = num_q_heads;
+  p.num_blocks = pool->num_blocks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  DecodeWeightsParams wp{};
+  const size_t decode = (decode_workspace_bytes(num_seqs, num_q_heads, pool->num_kv_heads) + 255) & ~(size_t)255;
+  wp.scores = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + decode);
+  wp.weights_in = weights_in;
+  wp.weights_out = weights_out;
+  wp.weights_stride = weights_stride;
+  wp.max_len = max_context_len;
+  cudaError_t e = launch_decode_weights(p, kmap, vmap, pool->dtype, num_q_heads / pool->num_kv_heads, wp,
+                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
 pa_status pa_kv_evict(const pa_kv_pool *pool, const int32_t *block_tables, int32_t max_blocks_per_seq,
                       const int32_t *context_lens, int32_t num_seqs, const float *weights, int32_t weights_stride,
                       int32_t budget, int32_t recent, int32_t sinks, const int32_t *dst_block_tables,

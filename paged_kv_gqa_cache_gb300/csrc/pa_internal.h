@@ -199,6 +199,17 @@ int decode_item_ctas(int items, int max_pages_per_item);
 bool decode_workspace_carve(void *ws, size_t bytes, int num_seqs, int num_q_heads, int num_kv_heads,
                             DecodeParams &p);
 
+// ---- decode that accumulates the attention weights (16-bit pools) -----------------
+struct DecodeWeightsParams {
+  float *scores;             // workspace: [pages of the call][16][G]
+  const float *weights_in;   // [S][Hkv][weights_stride], null: zeros
+  float *weights_out;        // may be weights_in
+  int64_t weights_stride;
+  int32_t max_len;           // the longest sequence that is computed
+};
+cudaError_t launch_decode_weights(const DecodeParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap, int dtype,
+                                  int group, const DecodeWeightsParams &wp, cudaStream_t stream);
+
 // ---- chunked prefill (tcgen05 tensor cores) -------------------------------------
 struct PrefillParams {
   const void *q;             // [rows][Hq][128]

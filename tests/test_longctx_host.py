@@ -70,6 +70,33 @@ def test_kv_evict_refusals(lib, kw, status):
     assert pa.STATUS[st] == status
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(S=0), "PA_OK"), (dict(S=-1), "PA_ERR_SHAPE"), (dict(w_out=0), "PA_ERR_NULL"), (dict(q=0), "PA_ERR_NULL"),
+    (dict(w_in=None, ws=0), "PA_ERR_WORKSPACE"), (dict(wsb=-1), "PA_ERR_WORKSPACE"), (dict(stride=255), "PA_ERR_SHAPE"),
+    (dict(mcl=257), "PA_ERR_SHAPE"), (dict(mcl=0), "PA_ERR_SHAPE"), (dict(hq=24), "PA_ERR_UNSUPPORTED"),
+    (dict(hq=12), "PA_ERR_SHAPE"), (dict(scale=0.0), "PA_ERR_SHAPE"), (dict(w_in=P + 2), "PA_ERR_ALIGN"),
+    (dict(w_out=P + 2), "PA_ERR_ALIGN"), (dict(ws=P + 8), "PA_ERR_ALIGN"), (dict(S=9000, wsb=1 << 40), "PA_ERR_UNSUPPORTED"),
+    (dict(pool=_pool(dtype=5)), "PA_ERR_DTYPE"),
+])
+def test_decode_weights_refusals(lib, kw, status):
+    S, mcl = kw.get("S", 4), kw.get("mcl", 256)
+    need = lib.pa_decode_weights_workspace_bytes(max(S, 1), kw.get("hq", 16), 8, max(mcl, 1))
+    wsb = kw.get("wsb", need)
+    st = lib.pa_paged_attn_decode_weights(kw.get("q", P), ctypes.byref(kw.get("pool", _pool())), P, 16, P, S,
+                                          kw.get("hq", 16), mcl, kw.get("scale", 0.1), kw.get("w_in", P),
+                                          kw.get("w_out", P), kw.get("stride", 256), P, kw.get("ws", P),
+                                          need - 1 if wsb == -1 else wsb, None)
+    assert pa.STATUS[st] == status
+
+
+def test_decode_weights_workspace_size(lib):
+    f = lib.pa_decode_weights_workspace_bytes
+    assert f(4, 16, 8, 256) >= lib.pa_decode_workspace_bytes(4, 16, 8, 256) + 4 * 256 * 16 * 4
+    assert f(4, 16, 8, 257) > f(4, 16, 8, 256)
+    assert f(70, 32, 4, 1 << 19) > 1 << 32  # 64-bit arithmetic
+    assert f(-1, 16, 8, 256) == 0 and f(4, 12, 8, 256) == 0 and f(4, 16, 8, 0) == 0
+
+
 # ---- rotary frequencies ----------------------------------------------------------------
 
 def _freqs(*a, **kw):
