@@ -73,65 +73,28 @@ struct Layout {
 // read (their table entries may already be freed).
 __device__ __forceinline__ int window_lo(int ctx, int window) { return window > 0 && ctx > window ? ctx - window : 0; }
 
-// The forms of the split worker: the plain decode; the decode that also leaves
-// every key's score in the workspace (all of its items become fragments); the
-// keys past a shared prefix (an item of a sequence with a prefix becomes a
-// fragment, to be joined with the prefix's).
-enum DecodeForm { kFormPlain = 0, kFormScores = 1, kFormSuffix = 2 };
-struct FormArgs {
-  float *scores = nullptr;              // kFormScores: [page of the global numbering][16 keys][G], log2 domain
-  int32_t max_len = INT32_MAX;          // kFormScores: the longest sequence the workspace and the weights hold
-  const int32_t *group_end = nullptr;   // kFormSuffix: sequences before the end of group g, ascending [num_groups]
-  const int32_t *group_len = nullptr;   //   its shared prefix in tokens, a multiple of 16 (0: none)
-  int32_t num_groups = 0;               //   sequences behind the last group share nothing
-};
-
-// Tokens that sequence s shares with its group.
-__device__ __forceinline__ int shared_len(const FormArgs &fa, int s) {
-  int lo = 0, hi = fa.num_groups;  // the first group that ends behind s
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (fa.group_end[mid] <= s) lo = mid + 1; else hi = mid;
-  }
-  return lo < fa.num_groups ? fa.group_len[lo] : 0;
-}
-
-// First key that a sequence's split pages cover.
-template <int FORM>
-__device__ __forceinline__ int first_key(const DecodeParams &p, const FormArgs &fa, int s, int ctx) {
-  if constexpr (FORM == kFormSuffix) return shared_len(fa, s);
-  return window_lo(ctx, p.window);
-}
-
 // Pages of sequence s that hold visible keys (from its window's first page).
-template <int FORM = kFormPlain>
-__device__ __forceinline__ int pages_of(const DecodeParams &p, int s, bool report, const FormArgs &fa = {}) {
+__device__ __forceinline__ int pages_of(const DecodeParams &p, int s, bool report) {
   const int ctx = __ldg(p.context_lens + s);
-  bool ok = ctx >= 1 && ctx <= p.max_blocks_per_seq * kBlock;
-  if constexpr (FORM == kFormScores) ok = ok && ctx <= fa.max_len;
-  int lo = 0;
-  if (ok) lo = first_key<FORM>(p, fa, s, ctx);
-  if constexpr (FORM == kFormSuffix) ok = ok && lo <= ctx;
-  if (!ok) {
+  if (ctx < 1 || ctx > p.max_blocks_per_seq * kBlock) {
     if (report) set_error(p.err, PA_ERR_RANGE, s);
     return 0;
   }
-  return (ctx + kBlock - 1) / kBlock - lo / kBlock;
+  return (ctx + kBlock - 1) / kBlock - window_lo(ctx, p.window) / kBlock;
 }
 
 // Exclusive prefix of pages over sequences into prefix[0..S]: all NT threads
 // of the CTA (warp_tot: NT / 32 ints of shared memory); bad lengths are
 // reported when `report`.
-template <int NT, int FORM = kFormPlain>
-__device__ void scan_pages_n(const DecodeParams &p, int32_t *prefix, int *warp_tot, bool report,
-                             const FormArgs &fa = {}) {
+template <int NT>
+__device__ void scan_pages_n(const DecodeParams &p, int32_t *prefix, int *warp_tot, bool report) {
   constexpr int NWT = NT / 32;
   const int n = p.num_seqs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (n + NT - 1) / NT;
   const int lo = min(n, tid * per), hi = min(n, lo + per);
   int sum = 0;
-  for (int s = lo; s < hi; ++s) sum += pages_of<FORM>(p, s, report, fa);
+  for (int s = lo; s < hi; ++s) sum += pages_of(p, s, report);
   int incl = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -149,7 +112,7 @@ __device__ void scan_pages_n(const DecodeParams &p, int32_t *prefix, int *warp_t
   int run = base + incl - sum;
   for (int s = lo; s < hi; ++s) {
     prefix[s] = run;
-    run += pages_of<FORM>(p, s, false, fa);
+    run += pages_of(p, s, false);
   }
   if (tid == 0) prefix[n] = total;
   __syncthreads();
@@ -294,13 +257,12 @@ __device__ __forceinline__ void append_row(uint8_t *stage, const DecodeParams &p
 // domain); (m, l, o) is the running state (m warp-uniform, l per lane, o for
 // the lane's 4 dims).  pbuf2 is the warp's [16 keys][G] scratch for the
 // probabilities.  With int8 codes a key's scale multiplies its dot product
-// once, and a value's scale multiplies its probability before the sum.  SCORES:
-// the scores also go to scores[16 keys][G] (-inf for a key that is not visible).
-template <typename T, int G, bool Q8, bool F8, bool SCORES = false>
+// once, and a value's scale multiplies its probability before the sum.
+template <typename T, int G, bool Q8, bool F8>
 __device__ __forceinline__ void decode_page(const uint8_t *kst, int nlo, int nv,
                                             const QReg<Q8 && !F8> (&q)[G][Layout<G>::DPL / 2], const float (&qsc)[G],
                                             float2 (&o)[G][2], float (&m)[G], float (&l)[G], float2 *pbuf2,
-                                            int lane, float *scores = nullptr) {
+                                            int lane) {
   using Ly = Layout<G>;
   constexpr int NQ = Ly::NQ, NT = Ly::NT, NP = Ly::NP, CPL = Ly::CPL;
   const int qd = lane % NQ;  // which dim slice of a key this lane scores
@@ -369,21 +331,6 @@ __device__ __forceinline__ void decode_page(const uint8_t *kst, int nlo, int nv,
         if constexpr (F8) a *= ksc;
       }
       sc[ps][gg] = (t >= nlo && t < nv) ? a : neg_inf;
-    }
-    if constexpr (SCORES) {  // the first lane of each key's NQ stores its G scores
-      if (qd == 0) {
-        float *dst = scores + t * G;
-        if constexpr (G == 1) {
-          dst[0] = sc[ps][0];
-        } else if constexpr (G == 2) {
-          *reinterpret_cast<float2 *>(dst) = make_float2(sc[ps][0], sc[ps][1]);
-        } else {
-#pragma unroll
-          for (int gg = 0; gg < G; gg += 4)
-            *reinterpret_cast<float4 *>(dst + gg) =
-                make_float4(sc[ps][gg], sc[ps][gg + 1], sc[ps][gg + 2], sc[ps][gg + 3]);
-        }
-      }
     }
   }
 
@@ -805,12 +752,10 @@ struct SplitSmem {
 // at smem.  Writes the outputs of the items it covers whole and the
 // fragments of the others (merged by the last fragment to arrive when the
 // workspace has counters).  w < W and W <= P, so the range is not empty.
-template <typename T, int G, bool Q8, bool F8, int NWC, int FORM = kFormPlain>
+template <typename T, int G, bool Q8, bool F8, int NWC>
 __device__ __forceinline__ void decode_split_worker(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                                     const DecodeParams &p, uint8_t *smem, const int32_t *prefix,
-                                                    int slot, int64_t w, int64_t P, int64_t W,
-                                                    const FormArgs &fa = {}) {
-  static_assert(FORM == kFormPlain || !Q8, "16-bit pools");
+                                                    int slot, int64_t w, int64_t P, int64_t W) {
   using Ly = Layout<G>;
   using Sm = SplitSmem<Q8, G, NWC>;
   constexpr int NQ = Ly::NQ, DPL = Ly::DPL;
@@ -840,12 +785,7 @@ __device__ __forceinline__ void decode_split_worker(const CUtensorMap &kmap, con
   auto issue_at = [&](int st, const Cursor &at) {
     const int base = at.page & ~31;
     if (at.s != win_s || base != win_base) {
-      if (at.s != win_s) {
-        if constexpr (FORM == kFormSuffix)
-          win_first = shared_len(fa, at.s) / kBlock;
-        else
-          win_first = p.window > 0 ? window_lo(__ldg(p.context_lens + at.s), p.window) / kBlock : 0;
-      }
+      if (at.s != win_s) win_first = p.window > 0 ? window_lo(__ldg(p.context_lens + at.s), p.window) / kBlock : 0;
       win_s = at.s;
       win_base = base;
       const int pg = base + lane;
@@ -941,9 +881,8 @@ __device__ __forceinline__ void decode_split_worker(const CUtensorMap &kmap, con
         }
       }
       ctx = __ldg(p.context_lens + cc.s);
-      const int lo = first_key<FORM>(p, fa, cc.s, ctx);
-      first = lo / kBlock;
-      lo_in_first = lo - first * kBlock;
+      first = window_lo(ctx, p.window) / kBlock;
+      lo_in_first = window_lo(ctx, p.window) - first * kBlock;
       whole = (cc.page == 0);
       open = true;
     }
@@ -957,8 +896,6 @@ __device__ __forceinline__ void decode_split_worker(const CUtensorMap &kmap, con
     }
 
     bool appended = false;
-    float *scores = nullptr;
-    if constexpr (FORM == kFormScores) scores = fa.scores + (x0 + g) * (kBlock * G);
     if (!((bad_mask >> st) & 1u)) {
       const int nv = min(kBlock, ctx - (first + cc.page) * kBlock);  // keys of the sequence in this page
       if constexpr (!Q8) {
@@ -971,10 +908,8 @@ __device__ __forceinline__ void decode_split_worker(const CUtensorMap &kmap, con
       if constexpr (Q8)
         decode_page_mma<G, F8>(stages + st * SST, cc.page == 0 ? lo_in_first : 0, nv, qa, qsc8, qbias8, st8, lane);
       else
-        decode_page<T, G, false, false, FORM == kFormScores>(stages + st * SST, cc.page == 0 ? lo_in_first : 0, nv,
-                                                             q, qsc, o, m, l, pbuf2, lane, scores);
-    } else if constexpr (FORM == kFormScores) {  // a page that could not be read has no weight
-      for (int i = lane; i < kBlock * G; i += 32) scores[i] = neg_inf;
+        decode_page<T, G, false, false>(stages + st * SST, cc.page == 0 ? lo_in_first : 0, nv, q, qsc, o, m, l,
+                                        pbuf2, lane);
     }
     __syncwarp();  // every lane is done with this stage and with pbuf
     if (appended) fence_proxy_async_smem();  // the generic writes precede the stage's next copy
@@ -984,9 +919,7 @@ __device__ __forceinline__ void decode_split_worker(const CUtensorMap &kmap, con
     const bool last_of_item = (cc.page == cc.pages - 1);
     if (last_of_item || g == npages - 1) {
       const int item = cc.s * hkv + cc.h;
-      bool final_out = whole && last_of_item;
-      if constexpr (FORM == kFormScores) final_out = false;
-      if constexpr (FORM == kFormSuffix) final_out = final_out && first == 0;  // nothing shared
+      const bool final_out = whole && last_of_item;
       if constexpr (Q8) {
         // lane (gl, tl) holds heads 2 tl and 2 tl + 1 at dims 16 gl .. 16 gl + 15; a head's (m, l) lives
         // in the quad of lanes 4 head .. 4 head + 3

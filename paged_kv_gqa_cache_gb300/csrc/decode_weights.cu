@@ -1,5 +1,5 @@
 // Paged GQA decode that also accumulates the attention weight every cached
-// token received, for sm_103a (the decode: decode_kernel.cuh).
+// token received, for sm_103a (the split worker: decode_mma.cuh).
 //
 //   out[s][g]           = softmax_j(scale q[s][g] . K_j) V_j
 //   weights_out[s][h][j] = weights_in[s][h][j] + sum over the G query heads g of
@@ -13,7 +13,7 @@
 // takes kChunkKeys keys, first joining the (m, l) of the item's fragments
 // itself (a few hundred bytes), so that no CTA waits for another.
 // HBM-bound: K and V once; the scores and weights stream at 8 G + 8 bytes a key.
-#include "decode_kernel.cuh"
+#include "decode_mma.cuh"
 
 namespace pa {
 namespace {
@@ -23,10 +23,10 @@ constexpr int kWeightThreads = 256;
 static_assert(kWeightThreads / 32 >= 8, "a warp per query head of a KV head");
 
 template <typename T, int G>
-__global__ void __launch_bounds__(NW * 32, 1)
+__global__ void __launch_bounds__(NW * 32, 2)
 decode_scores_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const DecodeParams p, float *scores, int max_len) {
-  using Sm = SplitSmem<false, G, NW>;
+  using Sm = SplitSmem16<NW>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ int warp_tot[NW];
@@ -40,16 +40,13 @@ decode_scores_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
   fa.scores = scores;
   fa.max_len = max_len;
   griddep_wait();
-  scan_pages_n<NW * 32, kFormScores>(p, prefix, warp_tot, blockIdx.x == 0, fa);
+  scan_form_pages<NW * 32, kFormScores>(p, fa, prefix, warp_tot, blockIdx.x == 0);
   const int64_t P = (int64_t)prefix[p.num_seqs] * p.num_kv_heads;
   const int64_t W = P < p.num_workers ? P : p.num_workers;
   const int w = blockIdx.x * NW + warp;
-  if (w >= W) {
-    if (blockIdx.x == 0 && warp == 0)  // only when no warp has pages (W = 0)
-      for (int i = lane; i <= p.num_seqs; i += 32) p.meta[i] = prefix[i];
-  } else {
-    decode_split_worker<T, G, false, false, NW, kFormScores>(kmap, vmap, p, smem, prefix, warp, w, P, W, fa);
-  }
+  if (blockIdx.x == 0 && warp == 0)  // for the pass that joins the fragments
+    for (int i = lane; i <= p.num_seqs; i += 32) p.meta[i] = prefix[i];
+  if (w < W) split_worker16<T, G, NW, kFormScores>(kmap, vmap, p, fa, smem, prefix, warp, w, P, W);
   griddep_launch_dependents();
 }
 
@@ -115,18 +112,9 @@ decode_weights_kernel(const DecodeParams p, const float *scores, const float *we
       w[u] = 0.f;
       if (k < j1) {
         if (weights_in) w[u] = weights_in[row + k];
-        if constexpr (G == 1) {
-          v[u][0] = sc[k];
-        } else if constexpr (G == 2) {
-          const float2 x = *reinterpret_cast<const float2 *>(sc + (int64_t)k * G);
-          v[u][0] = x.x, v[u][1] = x.y;
-        } else {
+        const float *page = sc + (int64_t)(k >> 4) * (kBlock * G) + (k & 15);
 #pragma unroll
-          for (int g = 0; g < G; g += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(sc + (int64_t)k * G + g);
-            v[u][g] = x.x, v[u][g + 1] = x.y, v[u][g + 2] = x.z, v[u][g + 3] = x.w;
-          }
-        }
+        for (int g = 0; g < G; ++g) v[u][g] = page[g * kBlock];
       }
     }
 #pragma unroll
@@ -146,8 +134,7 @@ template <typename T, int G>
 cudaError_t launch_weights_typed(const DecodeParams &p0, const CUtensorMap &kmap, const CUtensorMap &vmap,
                                  const DecodeWeightsParams &wp, cudaStream_t stream) {
   DecodeParams p = p0;
-  const int smem = 1024 + NW * kStages * stage_stride<false>() + NW * kStages * 8 + NW * 16 * G * 8 +
-                   (p.num_seqs + 1) * 4;
+  const int smem = 1024 + SplitSmem16<NW>::kPrefixOff + (p.num_seqs + 1) * 4;
   static KernelSetup setup;
   int per_sm = 0;
   cudaError_t e = kernel_setup(setup, decode_scores_kernel<T, G>, smem, NW * 32, &per_sm);

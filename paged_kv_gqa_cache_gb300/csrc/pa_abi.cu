@@ -856,7 +856,7 @@ pa_status pa_paged_attn_decode_weights(const void *q, const pa_kv_pool *pool, co
   DeviceState *d = nullptr;
   if ((st = device_state(&d)) != PA_OK) return st;  // also readies the tensor-map encoder
   CUtensorMap kmap, vmap;
-  if (!pool_map(&kmap, pool, pool->k_cache, true) || !pool_map(&vmap, pool, pool->v_cache, true)) return PA_ERR_CUDA;
+  if (!pool_map_vpages(&kmap, pool, pool->k_cache) || !pool_map_vpages(&vmap, pool, pool->v_cache)) return PA_ERR_CUDA;
   DecodeParams p{};
   if (!decode_workspace_carve(workspace, workspace_bytes, num_seqs, num_q_heads, pool->num_kv_heads, p))
     return PA_ERR_WORKSPACE;
