@@ -616,6 +616,49 @@ PA_API pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, c
                                   int32_t num_q_heads, void *q_out, const pa_kv_pool *pool, pa_stream_t stream);
 
 /*
+ * paged_attn_decode_shared — pa_paged_attn_decode for sequences that share
+ * prefixes by groups (their first blocks adopted by reference,
+ * pa_sequence_adopt_prefix or pa_sequence_fork): each group's prefix is read
+ * once and computed for all of its sequences together.
+ *   group_sizes   int32 [num_groups]: group g is the next group_sizes[g]
+ *                 sequences of the batch (the groups in order from sequence 0);
+ *                 sequences behind the last group share nothing.
+ *   prefix_lens   int32 [num_groups]: the tokens that a group's sequences share,
+ *                 a multiple of 16 (0: none).  They are read through the block
+ *                 table of the group's first sequence; the other members' table
+ *                 entries for them are not read.
+ *   num_groups    at most PA_MAX_PREFIX_GROUPS (0: the two metadata pointers are not read).
+ *   context_lens  the whole lengths, shared tokens included, as for
+ *                 pa_paged_attn_decode; at least the group's prefix.
+ *   workspace     pa_decode_shared_workspace_bytes(...) bytes (for the current
+ *                 device: it depends on its SM count), 16-byte aligned; its
+ *                 contents need no initialisation and are clobbered.  Calls
+ *                 sharing one must not overlap on the GPU.
+ * The query-key and probability-value products of the prefix run on the tensor
+ * cores with fp32 accumulation; the probabilities enter the second rounded to
+ * the pool dtype, as in pa_paged_attn_prefill_chunk, or, where a group has at
+ * most 128 query rows per KV head, in two terms.  A negative group size, a
+ * group past num_seqs, and a prefix length that is negative, not a multiple of
+ * 16 or beyond the block table record PA_ERR_RANGE (detail: the group); such a
+ * group shares nothing and its sequences are computed from their own tables.  A
+ * sequence shorter than its group's prefix is treated as one with a bad length.
+ * A block id outside the pool is reported (detail: the sequence whose table
+ * holds it); the outputs that needed that page are undefined.  16-bit pools; at
+ * most 6000 sequences.  group_sizes and prefix_lens are read before the
+ * dependency wait, as block_tables are.  Other arguments and errors as
+ * pa_paged_attn_decode.
+ */
+#define PA_MAX_PREFIX_GROUPS 256
+PA_API size_t pa_decode_shared_workspace_bytes(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
+                                               int32_t num_kv_heads);
+PA_API pa_status pa_paged_attn_decode_shared(const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
+                                             int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                             int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
+                                             float scale, const int32_t *group_sizes, const int32_t *prefix_lens,
+                                             int32_t num_groups, void *out, void *workspace, size_t workspace_bytes,
+                                             pa_stream_t stream);
+
+/*
  * paged_attn_decode_weights — pa_paged_attn_decode that also accumulates the
  * attention weight every cached token received (what pa_kv_evict decides by):
  *   weights_out[s][h][j] = weights_in[s][h][j] + sum over the query heads g of

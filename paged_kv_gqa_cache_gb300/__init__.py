@@ -19,6 +19,7 @@ Calls (see include/pagedattn.h for the full contract):
 * ``qk_norm_rope_kv_write``: q/k RMSNorm + rotary embedding fused into the KV write
 * ``rope_kv_write``: rotary embedding of any layout, width and frequencies (``rope_inv_freq``
   for the long-context scalings), with the KV write
+* ``paged_attn_decode_shared``: decode for sequences that share prefixes by groups, each computed once
 * ``paged_attn_decode_weights``: decode that accumulates the attention weight of every cached token
 * ``kv_evict``: a cache shortened to a budget by accumulated attention weight
 * ``kv_block_copy(pools, pairs)``: copy-on-write block copy over every layer
@@ -54,6 +55,7 @@ EXPORTS = ("pa_kv_cache_write", "pa_decode_workspace_bytes", "pa_paged_attn_deco
            "pa_paged_attn_decode_ex", "pa_paged_attn_decode_q8_ex", "pa_prefill_workspace_bytes",
            "pa_paged_attn_prefill_chunk_ex", "pa_paged_attn_prefill_chunk_q8", "pa_mixed_step",
            "pa_mixed_step_workspace_bytes", "pa_rope_inv_freq", "pa_rope_kv_write", "pa_kv_evict",
+           "pa_decode_shared_workspace_bytes", "pa_paged_attn_decode_shared",
            "pa_decode_weights_workspace_bytes", "pa_paged_attn_decode_weights",
            "pa_sequence_unshare", "pa_sequence_truncate",
            "pa_allocator_create", "pa_allocator_destroy", "pa_allocator_allocate", "pa_allocator_retain",
@@ -167,6 +169,11 @@ def load_library(path: str = LIB_PATH):
         lib.pa_rope_kv_write.argtypes = [P, P, P, ctypes.POINTER(Rope), P, P, ctypes.c_float, P, P, i32, i32, P,
                                          pool_p, P]
         lib.pa_rope_kv_write.restype = i32
+        lib.pa_decode_shared_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        lib.pa_decode_shared_workspace_bytes.restype = ctypes.c_size_t
+        lib.pa_paged_attn_decode_shared.argtypes = [P, pool_p, P, i32, P, i32, i32, i32, ctypes.c_float, P, P, i32,
+                                                    P, P, ctypes.c_size_t, P]
+        lib.pa_paged_attn_decode_shared.restype = i32
         lib.pa_decode_weights_workspace_bytes.argtypes = [i32, i32, i32, i32]
         lib.pa_decode_weights_workspace_bytes.restype = ctypes.c_size_t
         lib.pa_paged_attn_decode_weights.argtypes = [P, pool_p, P, i32, P, i32, i32, i32, ctypes.c_float, P, P, i32,
@@ -747,6 +754,7 @@ def qk_norm_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_n
 
 # ---- long contexts: rotary positions, eviction -------------------------------------------
 
+MAX_PREFIX_GROUPS = 256
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = range(5)
 
@@ -824,6 +832,53 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
     if fresh:
         _hold(stream, q_out)
     return q_out
+
+
+def decode_shared_workspace_bytes(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int) -> int:
+    return int(load_library().pa_decode_shared_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads))
+
+
+def alloc_decode_shared_workspace(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int,
+                                  device=None) -> torch.Tensor:
+    n = decode_shared_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                             block_tables: torch.Tensor, context_lens: torch.Tensor, group_sizes: torch.Tensor,
+                             prefix_lens: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None, max_context_len: Optional[int] = None,
+                             stream=None) -> torch.Tensor:
+    """Decode attention (as :func:`paged_attn_decode`) for sequences that share
+    prefixes: group g is the next ``group_sizes[g]`` sequences (int32 [groups]),
+    which share their first ``prefix_lens[g]`` tokens (int32 [groups], multiples
+    of 16), read once through the group's first block table."""
+    pool = make_pool(k_cache, v_cache)
+    S, hq, mb, mcl = _decode_args(q, pool, k_cache, block_tables, context_lens, max_context_len)
+    _need(group_sizes, "group_sizes", torch.int32)
+    _need(prefix_lens, "prefix_lens", torch.int32)
+    if group_sizes.dim() != 1 or prefix_lens.shape != group_sizes.shape:
+        raise ValueError("group_sizes and prefix_lens must both be [groups]")
+    n = group_sizes.shape[0]
+    fresh = []
+    if out is None:
+        out = torch.empty_like(q)
+        fresh.append(out)
+    _need(out, "out", q.dtype)
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if workspace is None:
+        workspace = alloc_decode_shared_workspace(S, n, hq, pool.num_kv_heads, q.device)
+        fresh.append(workspace)
+    _need(workspace, "workspace")
+    _here(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
+          group_sizes=group_sizes, prefix_lens=prefix_lens, out=out, workspace=workspace)
+    _check(load_library().pa_paged_attn_decode_shared(
+        q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq, mcl,
+        float(scale), group_sizes.data_ptr(), prefix_lens.data_ptr(), n, out.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "pa_paged_attn_decode_shared")
+    _hold(stream, *fresh)
+    return out
 
 
 def decode_weights_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, max_context_len: int) -> int:

@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedattn.so")
 
 SOURCES = ["pa_abi.cu", "kv_write.cu", "decode.cu", "prefill.cu", "prefill8.cu", "mixed.cu", "decode_noalloc.cu", "block_copy.cu",
-           "rope_write.cu", "rope_kv.cu", "decode_weights.cu", "evict.cu", "selftest.cu",
+           "rope_write.cu", "rope_kv.cu", "decode_weights.cu", "decode_shared.cu", "evict.cu", "selftest.cu",
            "allocator.cpp"]
 HEADERS = ["pa_device.cuh", "pa_internal.h", "tcgen05.cuh", "context_cache.h", "prefill_kernel.cuh", "decode_kernel.cuh", "decode_mma.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

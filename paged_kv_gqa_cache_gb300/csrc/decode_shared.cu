@@ -1,0 +1,776 @@
+// Paged GQA decode for sequences that share prefixes by groups, for sm_103a:
+// each group's prefix is read and multiplied once for all of its sequences.
+//
+//   out[s][g] = softmax_j(scale q[s][g] . K_j) V_j over the whole context of s,
+// the keys split in two: the shared prefix of the sequence's group and the rest.
+// For online softmax states (m, l, o) over disjoint key sets the join is
+//   m = max m_i,  l = sum l_i 2^(m_i - m),  o = sum o_i 2^(m_i - m),  out = o / l.
+//
+// Three kernels:
+//   prefix  The query rows of a group's sequences for one KV head (sequences x
+//           G rows) against the prefix is a matrix product: query tiles of 128
+//           rows, key tiles of 128 keys, on the tcgen05 tensor cores with the
+//           tile machinery of prefill_kernel.cuh (no causal mask).  One CTA per
+//           SM over an equal share of all (query tile, key tile) pairs; a
+//           piece of a query tile's keys leaves its state in the workspace.
+//           One query tile per KV head is bound by HBM (64 KB of K and V per
+//           0.78 us of tensor time, against 1.47 us of an SM's share of HBM),
+//           more by the tensor cores; then the key range is cut into blocks
+//           about as long as a CTA's share, the query tiles of a block next to
+//           each other in the order, so that the CTAs that need the same keys
+//           run at the same time and all but one of them read L2.
+//   suffix  The rest of each sequence by the split workers of decode_mma.cuh,
+//           two small CTAs per SM.  It does not read what the prefix kernel
+//           writes, so it starts as soon as SMs are free beside it (the prefix
+//           CTAs release their dependents once the work before them has ended)
+//           and waits for the prefix kernel only before it ends, so that the
+//           join, its dependent, runs after both.
+//   join    A warp per (sequence, KV head, part of the dims) adds up the pieces.
+#include "decode_mma.cuh"
+#include "prefill_kernel.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kGroups = kMaxPrefixGroups;
+constexpr int kPVStages = 2;
+constexpr int P_OFF_Q = 0;
+constexpr int P_OFF_K = 2 * kHalf;
+constexpr int P_OFF_V = P_OFF_K + kKStages * 2 * kHalf;
+constexpr int P_OFF_X = P_OFF_V + kPVStages * 2 * kHalf;  // (m, l) exchange [unit parity][half][128]
+constexpr int P_OFF_PLAN = P_OFF_X + 2 * 2 * 128 * 8;
+struct PBars {
+  uint64_t q_full, q_free;
+  uint64_t k_full[kKStages], s_full[kKStages];
+  uint64_t v_full[kPVStages], p_full[kPVStages], pv_done[kPVStages];
+  uint64_t x_full, o_free, drain;
+  uint32_t tmem_base;
+};
+static_assert(sizeof(PBars) <= 256, "barriers");
+
+// The groups and the order of the prefix work.  Group g: sequences end[g - 1]
+// .. end[g] - 1, len[g] shared tokens; its pairs start at pairs[g], its units
+// at units[g].  A unit is (KV head, key block, query tile); its key block has
+// at most `share` key tiles when the group has several query tiles, else all.
+struct SharedPlan {
+  int32_t num_groups, share, ctas, total;  // total: pairs of all groups; ctas: the CTAs that share them
+  int32_t end[kGroups], len[kGroups];
+  int32_t pairs[kGroups + 1], units[kGroups + 1];
+};
+constexpr int P_OFF_BAR = P_OFF_PLAN + ((int)sizeof(SharedPlan) + 127) / 128 * 128;
+constexpr int P_SMEM_BYTES = P_OFF_BAR + 256 + 1024;
+static_assert(P_SMEM_BYTES <= 232448, "shared memory");
+
+struct GroupShape {
+  int kt, mt, blocks, blen;  // key tiles, query tiles, key blocks per KV head, key tiles per block (the last: fewer)
+};
+template <int G>
+__device__ __forceinline__ GroupShape group_shape(int size, int len, int share) {
+  constexpr int TQ = 128 / G;
+  GroupShape s;
+  s.kt = (len + 127) / 128;
+  s.mt = (size + TQ - 1) / TQ;
+  s.blocks = s.mt > 1 && s.kt > 0 ? (s.kt + share - 1) / share : 1;
+  s.blen = (s.kt + s.blocks - 1) / s.blocks;  // <= share, and every block has a key tile
+  return s;
+}
+
+// Sum of `mine` over the threads before this one and, in carry, over all (NT
+// threads, all of them take part).
+template <int NT>
+__device__ __forceinline__ int scan_step(int mine, int &carry, int *warp_tot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(FULL, incl, off);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 31) warp_tot[warp] = incl;
+  __syncthreads();
+  int base = carry, total = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) {
+    base += i < warp ? warp_tot[i] : 0;
+    total += warp_tot[i];
+  }
+  carry += total;
+  __syncthreads();
+  return base + incl - mine;
+}
+
+// Every group's end and shared length, as all kernels of the call understand
+// them.  A group with a bad size counts as empty; one with a bad length, with
+// a single sequence or that runs past the sequences shares nothing.  Reported if asked.
+template <int NT>
+__device__ void load_groups(const SharedParams &p, int32_t *end, int32_t *len, int *warp_tot, bool report) {
+  int carry = 0;
+  for (int g0 = 0; g0 < p.num_groups; g0 += NT) {
+    const int g = g0 + (int)threadIdx.x;
+    int size = 0, n = 0;
+    bool bad = false;
+    if (g < p.num_groups) {
+      size = __ldg(p.group_sizes + g);
+      n = __ldg(p.prefix_lens + g);
+      const bool bad_size = size < 0 || size > p.num_seqs;
+      const bool bad_len = n < 0 || n % kBlock != 0 || n > p.max_blocks_per_seq * kBlock;
+      bad = bad_size || bad_len;
+      if (bad_size) size = 0;
+      if (bad_len || size < 2) n = 0;
+    }
+    const int e = scan_step<NT>(size, carry, warp_tot) + size;
+    if (g < p.num_groups) {
+      const bool over = e > p.num_seqs;
+      if (report && (bad || (over && size > 0))) set_error(p.err, PA_ERR_RANGE, g);
+      end[g] = min(e, p.num_seqs);
+      len[g] = over ? 0 : n;
+    }
+  }
+  __syncthreads();
+}
+
+// The rest of the plan from the groups' ends and lengths in it.
+template <int G, int NT>
+__device__ void make_plan(SharedPlan &pl, int num_groups, int hkv, int grid, int *warp_tot) {
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {  // the pairs, then (with the share known) the units
+    int32_t *out = round ? pl.units : pl.pairs;
+    int carry = 0;
+    for (int g0 = 0; g0 < num_groups; g0 += NT) {
+      const int g = g0 + (int)threadIdx.x;
+      int mine = 0;
+      if (g < num_groups && pl.len[g] > 0) {
+        const GroupShape s = group_shape<G>(pl.end[g] - (g ? pl.end[g - 1] : 0), pl.len[g], round ? pl.share : 1);
+        mine = hkv * s.mt * (round ? s.blocks : s.kt);
+      }
+      const int before = scan_step<NT>(mine, carry, warp_tot);
+      if (g < num_groups) out[g] = before;
+    }
+    if (threadIdx.x == 0) {
+      out[num_groups] = carry;
+      if (!round) {
+        pl.num_groups = num_groups;
+        pl.total = carry;
+        pl.ctas = carry < grid ? carry : grid;  // so that no share is empty
+        pl.share = carry > 0 ? (carry + pl.ctas - 1) / pl.ctas : 1;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// CTA b's share of W pairs over n CTAs, [b W / n, (b + 1) W / n), and the CTA that owns pair y.
+__device__ __forceinline__ int share_start(int b, int W, int n) { return b >= n ? W : (int)((int64_t)b * W / n); }
+__device__ __forceinline__ int share_owner(int y, int W, int n) {
+  return (int)((((int64_t)y + 1) * n + W - 1) / W - 1);
+}
+
+// A run of pairs of one unit: key tiles ka .. kb - 1 of query tile mt.
+struct PUnit {
+  int g, h, mt, ka, kb, kt_last, unit, seq0, size, len;
+  bool two_terms;
+};
+template <int G>
+__device__ __forceinline__ PUnit punit_at(const SharedPlan &pl, int x, int x_end) {
+  int lo = 0, hi = pl.num_groups - 1;  // the last group with pairs[g] <= x: the one that holds x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pl.pairs[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  PUnit u;
+  u.g = lo;
+  u.seq0 = lo ? pl.end[lo - 1] : 0;
+  u.size = pl.end[lo] - u.seq0;
+  u.len = pl.len[lo];
+  const GroupShape s = group_shape<G>(u.size, u.len, pl.share);
+  int r = x - pl.pairs[lo];
+  u.h = r / (s.mt * s.kt);
+  r -= u.h * s.mt * s.kt;
+  const int j = r / (s.mt * s.blen);
+  r -= j * s.mt * s.blen;
+  const int bl = min(s.blen, s.kt - j * s.blen);
+  u.mt = r / bl;
+  r -= u.mt * bl;
+  u.ka = j * s.blen + r;
+  u.kb = u.ka + min(bl - r, x_end - x);
+  u.kt_last = s.kt - 1;
+  u.unit = pl.units[lo] + (u.h * s.blocks + j) * s.mt + u.mt;
+  u.two_terms = s.mt == 1;
+  return u;
+}
+
+// ---- the prefix kernel ----
+// The roles of prefill_kernel.cuh, each looping over the CTA's runs of pairs
+// with a key-tile counter c that runs on across them: warps 0..7 softmax and
+// epilogue (the halves of a key tile never meet in the loop), warps 8..14
+// load, warp 15 owns the tensor memory and issues the MMAs.  A run's Q is
+// loaded once the previous run's last Q K^T has completed (q_free); its first
+// P V product waits until the previous run's epilogue has read O (o_free).
+// P goes into P V rounded to the 16-bit type where a group has several query
+// tiles (tensor-bound), and in two terms where it has one (HBM-bound: the 8
+// more MMAs per key tile, 0.26 us, find the tensor core idle).
+template <typename T, int G>
+__global__ void __launch_bounds__(kThreads, 1)
+shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const __grid_constant__ CUtensorMap qmap, const SharedParams sp, const PrefillParams p) {
+  constexpr int TQ = 128 / G;
+  constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr uint32_t IDESC_S = tc::idesc_f16(kBF16, 128, 128, false);
+  constexpr uint32_t IDESC_O = tc::idesc_f16(kBF16, 128, 128, true);
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int warp_tot[kThreads / 32];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  PBars &bars = *reinterpret_cast<PBars *>(smem + P_OFF_BAR);
+  SharedPlan &pl = *reinterpret_cast<SharedPlan *>(smem + P_OFF_PLAN);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = (int)blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+    tma_prefetch_desc(&qmap);
+    mbar_init(&bars.q_full, 1);
+    mbar_init(&bars.q_free, 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&bars.k_full[i], kLoadWarps);
+      mbar_init(&bars.s_full[i], 1);
+    }
+    for (int i = 0; i < kPVStages; ++i) {
+      mbar_init(&bars.v_full[i], kLoadWarps);
+      mbar_init(&bars.p_full[i], kSoftmaxThreads);
+      mbar_init(&bars.pv_done[i], 1);
+    }
+    mbar_init(&bars.x_full, kSoftmaxThreads);
+    mbar_init(&bars.o_free, kSoftmaxThreads);
+    mbar_init(&bars.drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tc::tmem_alloc(&bars.tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  // The plan, from the group metadata alone (like block tables and lengths it is
+  // read before the dependency wait), the same in every CTA.
+  load_groups<kThreads>(sp, pl.end, pl.len, warp_tot, b == 0);
+  make_plan<G, kThreads>(pl, sp.num_groups, sp.num_kv_heads, (int)gridDim.x, warp_tot);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bars.tmem_base;
+  const int x0 = share_start(b, pl.total, pl.ctas), x1 = share_start(b + 1, pl.total, pl.ctas);
+  bool timed_out = false;
+
+  if (warp < kSoftmaxWarps) {
+    regs_inc<kRegsSoftmax>();
+    regs_taken();
+    // ---------------- softmax + epilogue (warps 0..7), run after run ----------------
+    const int quad = warp & 3, ch = warp >> 2;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+    const uint32_t o_self = tmem + lane_base + kColO + ch * 128;
+    const float sl2 = p.scale_log2;
+    int c = 0, ui = 0;
+    for (int x = x0; x < x1 && !timed_out; ++ui) {
+      const PUnit U = punit_at<G>(pl, x, x1);
+      x += U.kb - U.ka;
+      const int span = U.len - 1;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int kt = U.ka; kt < U.kb; ++kt, ++c) {
+        const int sb = c & 1, ks = c % kKStages, vs = c % kPVStages;
+        if (!mbar_wait(&bars.s_full[ks], (c / kKStages) & 1)) {
+          timed_out = true;
+          break;
+        }
+        tc::fence_after_sync();
+        const uint32_t s_addr = tmem + lane_base + sb * 128 + ch * 64;
+        const int kb = kt * 128 + ch * 64;  // first key of this half
+        uint32_t v[2][32];
+        tc::ld_32x32b_x32(s_addr, v[0]);
+        tc::ld_32x32b_x32(s_addr + 32, v[1]);
+        tc::wait_ld();
+        const bool full = kb + 63 <= span;  // (the same in every thread of the half)
+        const bool first = m_ref == -INFINITY;  // nothing accumulated for this row yet
+        const bool common = !U.two_terms && __all_sync(FULL, full && !first);
+        float mx = -INFINITY, ls = 0.f;
+        if (common) ls = exp_pack_store<T, false>(v, s_addr, sl2, m_ref, true, kb, span);
+        if (!common || ls > kRescaleSum) {
+          if (full) {
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                float &a = m4[cc * 2 + ((j >> 2) & 1)];
+                a = fmax3(a, __uint_as_float(v[cc][j]), __uint_as_float(v[cc][j + 1]));
+                a = fmax3(a, __uint_as_float(v[cc][j + 2]), __uint_as_float(v[cc][j + 3]));
+              }
+            mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+          } else {
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (kb + cc * 32 + j <= span) mx = fmaxf(mx, __uint_as_float(v[cc][j]));
+          }
+        }
+        const float mc = mx * sl2;
+        const bool need = !first && mc > m_ref + kRescale;
+        const bool redo = __any_sync(FULL, need);
+        if (redo) {  // warp-uniform; key tile c - 1 belongs to this run (first is false)
+          if (common) tc::wait_st();
+          const float f = need ? ex2(m_ref - mc) : 1.f;
+          if (need) {
+            l *= f;
+            m_ref = mc;
+          }
+          if (!mbar_wait(&bars.pv_done[(c - 1) % kPVStages], ((c - 1) / kPVStages) & 1)) {
+            timed_out = true;
+            break;
+          }
+          tc::fence_after_sync();
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t ov[32];
+            tc::ld_32x32b_x32(o_self + cc * 32, ov);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
+            tc::st_32x32b_x32(o_self + cc * 32, ov);
+          }
+        }
+        if (first) m_ref = mc;
+        if (!common || redo)
+          ls = U.two_terms ? exp_pack_store<T, true>(v, s_addr, sl2, m_ref, full, kb, span)
+                           : exp_pack_store<T, false>(v, s_addr, sl2, m_ref, full, kb, span);
+        l += ls;
+        tc::wait_st();
+        if (!mbar_wait(&bars.v_full[vs], (c / kPVStages) & 1)) {
+          timed_out = true;
+          break;
+        }
+        if (kt == U.kt_last) {  // value rows past the prefix, this half only
+          const int z0 = max(U.len - kt * 128, ch * 64), z1 = ch * 64 + 64;
+          uint8_t *vbase = smem + P_OFF_V + vs * 2 * kHalf;
+          for (int idx = (warp & 3) * 32 + lane; idx < (z1 - z0) * 16; idx += kSoftmaxThreads / 2) {
+            const int row = z0 + (idx >> 4), part = idx & 15;
+            *reinterpret_cast<uint4 *>(vbase + (row >> 4) * kVPage + (part >> 3) * (kVPage / 2) + (row & 15) * 128 +
+                                       (part & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc::fence_before_sync();
+        mbar_arrive(&bars.p_full[vs]);
+      }
+      if (timed_out) break;
+
+      // ---- the run's state into the workspace ----
+      const int cl = c - 1;
+      bool ok = mbar_wait(&bars.pv_done[cl % kPVStages], (cl / kPVStages) & 1);
+      tc::fence_after_sync();
+      float2 *xm = reinterpret_cast<float2 *>(smem + P_OFF_X) + (ui & 1) * 256;
+      if (ok) {
+        xm[ch * 128 + r] = make_float2(m_ref, l);
+        mbar_arrive(&bars.x_full);
+        ok = mbar_wait(&bars.x_full, ui & 1);
+      }
+      if (!__all_sync(FULL, ok)) {  // warp-uniform before the warp-wide loads
+        timed_out = true;
+        break;
+      }
+      const float2 other = xm[(1 - ch) * 128 + r];
+      const float m0 = ch == 0 ? m_ref : other.x, l0 = ch == 0 ? l : other.y;
+      const float m1 = ch == 0 ? other.x : m_ref, l1 = ch == 0 ? other.y : l;
+      const float M = fmaxf(m0, m1);
+      const float f0 = (m0 == -INFINITY) ? 0.f : ex2(m0 - M);
+      const float f1 = (m1 == -INFINITY) ? 0.f : ex2(m1 - M);
+      // this thread's 64 dims of the row, both key halves, out of tensor memory; then O is free
+      const uint32_t o0 = tmem + lane_base + kColO + ch * 64, o1 = o0 + 128;
+      uint32_t a[64], bq[64];
+      tc::ld_32x32b_x32(o0, *reinterpret_cast<uint32_t(*)[32]>(a));
+      tc::ld_32x32b_x32(o0 + 32, *reinterpret_cast<uint32_t(*)[32]>(a + 32));
+      tc::ld_32x32b_x32(o1, *reinterpret_cast<uint32_t(*)[32]>(bq));
+      tc::ld_32x32b_x32(o1 + 32, *reinterpret_cast<uint32_t(*)[32]>(bq + 32));
+      tc::wait_ld();
+      tc::fence_before_sync();
+      mbar_arrive(&bars.o_free);
+      if (U.mt * TQ + r / G < U.size) {  // rows past the group's last sequence hold nothing
+        const int64_t slot = U.unit + b;
+        float4 *dst = reinterpret_cast<float4 *>(sp.ws_o) + (slot * 32 + ch * 16) * 128 + r;  // [dims / 4][row]
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[e] = __uint_as_float(a[4 * i + e]) * f0 + __uint_as_float(bq[4 * i + e]) * f1;
+          dst[i * 128] = make_float4(y[0], y[1], y[2], y[3]);
+        }
+        if (ch == 0) sp.ws_ml[slot * 128 + r] = make_float2(M, l0 * f0 + l1 * f1);
+      }
+    }
+    regs_dec<128>();
+  } else {
+    // every loader and MMA warp runs this one decrease (setmaxnreg acts on whole warpgroups)
+    regs_dec<kRegsOther>();
+    if (warp != kWarpMma) {
+      // ---------------- loader warps ----------------
+      const int lw = warp - kWarpLoad0;
+      griddep_wait();  // Q, K and V may come from the kernels before
+      // The suffix kernel may start: the work before this kernel has ended, and
+      // it reads nothing that this kernel writes.
+      griddep_launch_dependents();
+      if (b == 0)  // the join's copy of the plan (after the wait: the previous call's join may still read it)
+        for (int i = lw * 32 + lane; i < (int)(sizeof(SharedPlan) / 4); i += kLoadWarps * 32)
+          reinterpret_cast<int32_t *>(sp.plan)[i] = reinterpret_cast<const int32_t *>(&pl)[i];
+      const int kb0 = lw, vb0 = (lw + 5) % kLoadWarps;
+      int c = 0, ui = 0, k_issued = 0, v_issued = 0;
+      for (int x = x0; x < x1 && !timed_out; ++ui) {
+        const PUnit U = punit_at<G>(pl, x, x1);
+        x += U.kb - U.ka;
+        const int32_t *bt = p.block_tables + (int64_t)U.seq0 * p.max_blocks_per_seq;  // the group's first sequence
+        const int npages = U.len / kBlock;
+        if (lw == 0 && lane == 0) {
+          if (ui > 0 && !mbar_wait(&bars.q_free, (ui - 1) & 1)) timed_out = true;
+          // (rows past the group belong to other sequences or read as zeros; nothing is stored for them)
+          mbar_arrive_expect_tx(&bars.q_full, 2 * kHalf);
+          tma_load_3d(smem + P_OFF_Q, &qmap, &bars.q_full, 0, U.h * G, U.seq0 + U.mt * TQ);
+          tma_load_3d(smem + P_OFF_Q + kHalf, &qmap, &bars.q_full, 64, U.h * G, U.seq0 + U.mt * TQ);
+        }
+        timed_out = __any_sync(FULL, timed_out);
+        for (int t = U.ka; t < U.kb && !timed_out; ++t, ++c) {
+          const int ks = c % kKStages, vs = c % kPVStages;
+          if (c >= kKStages && !mbar_wait(&bars.s_full[ks], ((c - kKStages) / kKStages) & 1)) {
+            timed_out = true;
+            break;
+          }
+          load_boxes(smem + P_OFF_K + ks * 2 * kHalf, &kmap, &bars.k_full[ks], t, kb0, U.h, 0, npages, nullptr, bt, p,
+                     U.seq0, lane);
+          k_issued = c + 1;
+          if (c >= kPVStages && !mbar_wait(&bars.pv_done[vs], ((c - kPVStages) / kPVStages) & 1)) {
+            timed_out = true;
+            break;
+          }
+          load_vpages(smem + P_OFF_V + vs * 2 * kHalf, &vmap, &bars.v_full[vs], t, vb0, U.h, 0, npages, nullptr, bt, p,
+                      U.seq0, lane);
+          v_issued = c + 1;
+        }
+        timed_out = __any_sync(FULL, timed_out);
+      }
+      if (timed_out) {  // a short, bounded chance for this warp's copies in flight to land
+        if (lw == 0 && ui > 0) mbar_wait(&bars.q_full, (ui - 1) & 1, kWaitLimitNs / 8);
+        for (int t = k_issued - kKStages > 0 ? k_issued - kKStages : 0; t < k_issued; ++t)
+          mbar_wait(&bars.k_full[t % kKStages], (t / kKStages) & 1, kWaitLimitNs / 8);
+        for (int t = v_issued - kPVStages > 0 ? v_issued - kPVStages : 0; t < v_issued; ++t)
+          mbar_wait(&bars.v_full[t % kPVStages], (t / kPVStages) & 1, kWaitLimitNs / 8);
+      }
+    } else {
+      // ---------------- MMA issuer (warp-uniform loop, one elected lane issues) ----------------
+      const bool leader = elect_one();
+      auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, mbar_wait(bar, parity)) != 0; };
+      const uint64_t qdesc = tc::desc_sw128(smem_u32(smem + P_OFF_Q), 16, 1024);
+      const uint64_t kdesc0 = tc::desc_sw128(smem_u32(smem + P_OFF_K), 16, 1024);
+      const uint64_t vdesc0 = tc::desc_sw128(smem_u32(smem + P_OFF_V), kVPage / 2, 1024);
+      constexpr uint64_t kStageStep = (2 * kHalf) >> 4;
+      constexpr uint64_t kHalfStep = kHalf >> 4;
+      // the P V product of key tile pc (pending), issued once P is ready
+      int pc = -1, p_run = 0;
+      bool p_first = false, p_two = false;
+      auto issue_pv = [&]() -> bool {
+        const int jv = pc % kPVStages;
+        if (!wait_all(&bars.p_full[jv], (pc / kPVStages) & 1)) return false;
+        if (p_first && p_run > 0 && !wait_all(&bars.o_free, (p_run - 1) & 1)) return false;
+        tc::fence_after_sync();
+        const uint64_t vdesc = vdesc0 + (uint64_t)jv * kStageStep;
+        const uint32_t p_col = tmem + (pc & 1) * 128;
+        const uint32_t acc0 = p_first ? 0u : 1u;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t o_col = tmem + kColO + (kk >> 2) * 128;
+            const uint32_t a_hi = p_col + 32 * (kk >> 1) + 8 * (kk & 1);
+            const uint64_t bdesc = vdesc + (uint64_t)(kk * (kVPage >> 4));
+            tc::mma_f16_ts(o_col, a_hi, bdesc, IDESC_O, (kk & 3) > 0 ? 1u : acc0);
+            if (p_two) tc::mma_f16_ts(o_col, a_hi + 16, bdesc, IDESC_O, 1u);
+          }
+          tc::commit(&bars.pv_done[jv]);
+        }
+        __syncwarp();
+        return true;
+      };
+      int c = 0, ui = 0;
+      for (int x = x0; x < x1 && !timed_out; ++ui) {
+        const PUnit U = punit_at<G>(pl, x, x1);
+        x += U.kb - U.ka;
+        // the previous run's last P V first: its epilogue need not wait for this run's Q and first K
+        if (pc >= 0) {
+          if (!issue_pv()) {
+            timed_out = true;
+            break;
+          }
+          pc = -1;
+        }
+        if (!wait_all(&bars.q_full, ui & 1)) {
+          timed_out = true;
+          break;
+        }
+        for (int kt = U.ka; kt < U.kb; ++kt, ++c) {
+          const int ks = c % kKStages;
+          if (!wait_all(&bars.k_full[ks], (c / kKStages) & 1)) {
+            timed_out = true;
+            break;
+          }
+          tc::fence_after_sync();
+          const uint64_t kdesc = kdesc0 + (uint64_t)ks * kStageStep;
+          const uint32_t s_col = tmem + (c & 1) * 128;
+          if (leader) {
+            tc::mma_f16(s_col, qdesc, kdesc, IDESC_S, 0u);
+#pragma unroll
+            for (int kk = 1; kk < 8; ++kk) {
+              const uint64_t off = (uint64_t)((kk >> 2) * kHalfStep + (kk & 3) * 2);
+              tc::mma_f16(s_col, qdesc + off, kdesc + off, IDESC_S, 1u);
+            }
+            tc::commit(&bars.s_full[ks]);
+            if (kt == U.kb - 1) tc::commit(&bars.q_free);  // the run's Q is no longer read
+          }
+          __syncwarp();
+          if (pc >= 0 && !issue_pv()) {
+            timed_out = true;
+            break;
+          }
+          pc = c;
+          p_run = ui;
+          p_first = kt == U.ka;
+          p_two = U.two_terms;
+        }
+      }
+      if (!timed_out && pc >= 0 && !issue_pv()) timed_out = true;
+      if (timed_out) {  // every MMA issued so far, bounded, before the tensor memory is freed
+        if (leader) tc::commit(&bars.drain);
+        __syncwarp();
+        mbar_wait(&bars.drain, 0, kWaitLimitNs / 8);
+      }
+    }
+    regs_wait_taken();  // (the softmax warps hold their registers by now)
+    regs_inc<128>();
+  }
+  if (timed_out) set_error(p.err, PA_ERR_TIMEOUT, b);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---- the suffix kernel ----
+template <typename T, int G>
+__global__ void __launch_bounds__(NW * 32, 2)
+shared_suffix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const SharedParams sp, const DecodeParams p) {
+  using Sm = SplitSmem16<NW>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ int warp_tot[NW];
+  __shared__ int32_t g_end[kGroups], g_len[kGroups];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t *prefix = reinterpret_cast<int32_t *>(smem + Sm::kPrefixOff);
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  load_groups<NW * 32>(sp, g_end, g_len, warp_tot, false);
+  FormArgs fa;
+  fa.group_end = g_end;
+  fa.group_len = g_len;
+  fa.num_groups = sp.num_groups;
+  scan_form_pages<NW * 32, kFormSuffix>(p, fa, prefix, warp_tot, blockIdx.x == 0);
+  const int64_t P = (int64_t)prefix[p.num_seqs] * p.num_kv_heads;
+  const int64_t W = P < p.num_workers ? P : p.num_workers;
+  const int w = blockIdx.x * NW + warp;
+  // Every prefix CTA has seen the work before it end, or this kernel would not
+  // run: q, the pool and the workspace are ready.
+  if (blockIdx.x == 0 && warp == 0)
+    for (int i = lane; i <= p.num_seqs; i += 32) p.meta[i] = prefix[i];
+  if (w < W) split_worker16<T, G, NW, kFormSuffix>(kmap, vmap, p, fa, smem, prefix, warp, w, P, W);
+  griddep_wait();  // this kernel's end then implies the prefix kernel's: the join needs both
+}
+
+// ---- the join ----
+// Warp (s, h, part): lane (gg, quad) adds up head gg's dims 4 quad .. 4 quad +
+// 3 over the pieces of the prefix and of the suffix.
+template <typename T, int G>
+__global__ void __launch_bounds__(128)
+shared_join_kernel(const SharedParams sp, const DecodeParams p) {
+  constexpr int TQ = 128 / G, QW = 32 / G;  // dim quads per warp
+  __shared__ SharedPlan pl;
+  griddep_wait();
+  for (int i = threadIdx.x; i < (int)(sizeof(SharedPlan) / 4); i += 128)
+    reinterpret_cast<int32_t *>(&pl)[i] = __ldcg(reinterpret_cast<const int32_t *>(sp.plan) + i);
+  __syncthreads();
+  const int wid = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int hkv = p.num_kv_heads;
+  if (wid >= p.num_seqs * hkv * G) return;
+  const int part = wid % G, item = wid / G, s = item / hkv, h = item % hkv;
+  const int gg = lane % G, quad = part * QW + lane / G;
+  const int ctx = __ldg(p.context_lens + s);
+  // the group of s
+  int lo = 0, hi = pl.num_groups;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (pl.end[mid] <= s) lo = mid + 1; else hi = mid;
+  }
+  const int g = lo, len = g < pl.num_groups ? pl.len[g] : 0;
+  if (ctx < 1 || ctx > p.max_blocks_per_seq * kBlock || ctx < len) return;  // reported; its rows are left
+  // the suffix's pieces: slots item + wf ..
+  const int pages = __ldcg(p.meta + s + 1) - __ldcg(p.meta + s);
+  const int64_t P = (int64_t)__ldcg(p.meta + p.num_seqs) * hkv;
+  const int64_t W = P < p.num_workers ? P : p.num_workers;
+  const int64_t A = (int64_t)hkv * __ldcg(p.meta + s) + (int64_t)h * pages;
+  const int wf = pages ? worker_of(A, P, W) : 0;
+  const int nfs = pages ? worker_of(A + pages - 1, P, W) - wf + 1 : 0;
+  if (len == 0 && nfs <= 1) return;  // the suffix worker wrote the output
+  float M = -INFINITY, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int U = 4;  // pieces in flight
+  auto add = [&](const float2 (&ml)[U], const float4 (&o)[U]) {
+    float mx = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
+    if (mx == -INFINITY) return;
+    const float f = ex2(M - mx);
+    L *= f;
+    O.x *= f, O.y *= f, O.z *= f, O.w *= f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = ex2(ml[u].x - mx);
+      L = fmaf(ml[u].y, w, L);
+      O.x = fmaf(o[u].x, w, O.x);
+      O.y = fmaf(o[u].y, w, O.y);
+      O.z = fmaf(o[u].z, w, O.z);
+      O.w = fmaf(o[u].w, w, O.w);
+    }
+    M = mx;
+  };
+  for (int f0 = 0; f0 < nfs; f0 += U) {
+    float2 ml[U];
+    float4 o[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ml[u] = make_float2(-INFINITY, 0.f);
+      o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (f0 + u < nfs) {
+        const int64_t slot = ((int64_t)item + wf + f0 + u) * G + gg;
+        ml[u] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml + slot * 2));
+        o[u] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + slot * kHeadDim + 4 * quad));
+      }
+    }
+    add(ml, o);
+  }
+  if (len > 0) {
+    const int seq0 = g ? pl.end[g - 1] : 0;
+    const GroupShape sh = group_shape<G>(pl.end[g] - seq0, len, pl.share);
+    const int mt = (s - seq0) / TQ, row = ((s - seq0) % TQ) * G + gg;
+    for (int j = 0; j < sh.blocks; ++j) {
+      const int bl = min(sh.blen, sh.kt - j * sh.blen);
+      const int xa = pl.pairs[g] + (h * sh.kt + j * sh.blen) * sh.mt + mt * bl;  // the unit's first pair
+      const int unit = pl.units[g] + (h * sh.blocks + j) * sh.mt + mt;
+      const int ff = share_owner(xa, pl.total, pl.ctas), fl = share_owner(xa + bl - 1, pl.total, pl.ctas);
+      for (int f0 = ff; f0 <= fl; f0 += U) {
+        float2 ml[U];
+        float4 o[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          ml[u] = make_float2(-INFINITY, 0.f);
+          o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (f0 + u <= fl) {
+            const int64_t slot = unit + f0 + u;
+            ml[u] = __ldcg(sp.ws_ml + slot * 128 + row);
+            o[u] = __ldcg(reinterpret_cast<const float4 *>(sp.ws_o) + (slot * 32 + quad) * 128 + row);
+          }
+        }
+        add(ml, o);
+      }
+    }
+  }
+  const float inv = 1.f / L;
+  T *op = reinterpret_cast<T *>(p.out) + ((int64_t)s * p.num_q_heads + h * G + gg) * kHeadDim + 4 * quad;
+  uint2 pk;
+  pk.x = Pack<T>::from_f2(O.x * inv, O.y * inv);
+  pk.y = Pack<T>::from_f2(O.z * inv, O.w * inv);
+  *reinterpret_cast<uint2 *>(op) = pk;
+}
+
+template <typename T, int G>
+cudaError_t launch_shared_typed(const SharedParams &sp, const PrefillParams &pp, const DecodeParams &dp0,
+                                const CUtensorMap *maps, cudaStream_t stream) {
+  DecodeParams dp = dp0;
+  static KernelSetup prefix_setup, suffix_setup;
+  cudaError_t e = kernel_setup(prefix_setup, shared_prefix_kernel<T, G>, P_SMEM_BYTES, kThreads, nullptr);
+  if (e != cudaSuccess) return e;
+  const int smem = 1024 + SplitSmem16<NW>::kPrefixOff + (dp.num_seqs + 1) * 4;
+  int per_sm = 0;
+  e = kernel_setup(suffix_setup, shared_suffix_kernel<T, G>, smem, NW * 32, &per_sm);
+  if (e != cudaSuccess) return e;
+  int grid = sm_count() * per_sm;
+  if (grid * NW > kDecodeMaxWorkers) grid = kDecodeMaxWorkers / NW;
+  dp.num_workers = grid * NW;
+  e = launch_pdl(shared_prefix_kernel<T, G>, dim3(sm_count()), dim3(kThreads), P_SMEM_BYTES, stream, maps[0], maps[1],
+                 maps[2], sp, pp);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(shared_suffix_kernel<T, G>, dim3(grid), dim3(NW * 32), smem, stream, maps[3], maps[4], sp, dp);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(shared_join_kernel<T, G>, dim3((dp.num_seqs * dp.num_q_heads + 3) / 4), dim3(128), 0, stream, sp,
+                    dp);
+}
+
+}  // namespace
+
+namespace {
+struct SharedLayout {
+  size_t plan, decode, ml, o, total;
+};
+SharedLayout shared_layout(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int sms) {
+  const size_t group = num_q_heads / num_kv_heads;
+  // pieces: at most one per unit and one more per CTA; units: at most one per CTA and one per query tile
+  const size_t tiles = (size_t)num_kv_heads * (num_groups + (size_t)num_seqs * group / 128);
+  const size_t slots = 2 * (size_t)sms + tiles;
+  auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+  SharedLayout l;
+  l.plan = 0;
+  l.decode = up(sizeof(SharedPlan));
+  l.ml = l.decode + up(decode_workspace_counters_offset(num_seqs, num_q_heads, num_kv_heads));
+  l.o = l.ml + up(slots * 128 * sizeof(float2));
+  l.total = l.o + slots * 128 * kHeadDim * sizeof(float);
+  return l;
+}
+}  // namespace
+
+size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int sms) {
+  return shared_layout(num_seqs, num_groups, num_q_heads, num_kv_heads, sms).total;
+}
+
+cudaError_t launch_decode_shared(SharedParams sp, const PrefillParams &pp, DecodeParams dp, void *workspace,
+                                 const CUtensorMap *maps, int dtype, int group, cudaStream_t stream) {
+  const SharedLayout l = shared_layout(dp.num_seqs, sp.num_groups, dp.num_q_heads, dp.num_kv_heads, sm_count());
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  sp.plan = ws + l.plan;
+  sp.ws_ml = reinterpret_cast<float2 *>(ws + l.ml);
+  sp.ws_o = reinterpret_cast<float *>(ws + l.o);
+  decode_workspace_carve(ws + l.decode, SIZE_MAX, dp.num_seqs, dp.num_q_heads, dp.num_kv_heads, dp);
+#define PA_SHARED_CASE(T, G) \
+  if (group == G) return launch_shared_typed<T, G>(sp, pp, dp, maps, stream);
+  if (dtype == PA_BF16) {
+    PA_SHARED_CASE(__nv_bfloat16, 1)
+    PA_SHARED_CASE(__nv_bfloat16, 2)
+    PA_SHARED_CASE(__nv_bfloat16, 4)
+    PA_SHARED_CASE(__nv_bfloat16, 8)
+  } else {
+    PA_SHARED_CASE(__half, 1)
+    PA_SHARED_CASE(__half, 2)
+    PA_SHARED_CASE(__half, 4)
+    PA_SHARED_CASE(__half, 8)
+  }
+#undef PA_SHARED_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

@@ -828,6 +828,80 @@ pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, const pa
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
+namespace {
+constexpr int kSharedMaxSeqs = 6000;  // the suffix kernel's page prefix in shared memory
+}
+
+size_t pa_decode_shared_workspace_bytes(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
+                                        int32_t num_kv_heads) {
+  if (num_seqs < 0 || num_seqs > kSharedMaxSeqs || num_groups < 0 || num_groups > kMaxPrefixGroups ||
+      num_kv_heads < 1 || num_q_heads < 1 || num_q_heads % num_kv_heads != 0)
+    return 0;
+  const int sms = sm_count();
+  return shared_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads, sms > 0 ? sms : 1);
+}
+
+pa_status pa_paged_attn_decode_shared(const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                                      int32_t num_q_heads, int32_t max_context_len, float scale,
+                                      const int32_t *group_sizes, const int32_t *prefix_lens, int32_t num_groups,
+                                      void *out, void *workspace, size_t workspace_bytes, pa_stream_t stream) {
+  pa_status st = decode_check_args(q, pool, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                                   max_context_len, scale, out);
+  if (st != PA_OK) return st;
+  if (num_groups < 0) return PA_ERR_SHAPE;
+  if (num_seqs == 0) return PA_OK;
+  if (num_groups > 0 && (!group_sizes || !prefix_lens)) return PA_ERR_NULL;
+  if (num_groups > kMaxPrefixGroups || num_seqs > kSharedMaxSeqs) return PA_ERR_UNSUPPORTED;
+  const int group = num_q_heads / pool->num_kv_heads;
+  // the prefix work is counted in 32 bits: (query tile, key tile) pairs
+  const int64_t tiles = (int64_t)pool->num_kv_heads * (num_groups + (int64_t)num_seqs * group / 128);
+  if (tiles * (((int64_t)max_blocks_per_seq * kBlock + 127) / 128) > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (!aligned4(group_sizes) || !aligned4(prefix_lens)) return PA_ERR_ALIGN;
+  if (!workspace) return PA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return PA_ERR_ALIGN;
+  DeviceState *d = nullptr;
+  if ((st = device_state(&d)) != PA_OK) return st;  // also readies the tensor-map encoder
+  if (workspace_bytes < shared_workspace_bytes(num_seqs, num_groups, num_q_heads, pool->num_kv_heads, d->sm_count))
+    return PA_ERR_WORKSPACE;
+  CUtensorMap maps[5], omap;
+  if (!pool_map(&maps[0], pool, pool->k_cache, false) || !pool_map_vpages(&maps[1], pool, pool->v_cache) ||
+      !query_maps(&maps[2], &omap, q, out, pool->dtype, num_q_heads, num_seqs, group) ||
+      !pool_map_vpages(&maps[3], pool, pool->k_cache))
+    return PA_ERR_CUDA;
+  maps[4] = maps[1];
+  SharedParams sp{};
+  sp.group_sizes = group_sizes;
+  sp.prefix_lens = prefix_lens;
+  sp.num_groups = num_groups;
+  sp.num_seqs = num_seqs;
+  sp.num_kv_heads = pool->num_kv_heads;
+  sp.max_blocks_per_seq = max_blocks_per_seq;
+  sp.err = d->err;
+  PrefillParams pp{};
+  pp.block_tables = block_tables;
+  pp.err = d->err;
+  pp.max_blocks_per_seq = max_blocks_per_seq;
+  pp.num_kv_heads = pool->num_kv_heads;
+  pp.num_q_heads = num_q_heads;
+  pp.num_blocks = pool->num_blocks;
+  pp.scale_log2 = scale * 1.4426950408889634f;
+  DecodeParams dp{};
+  dp.q = q;
+  dp.block_tables = block_tables;
+  dp.context_lens = context_lens;
+  dp.out = out;
+  dp.err = d->err;
+  dp.max_blocks_per_seq = max_blocks_per_seq;
+  dp.num_seqs = num_seqs;
+  dp.num_kv_heads = pool->num_kv_heads;
+  dp.num_q_heads = num_q_heads;
+  dp.num_blocks = pool->num_blocks;
+  dp.scale_log2 = pp.scale_log2;
+  cudaError_t e = launch_decode_shared(sp, pp, dp, workspace, maps, pool->dtype, group, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
 size_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                          int32_t max_context_len) {
   if (num_seqs < 0 || num_kv_heads < 1 || num_q_heads < 1 || num_q_heads % num_kv_heads != 0 || max_context_len < 1)

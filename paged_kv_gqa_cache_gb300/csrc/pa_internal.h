@@ -262,6 +262,26 @@ cudaError_t launch_prefill8(const PrefillParams &p, const CUtensorMap &kmap, con
                             const CUtensorMap &qmap, const CUtensorMap &omap, int dtype, int group, bool f8,
                             cudaStream_t stream);
 
+// ---- decode over prefixes shared by groups of sequences (16-bit pools) -----------
+constexpr int kMaxPrefixGroups = 256;
+struct SharedParams {
+  const int32_t *group_sizes;   // [num_groups]
+  const int32_t *prefix_lens;   // [num_groups]
+  int32_t num_groups;
+  int32_t num_seqs;
+  int32_t num_kv_heads;
+  int32_t max_blocks_per_seq;
+  int *err;
+  void *plan;                   // workspace: the prefix kernel's plan, for the join
+  float2 *ws_ml;                //   per prefix piece and row: (max, sum)
+  float *ws_o;                  //   per prefix piece: [dims / 4][128 rows][4] unnormalised outputs
+};
+size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int sms);
+// maps: K (2 KB half boxes), V (4 KB pages) and q for the prefix, K and V (4 KB
+// swizzled pages) for the suffix.
+cudaError_t launch_decode_shared(SharedParams sp, const PrefillParams &pp, DecodeParams dp, void *workspace,
+                                 const CUtensorMap *maps, int dtype, int group, cudaStream_t stream);
+
 // ---- one persistent launch for a mixed step (16-bit pools) ---------------------
 // The step's KV write (w), its chunks' prefill (pp: no window, no workspace)
 // and its sequences' decode (dp: counters set, split items merged in the

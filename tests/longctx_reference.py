@@ -91,3 +91,23 @@ def random_pool(gen, blocks, hkv, dtype, device="cuda"):
 
 def bits(t):
     return t.detach().contiguous().cpu().view(torch.int16).numpy().copy()
+
+
+def attention_torch(q, k_cache, v_cache, tables, lens, scale):
+    """(out, sum of |p v|, largest scale * sum |q_i k_i|) of the same in float64 on the tensors' own device."""
+    S, hq, _ = q.shape
+    hkv = k_cache.shape[2]
+    G = hq // hkv
+    out = torch.zeros(q.shape, dtype=torch.float64, device=q.device)
+    mag, worst = torch.zeros_like(out), 0.0
+    for s in range(S):
+        n = int(lens[s])
+        rows = torch.as_tensor(tables[s][:-(-n // BLOCK)], device=q.device).long()
+        k = k_cache[rows].flatten(0, 1)[:n].double().transpose(0, 1)  # [Hkv, n, 128]
+        v = v_cache[rows].flatten(0, 1)[:n].double().transpose(0, 1)
+        x = q[s].double().view(hkv, G, DIM)
+        p = torch.softmax(scale * torch.matmul(x, k.transpose(1, 2)), -1)
+        out[s] = torch.matmul(p, v).view(hq, DIM)
+        mag[s] = torch.matmul(p, v.abs()).view(hq, DIM)
+        worst = max(worst, float(scale * torch.matmul(x.abs(), k.abs().transpose(1, 2)).max()))
+    return out, mag, worst

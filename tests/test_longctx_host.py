@@ -97,6 +97,35 @@ def test_decode_weights_workspace_size(lib):
     assert f(-1, 16, 8, 256) == 0 and f(4, 12, 8, 256) == 0 and f(4, 16, 8, 0) == 0
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(S=0), "PA_OK"), (dict(S=-1), "PA_ERR_SHAPE"), (dict(q=0), "PA_ERR_NULL"), (dict(groups=-1), "PA_ERR_SHAPE"),
+    (dict(sizes=0), "PA_ERR_NULL"), (dict(prefix=0), "PA_ERR_NULL"), (dict(groups=257), "PA_ERR_UNSUPPORTED"),
+    (dict(S=6001), "PA_ERR_UNSUPPORTED"), (dict(ws=0), "PA_ERR_WORKSPACE"), (dict(ws=P + 8), "PA_ERR_ALIGN"),
+    (dict(sizes=P + 2), "PA_ERR_ALIGN"), (dict(prefix=P + 1), "PA_ERR_ALIGN"), (dict(mcl=257), "PA_ERR_SHAPE"),
+    (dict(hq=24), "PA_ERR_UNSUPPORTED"), (dict(scale=-1.0), "PA_ERR_SHAPE"), (dict(pool=_pool(dtype=9)), "PA_ERR_DTYPE"),
+    (dict(mb=1 << 30), "PA_ERR_UNSUPPORTED"),
+])
+def test_decode_shared_refusals(lib, kw, status):
+    st = lib.pa_paged_attn_decode_shared(kw.get("q", P), ctypes.byref(kw.get("pool", _pool())), P, kw.get("mb", 16), P,
+                                         kw.get("S", 4), kw.get("hq", 16), kw.get("mcl", 256), kw.get("scale", 0.1),
+                                         kw.get("sizes", P), kw.get("prefix", P), kw.get("groups", 2), P,
+                                         kw.get("ws", P), kw.get("wsb", 1 << 40), None)
+    assert pa.STATUS[st] == status
+
+
+def test_shared_prefix_limits_match_the_header(lib):
+    import os
+    import re
+    header = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
+                               "pagedattn.h")).read()
+    defines = dict(re.findall(r"#define (PA_[A-Z0-9_]+) (\d+)\b", header))
+    assert int(defines["PA_MAX_PREFIX_GROUPS"]) == pa.MAX_PREFIX_GROUPS
+    for name in ("HALF", "INTERLEAVED", "PLAIN", "LINEAR", "NTK", "BANDS", "YARN"):
+        assert int(defines["PA_ROPE_" + name]) == getattr(pa, "ROPE_" + name)
+    f = lib.pa_decode_shared_workspace_bytes
+    assert f(4, 257, 16, 8) == 0 and f(6001, 1, 16, 8) == 0 and f(4, 1, 12, 8) == 0 and f(-1, 1, 16, 8) == 0
+
+
 # ---- rotary frequencies ----------------------------------------------------------------
 
 def _freqs(*a, **kw):
