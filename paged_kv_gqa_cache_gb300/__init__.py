@@ -759,12 +759,37 @@ ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = range(5)
 
 
-def _here(**tensors) -> None:
-    """The library launches on the current device: its tensors must live there."""
-    cur = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+def _complain(t, name, dtype, dev):
+    _need(t, name, dtype)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _check_all(dev: int, *specs) -> None:
+    """Every (tensor, name, dtype) is a contiguous tensor of its type on the
+    current device (the library launches there); dtype None: any."""
+    for t, name, dtype in specs:
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous() or \
+                (dtype is not None and t.dtype is not dtype):
+            _complain(t, name, dtype, dev)
+
+
+def _pool_of(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: int) -> KVPool:
+    """make_pool on the current device."""
+    _check_all(dev, (k_cache, "k_cache", None), (v_cache, "v_cache", k_cache.dtype))
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, num_kv_heads, head_dim]")
+    return KVPool(k_cache.data_ptr(), v_cache.data_ptr(), *shape, _dtype_code(k_cache))
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, dev: int) -> int:
+    """_stream, by the short way where torch has it (a fifth of a small call's host time else)."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def _hold(stream, *tensors) -> None:
@@ -797,39 +822,39 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
     [T, Hkv, 128] to ``positions``, after an RMSNorm where the weights are given,
     and write the rotated k and the unchanged v into their slots.
     ``inv_freq`` (float64 [rotary_dim / 2]) sets how much of the head turns."""
-    pool = make_pool(k_cache, v_cache)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(t, name, k_cache.dtype)
-    for name, t in (("q_norm_weight", q_norm_weight), ("k_norm_weight", k_norm_weight)):
-        if t is not None:
-            _need(t, name, k_cache.dtype)
-            if t.shape != (pool.head_dim,):
-                raise ValueError(f"{name} must be [{pool.head_dim}]")
-    _need(inv_freq, "inv_freq", torch.float64)
-    _need(positions, "positions", torch.int32)
-    _need(slot_mapping, "slot_mapping", torch.int64)
-    if q.dim() != 3 or inv_freq.dim() != 1:
-        raise ValueError("q must be [T, Hq, 128], inv_freq [rotary_dim / 2]")
-    T, hq, d = q.shape
-    if d != pool.head_dim or k.shape != (T, pool.num_kv_heads, d) or v.shape != k.shape or positions.shape != (T,) \
-            or slot_mapping.shape != (T,):
-        raise ValueError("q [T, Hq, 128], k/v [T, Hkv, 128], positions/slot_mapping [T]")
+    dev = torch.cuda.current_device()
+    pool = _pool_of(k_cache, v_cache, dev)
+    dt, hkv, d = k_cache.dtype, pool.num_kv_heads, pool.head_dim
     fresh = q_out is None
     if fresh:
         q_out = torch.empty_like(q)
-    _need(q_out, "q_out", q.dtype)
+    _check_all(dev, (q, "q", dt), (k, "k", dt), (v, "v", dt), (inv_freq, "inv_freq", torch.float64),
+               (positions, "positions", torch.int32), (slot_mapping, "slot_mapping", torch.int64),
+               (q_out, "q_out", dt))
+    T, hq = q.shape[0], q.shape[1] if q.dim() == 3 else 0
+    rows = (T, hkv, d)
+    if q.shape != (T, hq, d) or k.shape != rows or v.shape != rows or positions.shape != (T,) \
+            or slot_mapping.shape != (T,) or inv_freq.dim() != 1:
+        raise ValueError("q [T, Hq, 128], k/v [T, Hkv, 128], positions/slot_mapping [T], inv_freq [rotary_dim / 2]")
     if q_out.shape != q.shape:
         raise ValueError("q_out must have the shape of q")
-    _here(q=q, k=k, v=v, inv_freq=inv_freq, positions=positions, slot_mapping=slot_mapping, k_cache=k_cache,
-          v_cache=v_cache, q_norm_weight=q_norm_weight, k_norm_weight=k_norm_weight, q_out=q_out)
-    rope = Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), ROPE_INTERLEAVED if interleaved else ROPE_HALF,
-                float(attention_factor))
-    wq, wk = (None if t is None else t.data_ptr() for t in (q_norm_weight, k_norm_weight))
-    _check(load_library().pa_rope_kv_write(q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(rope), wq, wk,
-                                           float(eps), positions.data_ptr(), slot_mapping.data_ptr(), T, hq,
-                                           q_out.data_ptr(), ctypes.byref(pool), _stream(stream)),
-           "pa_rope_kv_write")
-    if fresh:
+    wq = wk = None
+    for name, t in (("q_norm_weight", q_norm_weight), ("k_norm_weight", k_norm_weight)):
+        if t is not None:
+            _check_all(dev, (t, name, dt))
+            if t.shape != (d,):
+                raise ValueError(f"{name} must be [{d}]")
+    if q_norm_weight is not None:
+        wq = q_norm_weight.data_ptr()
+    if k_norm_weight is not None:
+        wk = k_norm_weight.data_ptr()
+    rope = Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], ROPE_INTERLEAVED if interleaved else ROPE_HALF,
+                attention_factor)
+    _check((_lib or load_library()).pa_rope_kv_write(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(rope), wq, wk, eps, positions.data_ptr(),
+        slot_mapping.data_ptr(), T, hq, q_out.data_ptr(), ctypes.byref(pool), _stream_of(stream, dev)),
+        "pa_rope_kv_write")
+    if fresh and stream is not None:
         _hold(stream, q_out)
     return q_out
 
@@ -853,31 +878,23 @@ def paged_attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: to
     prefixes: group g is the next ``group_sizes[g]`` sequences (int32 [groups]),
     which share their first ``prefix_lens[g]`` tokens (int32 [groups], multiples
     of 16), read once through the group's first block table."""
-    pool = make_pool(k_cache, v_cache)
-    S, hq, mb, mcl = _decode_args(q, pool, k_cache, block_tables, context_lens, max_context_len)
-    _need(group_sizes, "group_sizes", torch.int32)
-    _need(prefix_lens, "prefix_lens", torch.int32)
+    dev = torch.cuda.current_device()
+    pool = _pool_of(k_cache, v_cache, dev)
+    S, hq, mb, mcl, out, fresh = _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out)
+    _check_all(dev, (group_sizes, "group_sizes", torch.int32), (prefix_lens, "prefix_lens", torch.int32))
     if group_sizes.dim() != 1 or prefix_lens.shape != group_sizes.shape:
         raise ValueError("group_sizes and prefix_lens must both be [groups]")
     n = group_sizes.shape[0]
-    fresh = []
-    if out is None:
-        out = torch.empty_like(q)
-        fresh.append(out)
-    _need(out, "out", q.dtype)
-    if out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
     if workspace is None:
         workspace = alloc_decode_shared_workspace(S, n, hq, pool.num_kv_heads, q.device)
         fresh.append(workspace)
-    _need(workspace, "workspace")
-    _here(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
-          group_sizes=group_sizes, prefix_lens=prefix_lens, out=out, workspace=workspace)
-    _check(load_library().pa_paged_attn_decode_shared(
-        q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq, mcl,
-        float(scale), group_sizes.data_ptr(), prefix_lens.data_ptr(), n, out.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "pa_paged_attn_decode_shared")
-    _hold(stream, *fresh)
+    _check_all(dev, (workspace, "workspace", None))
+    _check((_lib or load_library()).pa_paged_attn_decode_shared(
+        q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq, mcl, scale,
+        group_sizes.data_ptr(), prefix_lens.data_ptr(), n, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        _stream_of(stream, dev)), "pa_paged_attn_decode_shared")
+    if stream is not None:
+        _hold(stream, *fresh)
     return out
 
 
@@ -892,18 +909,26 @@ def alloc_decode_weights_workspace(num_seqs: int, num_q_heads: int, num_kv_heads
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
-def _decode_args(q, pool, k_cache, block_tables, context_lens, max_context_len):
-    """The checks the decode calls share; (sequences, query heads, table width, length bound)."""
-    _need(q, "q", k_cache.dtype)
-    _need(block_tables, "block_tables", torch.int32)
-    _need(context_lens, "context_lens", torch.int32)
-    if q.dim() != 3 or q.shape[2] != pool.head_dim:
+def _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out):
+    """The checks these decode calls share; (sequences, query heads, table width,
+    length bound, the output, the tensors allocated here)."""
+    dt = torch.float16 if pool.dtype == PA_F16 else torch.bfloat16
+    fresh = []
+    if out is None:
+        out = torch.empty_like(q)
+        fresh.append(out)
+    _check_all(dev, (q, "q", dt), (block_tables, "block_tables", torch.int32),
+               (context_lens, "context_lens", torch.int32), (out, "out", dt))
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != pool.head_dim:
         raise ValueError(f"q must be [S, Hq, {pool.head_dim}]")
-    S, hq, _ = q.shape
+    if out.shape != shape:
+        raise ValueError("out must have the shape of q")
+    S, hq, _ = shape
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
         raise ValueError("block_tables must be [S, max_blocks], context_lens [S]")
     mb = block_tables.shape[1]
-    return S, hq, mb, int(max_context_len) if max_context_len is not None else mb * pool.block_size
+    return S, hq, mb, mb * pool.block_size if max_context_len is None else max_context_len, out, fresh
 
 
 def paged_attn_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -917,36 +942,29 @@ def paged_attn_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     bound]; the same tensor: in place; ``weights_in`` None: zeros).  Entries from
     a sequence's length on are not touched.  ``max_context_len`` defaults to what
     both the block tables and the weights hold.  Returns (out, weights_out)."""
-    pool = make_pool(k_cache, v_cache)
-    S, hq, mb, mcl = _decode_args(q, pool, k_cache, block_tables, context_lens, max_context_len)
-    _need(weights_out, "weights_out", torch.float32)
-    if max_context_len is None and weights_out.dim() == 3:
-        mcl = min(mcl, weights_out.shape[2])
-    if weights_out.dim() != 3 or weights_out.shape[:2] != (S, pool.num_kv_heads):
+    dev = torch.cuda.current_device()
+    pool = _pool_of(k_cache, v_cache, dev)
+    S, hq, mb, mcl, out, fresh = _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out)
+    _check_all(dev, (weights_out, "weights_out", torch.float32))
+    wshape = weights_out.shape
+    if len(wshape) != 3 or wshape[0] != S or wshape[1] != pool.num_kv_heads:
         raise ValueError(f"weights_out must be [{S}, {pool.num_kv_heads}, stride]")
     if weights_in is not None:
-        _need(weights_in, "weights_in", torch.float32)
-        if weights_in.shape != weights_out.shape:
+        _check_all(dev, (weights_in, "weights_in", torch.float32))
+        if weights_in.shape != wshape:
             raise ValueError("weights_in and weights_out must have one shape")
-    fresh = []
-    if out is None:
-        out = torch.empty_like(q)
-        fresh.append(out)
-    _need(out, "out", q.dtype)
-    if out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
+    if max_context_len is None:
+        mcl = min(mcl, wshape[2])
     if workspace is None:
         workspace = alloc_decode_weights_workspace(S, hq, pool.num_kv_heads, mcl, q.device)
         fresh.append(workspace)
-    _need(workspace, "workspace")
-    _here(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
-          weights_in=weights_in, weights_out=weights_out, out=out, workspace=workspace)
-    _check(load_library().pa_paged_attn_decode_weights(
-        q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq, mcl,
-        float(scale), None if weights_in is None else weights_in.data_ptr(), weights_out.data_ptr(),
-        weights_out.shape[2], out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream(stream)), "pa_paged_attn_decode_weights")
-    _hold(stream, *fresh)
+    _check_all(dev, (workspace, "workspace", None))
+    _check((_lib or load_library()).pa_paged_attn_decode_weights(
+        q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq, mcl, scale,
+        None if weights_in is None else weights_in.data_ptr(), weights_out.data_ptr(), wshape[2], out.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _stream_of(stream, dev)), "pa_paged_attn_decode_weights")
+    if stream is not None:
+        _hold(stream, *fresh)
     return out, weights_out
 
 
@@ -963,42 +981,38 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
     (default: in place).  Returns (kept int32 [S, Hkv, budget] with -1 past the
     new length, new context lengths int32 [S]).  ``max_context_len`` is a host
     bound on ``context_lens`` for the check that the weights cover it."""
-    pool = make_pool(k_cache, v_cache)
-    _need(block_tables, "block_tables", torch.int32)
-    _need(context_lens, "context_lens", torch.int32)
-    _need(weights, "weights", torch.float32)
+    dev = torch.cuda.current_device()
+    pool = _pool_of(k_cache, v_cache, dev)
     dst = block_tables if dst_block_tables is None else dst_block_tables
     w_out = weights if weights_out is None else weights_out
-    _need(dst, "dst_block_tables", torch.int32)
-    _need(w_out, "weights_out", torch.float32)
+    i32, f32 = torch.int32, torch.float32
+    _check_all(dev, (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
+               (weights, "weights", f32), (dst, "dst_block_tables", i32), (w_out, "weights_out", f32))
     if block_tables.dim() != 2 or dst.dim() != 2 or weights.dim() != 3 or w_out.dim() != 3:
         raise ValueError("block_tables and dst_block_tables must be [S, max_blocks], the weights [S, Hkv, stride]")
-    S, hkv = block_tables.shape[0], pool.num_kv_heads
-    if context_lens.shape != (S,) or dst.shape[0] != S or weights.shape[:2] != (S, hkv) or \
-            w_out.shape[:2] != (S, hkv):
+    S, mb = block_tables.shape
+    hkv = pool.num_kv_heads
+    ws, wos = weights.shape, w_out.shape
+    if context_lens.shape != (S,) or dst.shape[0] != S or ws[0] != S or ws[1] != hkv or wos[0] != S or wos[1] != hkv:
         raise ValueError(f"sizes disagree: {S} sequences, {hkv} KV heads")
-    if max_context_len is not None and int(max_context_len) > weights.shape[2]:
-        raise ValueError(f"weights hold {weights.shape[2]} tokens, max_context_len is {int(max_context_len)}")
-    budget = int(budget)
+    if max_context_len is not None and max_context_len > ws[2]:
+        raise ValueError(f"weights hold {ws[2]} tokens, max_context_len is {max_context_len}")
     fresh = []
     if kept is None:
-        kept = torch.empty((S, hkv, max(budget, 0)), dtype=torch.int32, device=k_cache.device)
+        kept = torch.empty((S, hkv, max(budget, 0)), dtype=i32, device=k_cache.device)
         fresh.append(kept)
     if new_context_lens is None:
-        new_context_lens = torch.empty((S,), dtype=torch.int32, device=k_cache.device)
+        new_context_lens = torch.empty((S,), dtype=i32, device=k_cache.device)
         fresh.append(new_context_lens)
-    _need(kept, "kept", torch.int32)
-    _need(new_context_lens, "new_context_lens", torch.int32)
+    _check_all(dev, (kept, "kept", i32), (new_context_lens, "new_context_lens", i32))
     if kept.shape != (S, hkv, budget) or new_context_lens.shape != (S,):
         raise ValueError(f"kept must be [{S}, {hkv}, {budget}], new_context_lens [{S}]")
-    _here(k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens, weights=weights,
-          dst_block_tables=dst, weights_out=w_out, kept=kept, new_context_lens=new_context_lens)
-    _check(load_library().pa_kv_evict(ctypes.byref(pool), block_tables.data_ptr(), block_tables.shape[1],
-                                      context_lens.data_ptr(), S, weights.data_ptr(), weights.shape[2], budget,
-                                      int(recent), int(sinks), dst.data_ptr(), dst.shape[1], w_out.data_ptr(),
-                                      w_out.shape[2], kept.data_ptr(), new_context_lens.data_ptr(),
-                                      _stream(stream)), "pa_kv_evict")
-    _hold(stream, *fresh)
+    _check((_lib or load_library()).pa_kv_evict(
+        ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, weights.data_ptr(), ws[2], budget,
+        recent, sinks, dst.data_ptr(), dst.shape[1], w_out.data_ptr(), wos[2], kept.data_ptr(),
+        new_context_lens.data_ptr(), _stream_of(stream, dev)), "pa_kv_evict")
+    if stream is not None:
+        _hold(stream, *fresh)
     return kept, new_context_lens
 
 

@@ -701,7 +701,7 @@ shared_join_kernel(const SharedParams sp, const DecodeParams p) {
 
 template <typename T, int G>
 cudaError_t launch_shared_typed(const SharedParams &sp, const PrefillParams &pp, const DecodeParams &dp0,
-                                const CUtensorMap *maps, cudaStream_t stream) {
+                                const CUtensorMap *maps, int sms, cudaStream_t stream) {
   DecodeParams dp = dp0;
   static KernelSetup prefix_setup, suffix_setup;
   cudaError_t e = kernel_setup(prefix_setup, shared_prefix_kernel<T, G>, P_SMEM_BYTES, kThreads, nullptr);
@@ -710,10 +710,10 @@ cudaError_t launch_shared_typed(const SharedParams &sp, const PrefillParams &pp,
   int per_sm = 0;
   e = kernel_setup(suffix_setup, shared_suffix_kernel<T, G>, smem, NW * 32, &per_sm);
   if (e != cudaSuccess) return e;
-  int grid = sm_count() * per_sm;
+  int grid = sms * per_sm;
   if (grid * NW > kDecodeMaxWorkers) grid = kDecodeMaxWorkers / NW;
   dp.num_workers = grid * NW;
-  e = launch_pdl(shared_prefix_kernel<T, G>, dim3(sm_count()), dim3(kThreads), P_SMEM_BYTES, stream, maps[0], maps[1],
+  e = launch_pdl(shared_prefix_kernel<T, G>, dim3(sms), dim3(kThreads), P_SMEM_BYTES, stream, maps[0], maps[1],
                  maps[2], sp, pp);
   if (e != cudaSuccess) return e;
   e = launch_pdl(shared_suffix_kernel<T, G>, dim3(grid), dim3(NW * 32), smem, stream, maps[3], maps[4], sp, dp);
@@ -749,15 +749,15 @@ size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int
 }
 
 cudaError_t launch_decode_shared(SharedParams sp, const PrefillParams &pp, DecodeParams dp, void *workspace,
-                                 const CUtensorMap *maps, int dtype, int group, cudaStream_t stream) {
-  const SharedLayout l = shared_layout(dp.num_seqs, sp.num_groups, dp.num_q_heads, dp.num_kv_heads, sm_count());
+                                 const CUtensorMap *maps, int dtype, int group, int sms, cudaStream_t stream) {
+  const SharedLayout l = shared_layout(dp.num_seqs, sp.num_groups, dp.num_q_heads, dp.num_kv_heads, sms);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   sp.plan = ws + l.plan;
   sp.ws_ml = reinterpret_cast<float2 *>(ws + l.ml);
   sp.ws_o = reinterpret_cast<float *>(ws + l.o);
   decode_workspace_carve(ws + l.decode, SIZE_MAX, dp.num_seqs, dp.num_q_heads, dp.num_kv_heads, dp);
 #define PA_SHARED_CASE(T, G) \
-  if (group == G) return launch_shared_typed<T, G>(sp, pp, dp, maps, stream);
+  if (group == G) return launch_shared_typed<T, G>(sp, pp, dp, maps, sms, stream);
   if (dtype == PA_BF16) {
     PA_SHARED_CASE(__nv_bfloat16, 1)
     PA_SHARED_CASE(__nv_bfloat16, 2)

@@ -132,14 +132,14 @@ decode_weights_kernel(const DecodeParams p, const float *scores, const float *we
 
 template <typename T, int G>
 cudaError_t launch_weights_typed(const DecodeParams &p0, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                                 const DecodeWeightsParams &wp, cudaStream_t stream) {
+                                 const DecodeWeightsParams &wp, int sms, cudaStream_t stream) {
   DecodeParams p = p0;
   const int smem = 1024 + SplitSmem16<NW>::kPrefixOff + (p.num_seqs + 1) * 4;
   static KernelSetup setup;
   int per_sm = 0;
   cudaError_t e = kernel_setup(setup, decode_scores_kernel<T, G>, smem, NW * 32, &per_sm);
   if (e != cudaSuccess) return e;
-  int grid = sm_count() * per_sm;
+  int grid = sms * per_sm;
   const int64_t pages = (int64_t)p.num_seqs * p.num_kv_heads * ((wp.max_len + kBlock - 1) / kBlock);
   const int64_t want = ((pages + 3) / 4 + NW - 1) / NW;  // at least 4 pages per warp
   if (want < grid) grid = (int)want;
@@ -157,9 +157,9 @@ cudaError_t launch_weights_typed(const DecodeParams &p0, const CUtensorMap &kmap
 }  // namespace
 
 cudaError_t launch_decode_weights(const DecodeParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap, int dtype,
-                                  int group, const DecodeWeightsParams &wp, cudaStream_t stream) {
+                                  int group, const DecodeWeightsParams &wp, int sms, cudaStream_t stream) {
 #define PA_WEIGHTS_CASE(T, G) \
-  if (group == G) return launch_weights_typed<T, G>(p, kmap, vmap, wp, stream);
+  if (group == G) return launch_weights_typed<T, G>(p, kmap, vmap, wp, sms, stream);
   if (dtype == PA_BF16) {
     PA_WEIGHTS_CASE(__nv_bfloat16, 1)
     PA_WEIGHTS_CASE(__nv_bfloat16, 2)

@@ -263,14 +263,14 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv_evict_kernel(const EvictPara
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream) {
+cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
   static KernelSetup setup;
   const int smem = (int)sizeof(EvSmem);
   cudaError_t e = kernel_setup(setup, kv_evict_kernel, smem, kEvThreads, nullptr);
   if (e != cudaSuccess) return e;
   const int items = p.num_seqs * p.num_kv_heads;
   int C = 8;
-  while (C > 1 && items * C > 2 * sm_count()) C >>= 1;
+  while (C > 1 && items * C > 2 * sms) C >>= 1;
   return launch_pdl_cluster(kv_evict_kernel, dim3(items * C), dim3(kEvThreads), smem, C, stream, p);
 }
 

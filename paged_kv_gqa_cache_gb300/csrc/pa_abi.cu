@@ -530,16 +530,19 @@ namespace {
 
 // The prefill call; with a workspace (and at most kMaxChunksBalanced chunks)
 // the balanced launch runs, else the plain one.
-// q (and out) as a 3-D tensor {dim, query head, token}; boxes of {64 dims,
+// q (or out) as a 3-D tensor {dim, query head, token}; boxes of {64 dims,
 // G heads, 128/G tokens} give 128 rows (token-major, head-minor) of 128 bytes.
-bool query_maps(CUtensorMap *qmap, CUtensorMap *omap, const void *q, void *out, int dtype, int num_q_heads,
-                int total_q_tokens, int group) {
+bool query_map(CUtensorMap *map, const void *q, int dtype, int num_q_heads, int total_q_tokens, int group) {
   const uint64_t dims[3] = {(uint64_t)kHeadDim, (uint64_t)num_q_heads, (uint64_t)total_q_tokens};
   const uint64_t strides[2] = {kHeadDim * 2ull, (uint64_t)num_q_heads * kHeadDim * 2ull};
   const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)(128 / group)};
-  return encode_tensor_map(qmap, map_dtype(dtype), 3, const_cast<void *>(q), dims, strides, box,
-                           CU_TENSOR_MAP_SWIZZLE_128B) &&
-         encode_tensor_map(omap, map_dtype(dtype), 3, out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode_tensor_map(map, map_dtype(dtype), 3, const_cast<void *>(q), dims, strides, box,
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool query_maps(CUtensorMap *qmap, CUtensorMap *omap, const void *q, void *out, int dtype, int num_q_heads,
+                int total_q_tokens, int group) {
+  return query_map(qmap, q, dtype, num_q_heads, total_q_tokens, group) &&
+         query_map(omap, out, dtype, num_q_heads, total_q_tokens, group);
 }
 
 pa_status prefill_call(const void *q, const int32_t *chunk_starts, const int32_t *chunk_lens, const pa_kv_pool *pool,
@@ -824,7 +827,7 @@ pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, const pa
   p.interleaved = rope->layout == PA_ROPE_INTERLEAVED;
   p.attention_factor = rope->attention_factor;
   p.eps = eps;
-  cudaError_t e = launch_rope_kv(p, pool->dtype, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_rope_kv(p, pool->dtype, d->sm_count, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
@@ -864,10 +867,9 @@ pa_status pa_paged_attn_decode_shared(const void *q, const pa_kv_pool *pool, con
   if ((st = device_state(&d)) != PA_OK) return st;  // also readies the tensor-map encoder
   if (workspace_bytes < shared_workspace_bytes(num_seqs, num_groups, num_q_heads, pool->num_kv_heads, d->sm_count))
     return PA_ERR_WORKSPACE;
-  CUtensorMap maps[5], omap;
+  CUtensorMap maps[5];
   if (!pool_map(&maps[0], pool, pool->k_cache, false) || !pool_map_vpages(&maps[1], pool, pool->v_cache) ||
-      !query_maps(&maps[2], &omap, q, out, pool->dtype, num_q_heads, num_seqs, group) ||
-      !pool_map_vpages(&maps[3], pool, pool->k_cache))
+      !query_map(&maps[2], q, pool->dtype, num_q_heads, num_seqs, group) || !pool_map_vpages(&maps[3], pool, pool->k_cache))
     return PA_ERR_CUDA;
   maps[4] = maps[1];
   SharedParams sp{};
@@ -898,7 +900,8 @@ pa_status pa_paged_attn_decode_shared(const void *q, const pa_kv_pool *pool, con
   dp.num_q_heads = num_q_heads;
   dp.num_blocks = pool->num_blocks;
   dp.scale_log2 = pp.scale_log2;
-  cudaError_t e = launch_decode_shared(sp, pp, dp, workspace, maps, pool->dtype, group, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_decode_shared(sp, pp, dp, workspace, maps, pool->dtype, group, d->sm_count,
+                                       static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
@@ -953,7 +956,7 @@ pa_status pa_paged_attn_decode_weights(const void *q, const pa_kv_pool *pool, co
   wp.weights_stride = weights_stride;
   wp.max_len = max_context_len;
   cudaError_t e = launch_decode_weights(p, kmap, vmap, pool->dtype, num_q_heads / pool->num_kv_heads, wp,
-                                        static_cast<cudaStream_t>(stream));
+                                        d->sm_count, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
@@ -1002,7 +1005,7 @@ pa_status pa_kv_evict(const pa_kv_pool *pool, const int32_t *block_tables, int32
   p.budget = budget;
   p.recent = recent;
   p.sinks = sinks;
-  cudaError_t e = launch_evict(p, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_evict(p, d->sm_count, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 

@@ -98,7 +98,7 @@ struct RopeKvParams {
   float attention_factor;
   float eps;
 };
-cudaError_t launch_rope_kv(const RopeKvParams &p, int dtype, cudaStream_t stream);
+cudaError_t launch_rope_kv(const RopeKvParams &p, int dtype, int sms, cudaStream_t stream);
 
 // ---- eviction by accumulated attention weight ------------------------------------------------
 struct EvictParams {
@@ -123,7 +123,7 @@ struct EvictParams {
   int32_t recent;
   int32_t sinks;
 };
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream);
 
 // ---- self-test of the bounded waits --------------------------------------------------------
 cudaError_t launch_bounded_wait_selftest(int *err, uint64_t limit_ns, cudaStream_t stream);
@@ -208,7 +208,7 @@ struct DecodeWeightsParams {
   int32_t max_len;           // the longest sequence that is computed
 };
 cudaError_t launch_decode_weights(const DecodeParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap, int dtype,
-                                  int group, const DecodeWeightsParams &wp, cudaStream_t stream);
+                                  int group, const DecodeWeightsParams &wp, int sms, cudaStream_t stream);
 
 // ---- chunked prefill (tcgen05 tensor cores) -------------------------------------
 struct PrefillParams {
@@ -280,7 +280,7 @@ size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int
 // maps: K (2 KB half boxes), V (4 KB pages) and q for the prefix, K and V (4 KB
 // swizzled pages) for the suffix.
 cudaError_t launch_decode_shared(SharedParams sp, const PrefillParams &pp, DecodeParams dp, void *workspace,
-                                 const CUtensorMap *maps, int dtype, int group, cudaStream_t stream);
+                                 const CUtensorMap *maps, int dtype, int group, int sms, cudaStream_t stream);
 
 // ---- one persistent launch for a mixed step (16-bit pools) ---------------------
 // The step's KV write (w), its chunks' prefill (pp: no window, no workspace)

@@ -22,11 +22,15 @@
 // plus pi * 2^-25 from the conversion to fp32.
 //
 // HBM-bound: one pass over q, k and v (24.6 KB in and out per token at 32 / 8
-// heads).  A CTA takes one token at a time: its first d / 2 threads compute
-// the token's angles once for all of its heads, through shared memory (two
-// buffers, one barrier per token); 16 lanes hold one head row (8 values each,
-// 16-byte loads and stores), and a thread issues the loads of all its rows of
-// the token before the angles and the first use.
+// heads).  16 lanes hold one head row, 8 values each, chosen so that a lane
+// holds both values of its 4 pairs: dims 4 l .. and d / 2 + 4 l .. of the
+// rotated part in the half layout (two 8-byte accesses), 8 l .. in the
+// interleaved one, so that no value crosses a lane and a lane's 4 (cos, sin)
+// stay in registers for all rows of the token.  A CTA takes 4 tokens at a time
+// (2 warps each), or, when there are too few tokens to fill the GPU so, one
+// (8 warps): its threads compute the tokens' angles once for all heads, through
+// shared memory (two buffers, one barrier per step), while the first rows'
+// loads are on their way.
 #include "pa_device.cuh"
 
 namespace pa {
@@ -34,10 +38,12 @@ namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kRopeKvThreads = 256;
-constexpr int kRowsAtOnce = kRopeKvThreads / 16;  // head rows one pass of the CTA covers
-constexpr int kPasses = 3;                        // passes whose loads are in flight together
+constexpr int kBatch = 4;  // rows per half-warp whose loads are in flight together
 
-enum RopeMode { kInterleaved = 0, kHalfLanes = 1, kHalfAny = 2 };
+// kPairs: a lane holds both values of its pairs (interleaved, or half with
+// rotary_dim a multiple of 8); kExchange: any even rotary_dim in the half
+// layout, values exchanged through shared memory.
+enum RopeMode { kInterleaved = 0, kHalfPairs = 1, kHalfExchange = 2 };
 
 // The fraction of a turn per position as a 64-bit fixed-point number.
 __device__ __forceinline__ long long turns_fixed(double inv_freq) {
@@ -45,178 +51,195 @@ __device__ __forceinline__ long long turns_fixed(double inv_freq) {
   return __double2ll_rn((t - rint(t)) * 18446744073709551616.0);
 }
 
-// 8 values of one row (16 lanes per row, this lane's dims d0 .. d0 + 7) after
-// the optional norm, rotated.  cs: the token's (cos, sin) pairs.  Every lane
-// of the warp takes part (kHalfLanes shuffles, kHalfAny exchanges through the
-// warp's staging rows).
-template <int MODE>
-__device__ __forceinline__ void rotate_row(float (&x)[8], const float2 *cs, int d, int lane, float *stage) {
-  const int l16 = lane & 15, d0 = l16 * 8;
-  if constexpr (MODE == kInterleaved) {
-#pragma unroll
-    for (int e = 0; e < 8; e += 2)
-      if (d0 + e < d) {
-        const float2 c = cs[(d0 + e) >> 1];
-        const float a = x[e], b = x[e + 1];
-        x[e] = a * c.x - b * c.y;
-        x[e + 1] = b * c.x + a * c.y;
-      }
-  } else if constexpr (MODE == kHalfLanes) {  // d a multiple of 16: the partner's 8 dims are one lane's
-    const int hl = d >> 4;                    // lanes per half
-    const bool lo = l16 < hl;
-    const int src = (lane & 16) | (lo ? l16 + hl : (l16 < 2 * hl ? l16 - hl : l16));
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(FULL, x[e], src);
-    if (l16 < 2 * hl) {
-      const float4 *c4 = reinterpret_cast<const float4 *>(cs + (lo ? d0 : d0 - (d >> 1)));
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float4 c = c4[e >> 1];  // (cos, sin) of two consecutive pairs
-        const float s0 = lo ? -c.y : c.y, s1 = lo ? -c.w : c.w;
-        x[e] = x[e] * c.x + y[e] * s0;
-        x[e + 1] = x[e + 1] * c.z + y[e + 1] * s1;
-      }
-    }
-  } else {
-    float *row = stage + (lane >> 4) * kHeadDim;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) row[d0 + e] = x[e];
-    __syncwarp();
-    const int half = d >> 1;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int j = d0 + e;
-      if (j < d) {
-        const bool lo = j < half;
-        const float2 c = cs[lo ? j : j - half];
-        const float y = row[lo ? j + half : j - half];
-        x[e] = x[e] * c.x + (lo ? -y : y) * c.y;
-      }
-    }
-    __syncwarp();
-  }
-}
-
-template <typename T, int MODE, bool NORM>
-__global__ void __launch_bounds__(kRopeKvThreads) rope_kv_kernel(const RopeKvParams p) {
-  __shared__ __align__(16) float2 cs_buf[2][kHeadDim / 2];
-  __shared__ float stage_buf[MODE == kHalfAny ? kRopeKvThreads / 32 * 2 * kHeadDim : 1];
+// TOK tokens per CTA and step, 8 / TOK warps each.
+template <typename T, int MODE, bool NORM, int TOK>
+__global__ void __launch_bounds__(kRopeKvThreads, 4) rope_kv_kernel(const RopeKvParams p) {
+  constexpr int kWarps = kRopeKvThreads / 32 / TOK;  // warps per token
+  constexpr int kStep = 2 * kWarps;                  // rows per pass of them
+  __shared__ __align__(16) float2 cs_buf[2][TOK][kHeadDim / 2];
+  __shared__ float stage_buf[MODE == kHalfExchange ? kRopeKvThreads / 16 * kHeadDim : 1];
   const int tid = threadIdx.x, lane = tid & 31, l16 = lane & 15;
   const int hq = p.num_q_heads, hkv = p.num_kv_heads;
   const int rows = hq + 2 * hkv, d = p.rotary_dim;
-  float *stage = stage_buf + (MODE == kHalfAny ? (tid >> 5) * 2 * kHeadDim : 0);
+  // this lane's values: dims d0 .. d0 + 3 and d1 .. d1 + 3; its pairs' angles: pair 4 l16 + i
+  const bool split = MODE == kHalfPairs && 8 * l16 < d;
+  const int d0 = split ? 4 * l16 : 8 * l16, d1 = split ? d / 2 + 4 * l16 : 8 * l16 + 4;
+  float *stage = stage_buf + (MODE == kHalfExchange ? (tid >> 4) * kHeadDim : 0);
+  const int tok = tid / (32 * kWarps);                          // this warp's token of the step
+  const int r_first = ((tid >> 5) % kWarps) * 2 + (lane >> 4);  // this half-warp's first row
   griddep_wait();  // q, k, v may be the previous kernel's output; the pool may be read by it
   long long turns = 0;
-  if (tid < d / 2) turns = turns_fixed(__ldg(p.inv_freq + tid));
-  float wq[8], wk[8];
+  if (tid < TOK * 64 && (tid & 63) < d / 2) turns = turns_fixed(__ldg(p.inv_freq + (tid & 63)));
+  uint2 wq[2], wk[2];
   if constexpr (NORM) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q_weight) + 8 * l16);
-    const uint4 b = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_weight) + 8 * l16);
-    const uint32_t ua[4] = {a.x, a.y, a.z, a.w}, ub[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 fa = Pack<T>::to_f2(ua[i]), fb = Pack<T>::to_f2(ub[i]);
-      wq[2 * i] = fa.x, wq[2 * i + 1] = fa.y;
-      wk[2 * i] = fb.x, wk[2 * i + 1] = fb.y;
-    }
+    wq[0] = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p.q_weight) + d0);
+    wq[1] = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p.q_weight) + d1);
+    wk[0] = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p.k_weight) + d0);
+    wk[1] = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p.k_weight) + d1);
   }
   int buf = 0;
-  for (int t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
-    const int pos = __ldg(p.positions + t);
-    const int64_t slot = __ldg(p.slots + t);
-    if (pos < 0 || slot < 0 || slot >= p.num_slots) {  // (the same in every thread) nothing of it is written
-      if (tid == 0) set_error(p.err, PA_ERR_RANGE, t);
-      continue;
-    }
-    auto source = [&](int r) {
-      return r < hq         ? static_cast<const T *>(p.q) + ((int64_t)t * hq + r) * kHeadDim
-             : r < hq + hkv ? static_cast<const T *>(p.k) + ((int64_t)t * hkv + (r - hq)) * kHeadDim
-                            : static_cast<const T *>(p.v) + ((int64_t)t * hkv + (r - hq - hkv)) * kHeadDim;
+  for (int t0 = blockIdx.x * TOK; t0 < p.num_tokens; t0 += gridDim.x * TOK) {  // (block-uniform)
+    const int t = t0 + tok;
+    const int pos = t < p.num_tokens ? __ldg(p.positions + t) : -1;
+    const int64_t slot = t < p.num_tokens ? __ldg(p.slots + t) : -1;
+    const bool ok = pos >= 0 && slot >= 0 && slot < p.num_slots;  // else nothing of the token is written
+    if (!ok && t < p.num_tokens && tid % (32 * kWarps) == 0) set_error(p.err, PA_ERR_RANGE, t);
+    auto load = [&](int r, uint2 (&x)[2]) {
+      const T *src = r < hq         ? static_cast<const T *>(p.q) + ((int64_t)t * hq + r) * kHeadDim
+                     : r < hq + hkv ? static_cast<const T *>(p.k) + ((int64_t)t * hkv + (r - hq)) * kHeadDim
+                                    : static_cast<const T *>(p.v) + ((int64_t)t * hkv + (r - hq - hkv)) * kHeadDim;
+      if constexpr (MODE == kHalfPairs) {
+        x[0] = *reinterpret_cast<const uint2 *>(src + d0);
+        x[1] = *reinterpret_cast<const uint2 *>(src + d1);
+      } else {
+        const uint4 u = *reinterpret_cast<const uint4 *>(src + d0);
+        x[0] = make_uint2(u.x, u.y);
+        x[1] = make_uint2(u.z, u.w);
+      }
     };
-    bool first = true;
-    for (int r0 = 0; r0 < rows; r0 += kRowsAtOnce * kPasses) {
-      uint4 raw[kPasses];
+    uint2 raw[kBatch][2];
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int r = r0 + i * kRowsAtOnce + (tid >> 4);
-        raw[i] = r < rows ? *reinterpret_cast<const uint4 *>(source(r) + 8 * l16) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = r_first + i * kStep;
+      raw[i][0] = raw[i][1] = make_uint2(0, 0);
+      if (ok && r < rows) load(r, raw[i]);
+    }
+    // the step's angles, while the rows are on their way
+    if (tid < TOK * 64 && (tid & 63) < d / 2) {
+      const int at = t0 + (tid >> 6);
+      const int pa = at < p.num_tokens ? __ldg(p.positions + at) : 0;
+      const long long turn = (long long)((unsigned long long)turns * (unsigned long long)(unsigned)pa);
+      float s, c;
+      sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+      cs_buf[buf][tid >> 6][tid & 63] = make_float2(c * p.attention_factor, s * p.attention_factor);
+    }
+    __syncthreads();
+    if (ok) {  // (warp-uniform)
+      float2 cs[4];
+      if constexpr (MODE != kHalfExchange) {
+        const float4 *src = reinterpret_cast<const float4 *>(cs_buf[buf][tok] + 4 * l16);
+        const float4 u = src[0], v = src[1];  // (pairs past rotary_dim / 2 are not used)
+        cs[0] = make_float2(u.x, u.y), cs[1] = make_float2(u.z, u.w);
+        cs[2] = make_float2(v.x, v.y), cs[3] = make_float2(v.z, v.w);
       }
-      if (first) {  // the token's angles, while the rows are on their way
-        if (tid < d / 2) {
-          const long long turn = (long long)((unsigned long long)turns * (unsigned long long)(unsigned)pos);
-          float s, c;
-          sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-          cs_buf[buf][tid] = make_float2(c * p.attention_factor, s * p.attention_factor);
-        }
-        __syncthreads();
-        first = false;
-      }
+      for (int r0 = 0; r0 < rows; r0 += kStep * kBatch) {
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int r = r0 + i * kRowsAtOnce + (tid >> 4);
-        const int rw = r0 + i * kRowsAtOnce + (tid >> 5) * 2;  // the warp's first row
-        if (rw >= rows) break;                                 // (warp-uniform)
-        uint4 out = raw[i];
-        if (rw < hq + hkv) {  // (warp-uniform) the warp holds a query or key row
-          const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-          float x[8];
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = r0 + r_first + i * kStep;
+          if (r0 + i * kStep + ((tid >> 5) % kWarps) * 2 >= rows) break;  // (warp-uniform)
+          uint2 out[2] = {raw[i][0], raw[i][1]};
+          if (r0 + i * kStep + ((tid >> 5) % kWarps) * 2 < hq + hkv) {  // the warp holds a query or key row
+            float x[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = Pack<T>::to_f2(u[k]);
-            x[2 * k] = f.x, x[2 * k + 1] = f.y;
+            for (int k = 0; k < 2; ++k) {
+              const float2 f = Pack<T>::to_f2(raw[i][k].x), g = Pack<T>::to_f2(raw[i][k].y);
+              x[4 * k] = f.x, x[4 * k + 1] = f.y, x[4 * k + 2] = g.x, x[4 * k + 3] = g.y;
+            }
+            float inv = 1.f;
+            if constexpr (NORM) {
+              float ss = 0.f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
+#pragma unroll
+              for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(FULL, ss, off);
+              inv = rsqrtf(ss * (1.f / kHeadDim) + p.eps);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint2 w = r < hq ? wq[k] : wk[k];
+                const float2 f = Pack<T>::to_f2(w.x), g = Pack<T>::to_f2(w.y);
+                x[4 * k] *= f.x * inv, x[4 * k + 1] *= f.y * inv;
+                x[4 * k + 2] *= g.x * inv, x[4 * k + 3] *= g.y * inv;
+              }
+            }
+            if constexpr (MODE == kInterleaved) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (8 * l16 + 2 * k < d) {
+                  const float a = x[2 * k], b = x[2 * k + 1];
+                  x[2 * k] = a * cs[k].x - b * cs[k].y;
+                  x[2 * k + 1] = b * cs[k].x + a * cs[k].y;
+                }
+            } else if constexpr (MODE == kHalfPairs) {
+              if (split) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float a = x[k], b = x[4 + k];
+                  x[k] = a * cs[k].x - b * cs[k].y;
+                  x[4 + k] = b * cs[k].x + a * cs[k].y;
+                }
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) stage[8 * l16 + k] = x[k];
+              __syncwarp();
+              const int half = d >> 1;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int j = 8 * l16 + k;
+                if (j < d) {
+                  const bool low = j < half;
+                  const float2 c = cs_buf[buf][tok][low ? j : j - half];
+                  const float y = stage[low ? j + half : j - half];
+                  x[k] = x[k] * c.x + (low ? -y : y) * c.y;
+                }
+              }
+              __syncwarp();
+            }
+            if (r < hq + hkv) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                out[k] = make_uint2(Pack<T>::from_f2(x[4 * k], x[4 * k + 1]),
+                                    Pack<T>::from_f2(x[4 * k + 2], x[4 * k + 3]));
+            }
           }
-          if constexpr (NORM) {
-            float ss = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
-#pragma unroll
-            for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(FULL, ss, off);
-            const float inv = rsqrtf(ss * (1.f / kHeadDim) + p.eps);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] *= inv * (r < hq ? wq[k] : wk[k]);
+          if (r < rows) {
+            T *dst = r < hq         ? static_cast<T *>(p.q_out) + ((int64_t)t * hq + r) * kHeadDim
+                     : r < hq + hkv ? static_cast<T *>(p.k_cache) + (slot * hkv + (r - hq)) * kHeadDim
+                                    : static_cast<T *>(p.v_cache) + (slot * hkv + (r - hq - hkv)) * kHeadDim;
+            if constexpr (MODE == kHalfPairs) {
+              *reinterpret_cast<uint2 *>(dst + d0) = out[0];
+              *reinterpret_cast<uint2 *>(dst + d1) = out[1];
+            } else {
+              *reinterpret_cast<uint4 *>(dst + d0) = make_uint4(out[0].x, out[0].y, out[1].x, out[1].y);
+            }
           }
-          rotate_row<MODE>(x, cs_buf[buf], d, lane, stage);
-          if (r < hq + hkv)
-            out = make_uint4(Pack<T>::from_f2(x[0], x[1]), Pack<T>::from_f2(x[2], x[3]), Pack<T>::from_f2(x[4], x[5]),
-                             Pack<T>::from_f2(x[6], x[7]));
-        }
-        if (r < rows) {
-          T *dst = r < hq         ? static_cast<T *>(p.q_out) + ((int64_t)t * hq + r) * kHeadDim
-                   : r < hq + hkv ? static_cast<T *>(p.k_cache) + (slot * hkv + (r - hq)) * kHeadDim
-                                  : static_cast<T *>(p.v_cache) + (slot * hkv + (r - hq - hkv)) * kHeadDim;
-          st_v4(dst + 8 * l16, out);
+          const int rn = r + kStep * kBatch;  // this buffer's next row
+          if (rn < rows) load(rn, raw[i]);
         }
       }
     }
-    buf ^= 1;  // a thread is at most one token ahead of the slowest (the barrier), so two buffers do
+    buf ^= 1;  // a thread is at most one step ahead of the slowest (the barrier), so two buffers do
   }
   griddep_launch_dependents();
 }
 
-template <typename T>
+template <typename T, int TOK>
 cudaError_t launch_rope_kv_typed(const RopeKvParams &p, int grid, cudaStream_t stream) {
-  const int mode = p.interleaved ? kInterleaved : p.rotary_dim % 16 == 0 ? kHalfLanes : kHalfAny;
+  const int mode = p.interleaved ? kInterleaved : p.rotary_dim % 8 == 0 ? kHalfPairs : kHalfExchange;
 #define PA_ROPE_CASE(M, N) \
   if (mode == M && (p.q_weight != nullptr) == N) \
-    return launch_pdl(rope_kv_kernel<T, M, N>, dim3(grid), dim3(kRopeKvThreads), 0, stream, p);
+    return launch_pdl(rope_kv_kernel<T, M, N, TOK>, dim3(grid), dim3(kRopeKvThreads), 0, stream, p);
   PA_ROPE_CASE(kInterleaved, false)
   PA_ROPE_CASE(kInterleaved, true)
-  PA_ROPE_CASE(kHalfLanes, false)
-  PA_ROPE_CASE(kHalfLanes, true)
-  PA_ROPE_CASE(kHalfAny, false)
-  PA_ROPE_CASE(kHalfAny, true)
+  PA_ROPE_CASE(kHalfPairs, false)
+  PA_ROPE_CASE(kHalfPairs, true)
+  PA_ROPE_CASE(kHalfExchange, false)
+  PA_ROPE_CASE(kHalfExchange, true)
 #undef PA_ROPE_CASE
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_rope_kv(const RopeKvParams &p, int dtype, cudaStream_t stream) {
-  const int cap = sm_count() * 4;
-  const int grid = p.num_tokens < cap ? p.num_tokens : cap;
-  return dtype == PA_BF16 ? launch_rope_kv_typed<__nv_bfloat16>(p, grid, stream)
-                          : launch_rope_kv_typed<__half>(p, grid, stream);
+cudaError_t launch_rope_kv(const RopeKvParams &p, int dtype, int sms, cudaStream_t stream) {
+  const int cap = sms * 4;  // one wave: 4 CTAs fit on an SM
+  if (p.num_tokens <= cap) {  // a token per CTA
+    return dtype == PA_BF16 ? launch_rope_kv_typed<__nv_bfloat16, 1>(p, p.num_tokens, stream)
+                            : launch_rope_kv_typed<__half, 1>(p, p.num_tokens, stream);
+  }
+  const int want = (p.num_tokens + 3) / 4, grid = want < cap ? want : cap;
+  return dtype == PA_BF16 ? launch_rope_kv_typed<__nv_bfloat16, 4>(p, grid, stream)
+                          : launch_rope_kv_typed<__half, 4>(p, grid, stream);
 }
 
 }  // namespace pa
