@@ -231,6 +231,41 @@ __device__ __forceinline__ void decode_page16(uint32_t stage, int nv, const uint
   }
 }
 
+// The join of online-softmax pieces for one head's 4 dims: pieces (m, l) with o
+// come kJoinPieces at a time (m = -inf: none).
+constexpr int kJoinPieces = 8;
+struct JoinState {
+  float M = -INFINITY, L = 0.f;
+  float4 O = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(const float2 (&ml)[kJoinPieces], const float4 (&o)[kJoinPieces]) {
+    float mx = M;
+#pragma unroll
+    for (int u = 0; u < kJoinPieces; ++u) mx = fmaxf(mx, ml[u].x);
+    if (mx == -INFINITY) return;
+    const float f = ex2(M - mx);
+    L *= f;
+    O.x *= f, O.y *= f, O.z *= f, O.w *= f;
+#pragma unroll
+    for (int u = 0; u < kJoinPieces; ++u) {
+      const float w = ex2(ml[u].x - mx);
+      L = fmaf(ml[u].y, w, L);
+      O.x = fmaf(o[u].x, w, O.x);
+      O.y = fmaf(o[u].y, w, O.y);
+      O.z = fmaf(o[u].z, w, O.z);
+      O.w = fmaf(o[u].w, w, O.w);
+    }
+    M = mx;
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T *dst) const {
+    const float inv = 1.f / L;
+    uint2 pk;
+    pk.x = Pack<T>::from_f2(O.x * inv, O.y * inv);
+    pk.y = Pack<T>::from_f2(O.z * inv, O.w * inv);
+    *reinterpret_cast<uint2 *>(dst) = pk;
+  }
+};
+
 // Shared memory of NWC split workers: per warp kStages stages and their
 // barriers; then the page prefix (num_seqs + 1 ints).
 template <int NWC>

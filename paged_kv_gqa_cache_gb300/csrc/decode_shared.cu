@@ -413,7 +413,30 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     regs_dec<kRegsOther>();
     if (warp != kWarpMma) {
       // ---------------- loader warps ----------------
+      // Boxes lw, lw + 7, .. of a key tile's 16 K boxes (the 64-dim half b % 2 of
+      // page b / 2) and pages (lw + 5) % 7, + 7 of V, issued from parallel lanes.
+      // The block ids of 4 key tiles sit one per lane, the next 4 tiles' already
+      // on their way: a table read per tile would hold up every copy by an L2 trip.
       const int lw = warp - kWarpLoad0;
+      const int kbox = lw + kLoadWarps * lane, vpage = (lw + 5) % kLoadWarps + kLoadWarps * lane;
+      const int32_t *bt = nullptr;
+      int npages = 0, wbase = 0;
+      int32_t win = -1, win_next = -1;
+      auto ids_from = [&](int base) { return base + lane < npages ? __ldg(bt + base + lane) : -1; };
+      auto open_run = [&](const PUnit &U) {
+        bt = p.block_tables + (int64_t)U.seq0 * p.max_blocks_per_seq;  // the group's first sequence
+        npages = U.len / kBlock;
+        wbase = U.ka * 8;
+        win = ids_from(wbase);
+        win_next = ids_from(wbase + 32);
+      };
+      // The id of the key tile's page (every lane; -1 past the prefix), and whether it can be read.
+      auto id_of = [&](int t, int page) { return __shfl_sync(FULL, win, (t * 8 + page - wbase) & 31); };
+      PUnit U;
+      if (x0 < x1) {
+        U = punit_at<G>(pl, x0, x1);
+        open_run(U);
+      }
       griddep_wait();  // Q, K and V may come from the kernels before
       // The suffix kernel may start: the work before this kernel has ended, and
       // it reads nothing that this kernel writes.
@@ -421,13 +444,13 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
       if (b == 0)  // the join's copy of the plan (after the wait: the previous call's join may still read it)
         for (int i = lw * 32 + lane; i < (int)(sizeof(SharedPlan) / 4); i += kLoadWarps * 32)
           reinterpret_cast<int32_t *>(sp.plan)[i] = reinterpret_cast<const int32_t *>(&pl)[i];
-      const int kb0 = lw, vb0 = (lw + 5) % kLoadWarps;
       int c = 0, ui = 0, k_issued = 0, v_issued = 0;
       for (int x = x0; x < x1 && !timed_out; ++ui) {
-        const PUnit U = punit_at<G>(pl, x, x1);
+        if (ui > 0) {
+          U = punit_at<G>(pl, x, x1);
+          open_run(U);
+        }
         x += U.kb - U.ka;
-        const int32_t *bt = p.block_tables + (int64_t)U.seq0 * p.max_blocks_per_seq;  // the group's first sequence
-        const int npages = U.len / kBlock;
         if (lw == 0 && lane == 0) {
           if (ui > 0 && !mbar_wait(&bars.q_free, (ui - 1) & 1)) timed_out = true;
           // (rows past the group belong to other sequences or read as zeros; nothing is stored for them)
@@ -438,22 +461,55 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         timed_out = __any_sync(FULL, timed_out);
         for (int t = U.ka; t < U.kb && !timed_out; ++t, ++c) {
           const int ks = c % kKStages, vs = c % kPVStages;
-          if (c >= kKStages && !mbar_wait(&bars.s_full[ks], ((c - kKStages) / kKStages) & 1)) {
-            timed_out = true;
-            break;
+          if (t * 8 >= wbase + 32) {
+            wbase += 32;
+            win = win_next;
+            win_next = ids_from(wbase + 32);
           }
-          load_boxes(smem + P_OFF_K + ks * 2 * kHalf, &kmap, &bars.k_full[ks], t, kb0, U.h, 0, npages, nullptr, bt, p,
-                     U.seq0, lane);
-          k_issued = c + 1;
-          if (c >= kPVStages && !mbar_wait(&bars.pv_done[vs], ((c - kPVStages) / kPVStages) & 1)) {
-            timed_out = true;
-            break;
+          const int kid = id_of(t, kbox >> 1), vid = id_of(t, vpage);
+          {
+            const bool in = kbox < 16 && t * 8 + (kbox >> 1) < npages;
+            const bool ok = in && (unsigned)kid < (unsigned)p.num_blocks;
+            const unsigned okmask = __ballot_sync(FULL, ok);
+            if (c >= kKStages && !mbar_wait(&bars.s_full[ks], ((c - kKStages) / kKStages) & 1)) timed_out = true;
+            if (__any_sync(FULL, timed_out)) {
+              timed_out = true;
+              break;
+            }
+            uint8_t *box = smem + P_OFF_K + ks * 2 * kHalf + (kbox & 1) * kHalf + (kbox >> 1) * 2048;
+            if (in && !ok) {  // rare: keep the products finite
+              if ((kbox & 1) == 0) set_error(p.err, PA_ERR_RANGE, U.seq0);
+              for (int i = 0; i < 128; ++i) reinterpret_cast<uint4 *>(box)[i] = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+            }
+            __syncwarp();  // the zeroed boxes are written before the arrival below releases them
+            if (lane == 0) mbar_arrive_expect_tx(&bars.k_full[ks], (uint32_t)__popc(okmask) * 2048u);
+            __syncwarp();
+            if (ok) tma_load_4d(box, &kmap, &bars.k_full[ks], (kbox & 1) * 64, U.h, 0, kid);
+            k_issued = c + 1;
           }
-          load_vpages(smem + P_OFF_V + vs * 2 * kHalf, &vmap, &bars.v_full[vs], t, vb0, U.h, 0, npages, nullptr, bt, p,
-                      U.seq0, lane);
-          v_issued = c + 1;
+          {
+            const bool in = vpage < 8 && t * 8 + vpage < npages;  // (the softmax warps zero the rows past the prefix)
+            const bool ok = in && (unsigned)vid < (unsigned)p.num_blocks;
+            const unsigned okmask = __ballot_sync(FULL, ok);
+            if (c >= kPVStages && !mbar_wait(&bars.pv_done[vs], ((c - kPVStages) / kPVStages) & 1)) timed_out = true;
+            if (__any_sync(FULL, timed_out)) {
+              timed_out = true;
+              break;
+            }
+            uint8_t *box = smem + P_OFF_V + vs * 2 * kHalf + vpage * kVPage;
+            if (in && !ok) {
+              set_error(p.err, PA_ERR_RANGE, U.seq0);
+              for (int i = 0; i < kVPage / 16; ++i) reinterpret_cast<uint4 *>(box)[i] = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&bars.v_full[vs], (uint32_t)__popc(okmask) * (uint32_t)kVPage);
+            __syncwarp();
+            if (ok) tma_load_5d(box, &vmap, &bars.v_full[vs], 0, 0, 0, U.h, vid);
+            v_issued = c + 1;
+          }
         }
-        timed_out = __any_sync(FULL, timed_out);
       }
       if (timed_out) {  // a short, bounded chance for this warp's copies in flight to land
         if (lw == 0 && ui > 0) mbar_wait(&bars.q_full, (ui - 1) & 1, kWaitLimitNs / 8);
@@ -628,28 +684,8 @@ shared_join_kernel(const SharedParams sp, const DecodeParams p) {
   const int wf = pages ? worker_of(A, P, W) : 0;
   const int nfs = pages ? worker_of(A + pages - 1, P, W) - wf + 1 : 0;
   if (len == 0 && nfs <= 1) return;  // the suffix worker wrote the output
-  float M = -INFINITY, L = 0.f;
-  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int U = 4;  // pieces in flight
-  auto add = [&](const float2 (&ml)[U], const float4 (&o)[U]) {
-    float mx = M;
-#pragma unroll
-    for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
-    if (mx == -INFINITY) return;
-    const float f = ex2(M - mx);
-    L *= f;
-    O.x *= f, O.y *= f, O.z *= f, O.w *= f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float w = ex2(ml[u].x - mx);
-      L = fmaf(ml[u].y, w, L);
-      O.x = fmaf(o[u].x, w, O.x);
-      O.y = fmaf(o[u].y, w, O.y);
-      O.z = fmaf(o[u].z, w, O.z);
-      O.w = fmaf(o[u].w, w, O.w);
-    }
-    M = mx;
-  };
+  JoinState js;
+  constexpr int U = kJoinPieces;
   for (int f0 = 0; f0 < nfs; f0 += U) {
     float2 ml[U];
     float4 o[U];
@@ -663,7 +699,7 @@ shared_join_kernel(const SharedParams sp, const DecodeParams p) {
         o[u] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + slot * kHeadDim + 4 * quad));
       }
     }
-    add(ml, o);
+    js.add(ml, o);
   }
   if (len > 0) {
     const int seq0 = g ? pl.end[g - 1] : 0;
@@ -687,16 +723,11 @@ shared_join_kernel(const SharedParams sp, const DecodeParams p) {
             o[u] = __ldcg(reinterpret_cast<const float4 *>(sp.ws_o) + (slot * 32 + quad) * 128 + row);
           }
         }
-        add(ml, o);
+        js.add(ml, o);
       }
     }
   }
-  const float inv = 1.f / L;
-  T *op = reinterpret_cast<T *>(p.out) + ((int64_t)s * p.num_q_heads + h * G + gg) * kHeadDim + 4 * quad;
-  uint2 pk;
-  pk.x = Pack<T>::from_f2(O.x * inv, O.y * inv);
-  pk.y = Pack<T>::from_f2(O.z * inv, O.w * inv);
-  *reinterpret_cast<uint2 *>(op) = pk;
+  js.store(reinterpret_cast<T *>(p.out) + ((int64_t)s * p.num_q_heads + h * G + gg) * kHeadDim + 4 * quad);
 }
 
 template <typename T, int G>

@@ -18,8 +18,9 @@
 namespace pa {
 namespace {
 
-constexpr int kChunkKeys = 4096;
+constexpr int kChunkKeys = 2048;
 constexpr int kWeightThreads = 256;
+constexpr int kKeysPerThread = kChunkKeys / kWeightThreads;
 static_assert(kWeightThreads / 32 >= 8, "a warp per query head of a KV head");
 
 template <typename T, int G>
@@ -60,20 +61,60 @@ decode_weights_kernel(const DecodeParams p, const float *scores, const float *we
   const int s = item / hkv, h = item % hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t first = __ldg(p.meta + s), pages = __ldg(p.meta + s + 1) - first;
-  if (pages == 0) return;  // a bad length: reported, nothing written
+  const int ctx = __ldg(p.context_lens + s);
   const int64_t P = (int64_t)__ldg(p.meta + p.num_seqs) * hkv;
+  if (pages == 0) return;  // a bad length: reported, nothing written
   const int64_t W = P < p.num_workers ? P : p.num_workers;
   const int64_t A = (int64_t)hkv * first + (int64_t)h * pages;
   const int wf = worker_of(A, P, W), nf = worker_of(A + pages - 1, P, W) - wf + 1;
-  if (blockIdx.x == 0) {
-    if (warp < G) merge_fragments<T, G, 32>(p, s, h, warp, wf, nf, lane);
+  const int64_t slot0 = (int64_t)item + wf;
+  if (blockIdx.x == 0) {  // the outputs: warp -> head, lane -> its dims 4 lane ..
+    for (int g = warp; g < G; g += kWeightThreads / 32) {
+      JoinState js;
+      for (int f0 = 0; f0 < nf; f0 += kJoinPieces) {
+        float2 ml[kJoinPieces];
+        float4 o[kJoinPieces];
+#pragma unroll
+        for (int u = 0; u < kJoinPieces; ++u) {
+          ml[u] = make_float2(-INFINITY, 0.f);
+          o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (f0 + u < nf) {
+            const int64_t slot = (slot0 + f0 + u) * G + g;
+            ml[u] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml + slot * 2));
+            o[u] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + slot * kHeadDim + 4 * lane));
+          }
+        }
+        js.add(ml, o);
+      }
+      js.store(reinterpret_cast<T *>(p.out) + ((int64_t)s * p.num_q_heads + h * G + g) * kHeadDim + 4 * lane);
+    }
     return;
   }
-  const int ctx = __ldg(p.context_lens + s);
   const int j0 = ((int)blockIdx.x - 1) * kChunkKeys;
   if (j0 >= ctx) return;
+  // this thread's keys j0 + thread + 256 u: their scores and weights on the way first
+  const float *sc = scores + A * (kBlock * G);
+  const int64_t row = (int64_t)item * weights_stride;
+  constexpr int U = 4;  // keys in flight
+  static_assert(kKeysPerThread % U == 0, "whole batches");
+  float v[U][G], w[U];
+  auto fetch = [&](int b) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = j0 + (int)threadIdx.x + (b + u) * kWeightThreads;
+      w[u] = 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) v[u][g] = -INFINITY;
+      if (k < ctx) {
+        const float *page = sc + (int64_t)(k >> 4) * (kBlock * G) + (k & 15);
+#pragma unroll
+        for (int g = 0; g < G; ++g) v[u][g] = page[g * kBlock];
+        if (weights_in) w[u] = weights_in[row + k];
+      }
+    }
+  };
+  fetch(0);
   if (warp < G) {  // head `warp`: the row's maximum and sum over its fragments
-    const int64_t slot0 = (int64_t)item + wf;
     float m = -INFINITY, l = 0.f;
     for (int f = lane; f < nf; f += 32) {
       const float2 ml = *reinterpret_cast<const float2 *>(p.ws_ml + ((slot0 + f) * G + warp) * 2);
@@ -100,32 +141,16 @@ decode_weights_kernel(const DecodeParams p, const float *scores, const float *we
     m[g] = s_m[g];
     inv[g] = s_inv[g];
   }
-  const float *sc = scores + A * (kBlock * G);
-  const int64_t row = (int64_t)item * weights_stride;
-  const int j1 = min(ctx, j0 + kChunkKeys);
-  constexpr int U = 4;  // keys per thread in flight
-  for (int j = j0 + (int)threadIdx.x; j < j1; j += kWeightThreads * U) {
-    float v[U][G], w[U];
+#pragma unroll
+  for (int b = 0; b < kKeysPerThread; b += U) {
+    if (b) fetch(b);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = j + u * kWeightThreads;
-      w[u] = 0.f;
-      if (k < j1) {
-        if (weights_in) w[u] = weights_in[row + k];
-        const float *page = sc + (int64_t)(k >> 4) * (kBlock * G) + (k & 15);
+      const int k = j0 + (int)threadIdx.x + (b + u) * kWeightThreads;
+      float sum = 0.f;
 #pragma unroll
-        for (int g = 0; g < G; ++g) v[u][g] = page[g * kBlock];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = j + u * kWeightThreads;
-      if (k < j1) {
-        float sum = 0.f;
-#pragma unroll
-        for (int g = 0; g < G; ++g) sum = fmaf(exp2f(v[u][g] - m[g]), inv[g], sum);
-        weights_out[row + k] = w[u] + sum;
-      }
+      for (int g = 0; g < G; ++g) sum = fmaf(exp2f(v[u][g] - m[g]), inv[g], sum);
+      if (k < ctx) weights_out[row + k] = w[u] + sum;
     }
   }
 }
