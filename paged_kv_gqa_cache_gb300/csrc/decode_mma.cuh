@@ -31,52 +31,35 @@ enum DecodeForm {
   kFormScores = 1,  // every key's scores go to the workspace, every item becomes fragments
   kFormSuffix = 2   // the keys past a shared prefix; an item of a sequence with a prefix becomes fragments
 };
-struct FormArgs {
-  float *scores = nullptr;              // kFormScores: [page of the global numbering][G][16 keys], log2 domain
-  int32_t max_len = INT32_MAX;          // kFormScores: the longest sequence the workspace and the weights hold
-  const int32_t *group_end = nullptr;   // kFormSuffix: sequences before the end of group g, ascending [num_groups]
-  const int32_t *group_len = nullptr;   //   its shared prefix in tokens, a multiple of 16 (0: none)
-  int32_t num_groups = 0;               //   sequences behind the last group share nothing
-};
-
-// Tokens that sequence s shares with its group.
-__device__ __forceinline__ int shared_len(const FormArgs &fa, int s) {
-  int lo = 0, hi = fa.num_groups;  // the first group that ends behind s
+// The first of n ascending group ends behind sequence s (n: none).
+__device__ __forceinline__ int group_of(const int32_t *end, int n, int s) {
+  int lo = 0, hi = n;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (fa.group_end[mid] <= s) lo = mid + 1; else hi = mid;
+    if (end[mid] <= s) lo = mid + 1; else hi = mid;
   }
-  return lo < fa.num_groups ? fa.group_len[lo] : 0;
+  return lo;
 }
-
-// Pages of sequence s that the worker reads.
-template <int FORM>
-__device__ __forceinline__ int form_pages(const DecodeParams &p, const FormArgs &fa, int s, bool report) {
-  const int ctx = __ldg(p.context_lens + s);
-  bool ok = ctx >= 1 && ctx <= p.max_blocks_per_seq * kBlock;
-  int first = 0;
-  if constexpr (FORM == kFormScores) ok = ok && ctx <= fa.max_len;
-  if constexpr (FORM == kFormSuffix) {
-    first = shared_len(fa, s);
-    ok = ok && ctx >= first;
+struct FormArgs {
+  float *scores = nullptr;             // kFormScores: [page of the global numbering][G][16 keys], log2 domain
+  const int32_t *group_end = nullptr;  // kFormSuffix: sequences before the end of group g, ascending [num_groups]
+  const int32_t *group_len = nullptr;  //   the tokens that its sequences share, a multiple of 16 (0: none)
+  int32_t num_groups = 0;              //   sequences behind the last group share nothing
+  __device__ __forceinline__ int shared_len(int s) const {
+    const int g = group_of(group_end, num_groups, s);
+    return g < num_groups ? group_len[g] : 0;
   }
-  if (!ok) {
-    if (report) set_error(p.err, PA_ERR_RANGE, s);
-    return 0;
-  }
-  return (ctx + kBlock - 1) / kBlock - first / kBlock;
-}
+};
 
-// Exclusive prefix of pages over sequences into prefix[0 .. S], by NT threads
+// Exclusive prefix of pages(s) over sequences into prefix[0 .. n], by NT threads
 // (warp_tot: NT / 32 ints of shared memory).
-template <int NT, int FORM>
-__device__ void scan_form_pages(const DecodeParams &p, const FormArgs &fa, int32_t *prefix, int *warp_tot,
-                                bool report) {
-  const int n = p.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+template <int NT, typename Pages>
+__device__ void scan_pages_of(int n, int32_t *prefix, int *warp_tot, Pages pages) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int carry = 0;
   for (int s0 = 0; s0 < n; s0 += NT) {
     const int s = s0 + tid;
-    const int mine = s < n ? form_pages<FORM>(p, fa, s, report) : 0;
+    const int mine = s < n ? pages(s) : 0;
     int incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -276,17 +259,16 @@ struct SplitSmem16 {
 };
 
 // Worker w of W (as decode_split_worker): the pages [w P / W, (w + 1) P / W) of
-// the global numbering, by one warp with slot `slot` of the shared memory.
-// kmap, vmap: the pool's K and V in whole-page boxes, 128-byte swizzled.
-// Returns false if a wait gave up (reported).
-template <typename T, int G, int NWC, int FORM>
+// the global numbering, by one warp with kStages stages (1024-byte aligned) and
+// their barriers in shared memory of its own; prefix: the page prefix over
+// sequences.  kmap, vmap: the pool's K and V in whole-page boxes, 128-byte
+// swizzled.  Returns false if a wait gave up (reported).
+template <typename T, int G, int FORM>
 __device__ __forceinline__ bool split_worker16(const CUtensorMap &kmap, const CUtensorMap &vmap,
-                                               const DecodeParams &p, const FormArgs &fa, uint8_t *smem,
-                                               const int32_t *prefix, int slot, int64_t w, int64_t P, int64_t W) {
-  using Sm = SplitSmem16<NWC>;
+                                               const DecodeParams &p, const FormArgs &fa, uint8_t *stages,
+                                               uint64_t *bars, const int32_t *prefix, int64_t w, int64_t P,
+                                               int64_t W) {
   const int lane = threadIdx.x & 31;
-  uint8_t *stages = smem + Sm::kStagesOff + slot * kStages * STAGE;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Sm::kBarsOff) + slot * kStages;
   const int n = p.num_seqs, hkv = p.num_kv_heads;
   if (lane == 0) {
 #pragma unroll
@@ -307,7 +289,7 @@ __device__ __forceinline__ bool split_worker16(const CUtensorMap &kmap, const CU
     const int base = ic.page & ~31;
     if (ic.s != win_s || base != win_base) {
       if constexpr (FORM == kFormSuffix)
-        if (ic.s != win_s) win_first = shared_len(fa, ic.s) / kBlock;
+        if (ic.s != win_s) win_first = fa.shared_len(ic.s) / kBlock;
       win_s = ic.s;
       win_base = base;
       win = base + lane < ic.pages
@@ -348,7 +330,7 @@ __device__ __forceinline__ bool split_worker16(const CUtensorMap &kmap, const CU
       st16.m = -INFINITY;
       st16.l = 0.f;
       ctx = __ldg(p.context_lens + cc.s);
-      if constexpr (FORM == kFormSuffix) first = shared_len(fa, cc.s) / kBlock;
+      if constexpr (FORM == kFormSuffix) first = fa.shared_len(cc.s) / kBlock;
       whole = cc.page == 0;
       open = true;
     }

@@ -6,25 +6,30 @@
 // For online softmax states (m, l, o) over disjoint key sets the join is
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  o = sum o_i 2^(m_i - m),  out = o / l.
 //
-// Three kernels:
-//   prefix  The query rows of a group's sequences for one KV head (sequences x
-//           G rows) against the prefix is a matrix product: query tiles of 128
-//           rows, key tiles of 128 keys, on the tcgen05 tensor cores with the
-//           tile machinery of prefill_kernel.cuh (no causal mask).  One CTA per
-//           SM over an equal share of all (query tile, key tile) pairs; a
-//           piece of a query tile's keys leaves its state in the workspace.
-//           One query tile per KV head is bound by HBM (64 KB of K and V per
-//           0.78 us of tensor time, against 1.47 us of an SM's share of HBM),
-//           more by the tensor cores; then the key range is cut into blocks
-//           about as long as a CTA's share, the query tiles of a block next to
-//           each other in the order, so that the CTAs that need the same keys
-//           run at the same time and all but one of them read L2.
-//   suffix  The rest of each sequence by the split workers of decode_mma.cuh,
-//           two small CTAs per SM.  It does not read what the prefix kernel
-//           writes, so it starts as soon as SMs are free beside it (the prefix
-//           CTAs release their dependents once the work before them has ended)
-//           and waits for the prefix kernel only before it ends, so that the
-//           join, its dependent, runs after both.
+// Two kernels:
+//   shared  One CTA per SM; each has an equal share of the prefix work and of
+//           the rest.
+//           Prefix: the query rows of a group's sequences for one KV head
+//           (sequences x G rows) against the prefix are a matrix product: query
+//           tiles of 128 rows, key tiles of 128 keys, on the tcgen05 tensor cores
+//           with the tile machinery of prefill_kernel.cuh (no causal mask).  The
+//           (query tile, key tile) pairs are dealt evenly; a piece of a query
+//           tile's keys leaves its state in the workspace.  One query tile per KV
+//           head is bound by HBM (64 KB of K and V per 0.78 us of tensor time,
+//           against 1.47 us of an SM's share of HBM), more by the tensor cores;
+//           then the key range is cut into blocks about as long as a CTA's share,
+//           the query tiles of a block next to each other in the order, so that
+//           the CTAs that need the same keys run at the same time and all but one
+//           of them read L2.
+//           Suffix: the rest of each sequence, by the split workers of
+//           decode_mma.cuh on the 8 softmax warps.  Their stages (8 x 3 x 8 KB)
+//           take the very 192 KB of the query tile and the K and V rings, so a
+//           warp goes over to its pages as soon as its last query tile is
+//           stored.  (As a kernel of its own behind the prefix the suffix paid a
+//           launch, a schedule and a first trip to HBM, 57 us for 32 sequences
+//           and 32768 shared tokens; beside it on SMs of its own 54, but 139
+//           against 122 us where groups are large: its stream pushed the shared
+//           keys out of L2.)
 //   join    A warp per (sequence, KV head, part of the dims) adds up the pieces.
 #include "decode_mma.cuh"
 #include "prefill_kernel.cuh"
@@ -33,6 +38,7 @@ namespace pa {
 namespace {
 
 constexpr int kGroups = kMaxPrefixGroups;
+constexpr int kPhaseBarrier = 5;  // named barrier (4: the registers')
 constexpr int kPVStages = 2;
 constexpr int P_OFF_Q = 0;
 constexpr int P_OFF_K = 2 * kHalf;
@@ -44,9 +50,12 @@ struct PBars {
   uint64_t k_full[kKStages], s_full[kKStages];
   uint64_t v_full[kPVStages], p_full[kPVStages], pv_done[kPVStages];
   uint64_t x_full, o_free, drain;
+  uint64_t page[kSoftmaxWarps][kStages];  // the suffix workers' stages
   uint32_t tmem_base;
 };
-static_assert(sizeof(PBars) <= 256, "barriers");
+constexpr int kBarBytes = 512;
+static_assert(sizeof(PBars) <= kBarBytes, "barriers");
+static_assert(kSoftmaxWarps * kStages * STAGE <= P_OFF_X, "the suffix workers' stages fit the rings");
 
 // The groups and the order of the prefix work.  Group g: sequences end[g - 1]
 // .. end[g] - 1, len[g] shared tokens; its pairs start at pairs[g], its units
@@ -54,12 +63,28 @@ static_assert(sizeof(PBars) <= 256, "barriers");
 // at most `share` key tiles when the group has several query tiles, else all.
 struct SharedPlan {
   int32_t num_groups, share, ctas, total;  // total: pairs of all groups; ctas: the CTAs that share them
+  int32_t many;                            // a group has several query tiles
   int32_t end[kGroups], len[kGroups];
   int32_t pairs[kGroups + 1], units[kGroups + 1];
 };
+// What the join wants to know of a sequence.
+struct SeqRecord {
+  int32_t len, index, pairs, units;  // shared tokens; place in the group; the group's first pair and unit
+  int32_t kt, mt, blocks, blen;      // the group's shape
+};
+// The tables that one CTA leaves in the workspace for the join.
+struct SharedTables {
+  int32_t *head;       // [0] total, [1] ctas of the plan
+  SeqRecord *records;  // [num_seqs]
+};
+__host__ __device__ __forceinline__ SharedTables shared_tables(void *ws) {
+  uint8_t *b = static_cast<uint8_t *>(ws);
+  return {reinterpret_cast<int32_t *>(b), reinterpret_cast<SeqRecord *>(b + 16)};
+}
 constexpr int P_OFF_BAR = P_OFF_PLAN + ((int)sizeof(SharedPlan) + 127) / 128 * 128;
-constexpr int P_SMEM_BYTES = P_OFF_BAR + 256 + 1024;
-static_assert(P_SMEM_BYTES <= 232448, "shared memory");
+constexpr int P_OFF_PREFIX = P_OFF_BAR + kBarBytes;  // page prefix of the suffixes [num_seqs + 1]
+constexpr int P_SMEM_MAX = 232448;
+static_assert(P_OFF_PREFIX + (kSharedMaxSeqs + 1) * 4 + 1024 <= P_SMEM_MAX, "shared memory");
 
 struct GroupShape {
   int kt, mt, blocks, blen;  // key tiles, query tiles, key blocks per KV head, key tiles per block (the last: fewer)
@@ -75,38 +100,14 @@ __device__ __forceinline__ GroupShape group_shape(int size, int len, int share) 
   return s;
 }
 
-// Sum of `mine` over the threads before this one and, in carry, over all (NT
-// threads, all of them take part).
-template <int NT>
-__device__ __forceinline__ int scan_step(int mine, int &carry, int *warp_tot) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(FULL, incl, off);
-    if (lane >= off) incl += y;
-  }
-  if (lane == 31) warp_tot[warp] = incl;
-  __syncthreads();
-  int base = carry, total = 0;
-#pragma unroll
-  for (int i = 0; i < NT / 32; ++i) {
-    base += i < warp ? warp_tot[i] : 0;
-    total += warp_tot[i];
-  }
-  carry += total;
-  __syncthreads();
-  return base + incl - mine;
-}
-
-// Every group's end and shared length, as all kernels of the call understand
-// them.  A group with a bad size counts as empty; one with a bad length, with
-// a single sequence or that runs past the sequences shares nothing.  Reported if asked.
-template <int NT>
-__device__ void load_groups(const SharedParams &p, int32_t *end, int32_t *len, int *warp_tot, bool report) {
+// Every group's end and shared length (one warp).  A group with a bad size
+// counts as empty; one with a bad length, with a single sequence or that runs
+// past the sequences shares nothing.  Reported if asked.
+__device__ __forceinline__ void load_groups(const SharedParams &p, SharedPlan &pl, bool report) {
+  const int lane = threadIdx.x & 31;
   int carry = 0;
-  for (int g0 = 0; g0 < p.num_groups; g0 += NT) {
-    const int g = g0 + (int)threadIdx.x;
+  for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
+    const int g = g0 + lane;
     int size = 0, n = 0;
     bool bad = false;
     if (g < p.num_groups) {
@@ -118,44 +119,62 @@ __device__ void load_groups(const SharedParams &p, int32_t *end, int32_t *len, i
       if (bad_size) size = 0;
       if (bad_len || size < 2) n = 0;
     }
-    const int e = scan_step<NT>(size, carry, warp_tot) + size;
+    int e = size;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(FULL, e, off);
+      if (lane >= off) e += y;
+    }
+    e += carry;
+    carry = __shfl_sync(FULL, e, 31);
     if (g < p.num_groups) {
       const bool over = e > p.num_seqs;
       if (report && (bad || (over && size > 0))) set_error(p.err, PA_ERR_RANGE, g);
-      end[g] = min(e, p.num_seqs);
-      len[g] = over ? 0 : n;
+      pl.end[g] = min(e, p.num_seqs);
+      pl.len[g] = over ? 0 : n;
     }
   }
-  __syncthreads();
+  __syncwarp();
 }
 
-// The rest of the plan from the groups' ends and lengths in it.
-template <int G, int NT>
-__device__ void make_plan(SharedPlan &pl, int num_groups, int hkv, int grid, int *warp_tot) {
+// The rest of the plan from the groups' ends and lengths in it (one warp).
+template <int G>
+__device__ __forceinline__ void make_plan(SharedPlan &pl, int num_groups, int hkv, int grid) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int round = 0; round < 2; ++round) {  // the pairs, then (with the share known) the units
     int32_t *out = round ? pl.units : pl.pairs;
     int carry = 0;
-    for (int g0 = 0; g0 < num_groups; g0 += NT) {
-      const int g = g0 + (int)threadIdx.x;
+    bool many = false;
+    for (int g0 = 0; g0 < num_groups; g0 += 32) {
+      const int g = g0 + lane;
       int mine = 0;
       if (g < num_groups && pl.len[g] > 0) {
         const GroupShape s = group_shape<G>(pl.end[g] - (g ? pl.end[g - 1] : 0), pl.len[g], round ? pl.share : 1);
         mine = hkv * s.mt * (round ? s.blocks : s.kt);
+        many = many || s.mt > 1;
       }
-      const int before = scan_step<NT>(mine, carry, warp_tot);
-      if (g < num_groups) out[g] = before;
+      int incl = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(FULL, incl, off);
+        if (lane >= off) incl += y;
+      }
+      if (g < num_groups) out[g] = carry + incl - mine;
+      carry += __shfl_sync(FULL, incl, 31);
     }
-    if (threadIdx.x == 0) {
+    many = __any_sync(FULL, many);
+    if (lane == 0) {
       out[num_groups] = carry;
       if (!round) {
         pl.num_groups = num_groups;
         pl.total = carry;
         pl.ctas = carry < grid ? carry : grid;  // so that no share is empty
         pl.share = carry > 0 ? (carry + pl.ctas - 1) / pl.ctas : 1;
+        pl.many = many;
       }
     }
-    __syncthreads();
+    __syncwarp();
   }
 }
 
@@ -199,7 +218,7 @@ __device__ __forceinline__ PUnit punit_at(const SharedPlan &pl, int x, int x_end
   return u;
 }
 
-// ---- the prefix kernel ----
+// ---- the shared kernel ----
 // The roles of prefill_kernel.cuh, each looping over the CTA's runs of pairs
 // with a key-tile counter c that runs on across them: warps 0..7 softmax and
 // epilogue (the halves of a key tile never meet in the loop), warps 8..14
@@ -209,10 +228,14 @@ __device__ __forceinline__ PUnit punit_at(const SharedPlan &pl, int x, int x_end
 // P goes into P V rounded to the 16-bit type where a group has several query
 // tiles (tensor-bound), and in two terms where it has one (HBM-bound: the 8
 // more MMAs per key tile, 0.26 us, find the tensor core idle).
+// The softmax warps then are the suffix's split workers.  Where a group has
+// several query tiles, the upper half of the CTAs takes its suffix first, so
+// that tensor-bound and HBM-bound work run side by side.
 template <typename T, int G>
 __global__ void __launch_bounds__(kThreads, 1)
-shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                     const __grid_constant__ CUtensorMap qmap, const SharedParams sp, const PrefillParams p) {
+shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kpage,
+              const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap,
+              const SharedParams sp, const PrefillParams p, const DecodeParams dp) {
   constexpr int TQ = 128 / G;
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t IDESC_S = tc::idesc_f16(kBF16, 128, 128, false);
@@ -225,8 +248,9 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = (int)blockIdx.x;
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kThreads - 64) {
     tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&kpage);
     tma_prefetch_desc(&vmap);
     tma_prefetch_desc(&qmap);
     mbar_init(&bars.q_full, 1);
@@ -249,20 +273,57 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     tc::tmem_alloc(&bars.tmem_base, kTmemCols);
     tc::tmem_relinquish();
   }
-  // The plan, from the group metadata alone (like block tables and lengths it is
-  // read before the dependency wait), the same in every CTA.
-  load_groups<kThreads>(sp, pl.end, pl.len, warp_tot, b == 0);
-  make_plan<G, kThreads>(pl, sp.num_groups, sp.num_kv_heads, (int)gridDim.x, warp_tot);
+  // The plan and the page prefix of the suffixes, from the group metadata and the
+  // lengths (like block tables they are read before the dependency wait), the same
+  // in every CTA.  The last CTA reports what is wrong.
+  const bool scribe = b == (int)gridDim.x - 1;
+  int32_t *prefix = reinterpret_cast<int32_t *>(smem + P_OFF_PREFIX);
+  if (warp == 0) load_groups(sp, pl, scribe);
+  __syncthreads();
+  if (warp == 0) make_plan<G>(pl, sp.num_groups, sp.num_kv_heads, (int)gridDim.x);
+  scan_pages_of<kThreads>(sp.num_seqs, prefix, warp_tot, [&](int s) {
+    const int ctx = __ldg(dp.context_lens + s);
+    const int g = group_of(pl.end, sp.num_groups, s), len = g < sp.num_groups ? pl.len[g] : 0;
+    if (ctx >= 1 && ctx <= sp.max_blocks_per_seq * kBlock && ctx >= len)
+      return (ctx + kBlock - 1) / kBlock - len / kBlock;
+    if (scribe) set_error(sp.err, PA_ERR_RANGE, s);
+    return 0;
+  });
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = bars.tmem_base;
   const int x0 = share_start(b, pl.total, pl.ctas), x1 = share_start(b + 1, pl.total, pl.ctas);
+  const bool suffix_first = pl.many && 2 * b >= (int)gridDim.x;
   bool timed_out = false;
 
   if (warp < kSoftmaxWarps) {
     regs_inc<kRegsSoftmax>();
     regs_taken();
+    griddep_wait();
+#pragma unroll 1
+    for (int phase = 0; phase < 2; ++phase) {
+    if ((phase == 0) == suffix_first) {
+      // ---------------- the suffix: this warp's pages ----------------
+      // Worker numbers run from the last CTA down: with few pairs and pages the
+      // CTAs without pairs take the pages.  The rings are idle: every copy was
+      // consumed by an MMA, and the last P V, which this warp saw complete, came
+      // after all of them (or, suffix first, nothing has been copied yet).
+      const int64_t P = (int64_t)prefix[sp.num_seqs] * sp.num_kv_heads;
+      const int64_t W0 = (int64_t)gridDim.x * kSoftmaxWarps, W = P < W0 ? P : W0;
+      const int64_t w = (int64_t)((int)gridDim.x - 1 - b) * kSoftmaxWarps + warp;
+      if (w < W && !timed_out) {
+        FormArgs fa;
+        fa.group_end = pl.end;
+        fa.group_len = pl.len;
+        fa.num_groups = sp.num_groups;
+        if (!split_worker16<T, G, kFormSuffix>(kpage, vmap, dp, fa, smem + warp * (kStages * STAGE), bars.page[warp],
+                                               prefix, w, P, W))
+          timed_out = true;
+      }
+      if (suffix_first) named_barrier(kPhaseBarrier, kThreads);  // the rings are the loaders' again
+      continue;
+    }
     // ---------------- softmax + epilogue (warps 0..7), run after run ----------------
     const int quad = warp & 3, ch = warp >> 2;
     const int r = quad * 32 + lane;
@@ -407,10 +468,12 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         if (ch == 0) sp.ws_ml[slot * 128 + r] = make_float2(M, l0 * f0 + l1 * f1);
       }
     }
+    }
     regs_dec<128>();
   } else {
     // every loader and MMA warp runs this one decrease (setmaxnreg acts on whole warpgroups)
     regs_dec<kRegsOther>();
+    if (suffix_first) named_barrier(kPhaseBarrier, kThreads);
     if (warp != kWarpMma) {
       // ---------------- loader warps ----------------
       // Boxes lw, lw + 7, .. of a key tile's 16 K boxes (the 64-dim half b % 2 of
@@ -438,12 +501,26 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         open_run(U);
       }
       griddep_wait();  // Q, K and V may come from the kernels before
-      // The suffix kernel may start: the work before this kernel has ended, and
-      // it reads nothing that this kernel writes.
-      griddep_launch_dependents();
-      if (b == 0)  // the join's copy of the plan (after the wait: the previous call's join may still read it)
-        for (int i = lw * 32 + lane; i < (int)(sizeof(SharedPlan) / 4); i += kLoadWarps * 32)
-          reinterpret_cast<int32_t *>(sp.plan)[i] = reinterpret_cast<const int32_t *>(&pl)[i];
+      if (scribe) {  // the join's tables (after the wait: the previous call's join may still read them)
+        const SharedTables tb = shared_tables(sp.tables);
+        const int i0 = lw * 32 + lane;
+        if (i0 == 0) {
+          tb.head[0] = pl.total;
+          tb.head[1] = pl.ctas;
+        }
+        for (int i = i0; i <= sp.num_seqs; i += kLoadWarps * 32) {
+          dp.meta[i] = prefix[i];
+          if (i == sp.num_seqs) break;
+          SeqRecord r = {};
+          const int g = group_of(pl.end, sp.num_groups, i);
+          if (g < sp.num_groups && pl.len[g] > 0) {
+            const int seq0 = g ? pl.end[g - 1] : 0;
+            const GroupShape sh = group_shape<G>(pl.end[g] - seq0, pl.len[g], pl.share);
+            r = {pl.len[g], i - seq0, pl.pairs[g], pl.units[g], sh.kt, sh.mt, sh.blocks, sh.blen};
+          }
+          tb.records[i] = r;
+        }
+      }
       int c = 0, ui = 0, k_issued = 0, v_issued = 0;
       for (int x = x0; x < x1 && !timed_out; ++ui) {
         if (ui > 0) {
@@ -617,39 +694,6 @@ shared_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
   }
 }
 
-// ---- the suffix kernel ----
-template <typename T, int G>
-__global__ void __launch_bounds__(NW * 32, 2)
-shared_suffix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                     const SharedParams sp, const DecodeParams p) {
-  using Sm = SplitSmem16<NW>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ int warp_tot[NW];
-  __shared__ int32_t g_end[kGroups], g_len[kGroups];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int32_t *prefix = reinterpret_cast<int32_t *>(smem + Sm::kPrefixOff);
-  if (threadIdx.x == 0) {
-    tma_prefetch_desc(&kmap);
-    tma_prefetch_desc(&vmap);
-  }
-  load_groups<NW * 32>(sp, g_end, g_len, warp_tot, false);
-  FormArgs fa;
-  fa.group_end = g_end;
-  fa.group_len = g_len;
-  fa.num_groups = sp.num_groups;
-  scan_form_pages<NW * 32, kFormSuffix>(p, fa, prefix, warp_tot, blockIdx.x == 0);
-  const int64_t P = (int64_t)prefix[p.num_seqs] * p.num_kv_heads;
-  const int64_t W = P < p.num_workers ? P : p.num_workers;
-  const int w = blockIdx.x * NW + warp;
-  // Every prefix CTA has seen the work before it end, or this kernel would not
-  // run: q, the pool and the workspace are ready.
-  if (blockIdx.x == 0 && warp == 0)
-    for (int i = lane; i <= p.num_seqs; i += 32) p.meta[i] = prefix[i];
-  if (w < W) split_worker16<T, G, NW, kFormSuffix>(kmap, vmap, p, fa, smem, prefix, warp, w, P, W);
-  griddep_wait();  // this kernel's end then implies the prefix kernel's: the join needs both
-}
-
 // ---- the join ----
 // Warp (s, h, part): lane (gg, quad) adds up head gg's dims 4 quad .. 4 quad +
 // 3 over the pieces of the prefix and of the suffix.
@@ -657,30 +701,25 @@ template <typename T, int G>
 __global__ void __launch_bounds__(128)
 shared_join_kernel(const SharedParams sp, const DecodeParams p) {
   constexpr int TQ = 128 / G, QW = 32 / G;  // dim quads per warp
-  __shared__ SharedPlan pl;
   griddep_wait();
-  for (int i = threadIdx.x; i < (int)(sizeof(SharedPlan) / 4); i += 128)
-    reinterpret_cast<int32_t *>(&pl)[i] = __ldcg(reinterpret_cast<const int32_t *>(sp.plan) + i);
-  __syncthreads();
   const int wid = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int hkv = p.num_kv_heads;
   if (wid >= p.num_seqs * hkv * G) return;
   const int part = wid % G, item = wid / G, s = item / hkv, h = item % hkv;
   const int gg = lane % G, quad = part * QW + lane / G;
-  const int ctx = __ldg(p.context_lens + s);
-  // the group of s
-  int lo = 0, hi = pl.num_groups;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pl.end[mid] <= s) lo = mid + 1; else hi = mid;
-  }
-  const int g = lo, len = g < pl.num_groups ? pl.len[g] : 0;
+  const SharedTables tb = shared_tables(sp.tables);
+  const int4 ra = __ldcg(reinterpret_cast<const int4 *>(tb.records + s));
+  const int4 rb = __ldcg(reinterpret_cast<const int4 *>(tb.records + s) + 1);
+  const SeqRecord rec = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
+  const int2 head = __ldcg(reinterpret_cast<const int2 *>(tb.head));
+  const int ctx = __ldg(p.context_lens + s), len = rec.len;
+  const int m0 = __ldcg(p.meta + s), m1 = __ldcg(p.meta + s + 1), mn = __ldcg(p.meta + p.num_seqs);
   if (ctx < 1 || ctx > p.max_blocks_per_seq * kBlock || ctx < len) return;  // reported; its rows are left
   // the suffix's pieces: slots item + wf ..
-  const int pages = __ldcg(p.meta + s + 1) - __ldcg(p.meta + s);
-  const int64_t P = (int64_t)__ldcg(p.meta + p.num_seqs) * hkv;
+  const int pages = m1 - m0;
+  const int64_t P = (int64_t)mn * hkv;
   const int64_t W = P < p.num_workers ? P : p.num_workers;
-  const int64_t A = (int64_t)hkv * __ldcg(p.meta + s) + (int64_t)h * pages;
+  const int64_t A = (int64_t)hkv * m0 + (int64_t)h * pages;
   const int wf = pages ? worker_of(A, P, W) : 0;
   const int nfs = pages ? worker_of(A + pages - 1, P, W) - wf + 1 : 0;
   if (len == 0 && nfs <= 1) return;  // the suffix worker wrote the output
@@ -702,14 +741,12 @@ shared_join_kernel(const SharedParams sp, const DecodeParams p) {
     js.add(ml, o);
   }
   if (len > 0) {
-    const int seq0 = g ? pl.end[g - 1] : 0;
-    const GroupShape sh = group_shape<G>(pl.end[g] - seq0, len, pl.share);
-    const int mt = (s - seq0) / TQ, row = ((s - seq0) % TQ) * G + gg;
-    for (int j = 0; j < sh.blocks; ++j) {
-      const int bl = min(sh.blen, sh.kt - j * sh.blen);
-      const int xa = pl.pairs[g] + (h * sh.kt + j * sh.blen) * sh.mt + mt * bl;  // the unit's first pair
-      const int unit = pl.units[g] + (h * sh.blocks + j) * sh.mt + mt;
-      const int ff = share_owner(xa, pl.total, pl.ctas), fl = share_owner(xa + bl - 1, pl.total, pl.ctas);
+    const int mt = rec.index / TQ, row = (rec.index % TQ) * G + gg;
+    for (int j = 0; j < rec.blocks; ++j) {
+      const int bl = min(rec.blen, rec.kt - j * rec.blen);
+      const int xa = rec.pairs + (h * rec.kt + j * rec.blen) * rec.mt + mt * bl;  // the unit's first pair
+      const int unit = rec.units + (h * rec.blocks + j) * rec.mt + mt;
+      const int ff = share_owner(xa, head.x, head.y), fl = share_owner(xa + bl - 1, head.x, head.y);
       for (int f0 = ff; f0 <= fl; f0 += U) {
         float2 ml[U];
         float4 o[U];
@@ -734,20 +771,13 @@ template <typename T, int G>
 cudaError_t launch_shared_typed(const SharedParams &sp, const PrefillParams &pp, const DecodeParams &dp0,
                                 const CUtensorMap *maps, int sms, cudaStream_t stream) {
   DecodeParams dp = dp0;
-  static KernelSetup prefix_setup, suffix_setup;
-  cudaError_t e = kernel_setup(prefix_setup, shared_prefix_kernel<T, G>, P_SMEM_BYTES, kThreads, nullptr);
+  static KernelSetup setup;
+  const int smem = 1024 + P_OFF_PREFIX + (dp.num_seqs + 1) * 4;
+  cudaError_t e = kernel_setup(setup, shared_kernel<T, G>, smem, kThreads, nullptr);
   if (e != cudaSuccess) return e;
-  const int smem = 1024 + SplitSmem16<NW>::kPrefixOff + (dp.num_seqs + 1) * 4;
-  int per_sm = 0;
-  e = kernel_setup(suffix_setup, shared_suffix_kernel<T, G>, smem, NW * 32, &per_sm);
-  if (e != cudaSuccess) return e;
-  int grid = sms * per_sm;
-  if (grid * NW > kDecodeMaxWorkers) grid = kDecodeMaxWorkers / NW;
-  dp.num_workers = grid * NW;
-  e = launch_pdl(shared_prefix_kernel<T, G>, dim3(sms), dim3(kThreads), P_SMEM_BYTES, stream, maps[0], maps[1],
-                 maps[2], sp, pp);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(shared_suffix_kernel<T, G>, dim3(grid), dim3(NW * 32), smem, stream, maps[3], maps[4], sp, dp);
+  dp.num_workers = sms * kSoftmaxWarps;
+  e = launch_pdl(shared_kernel<T, G>, dim3(sms), dim3(kThreads), smem, stream, maps[0], maps[1], maps[2], maps[3], sp,
+                 pp, dp);
   if (e != cudaSuccess) return e;
   return launch_pdl(shared_join_kernel<T, G>, dim3((dp.num_seqs * dp.num_q_heads + 3) / 4), dim3(128), 0, stream, sp,
                     dp);
@@ -757,7 +787,7 @@ cudaError_t launch_shared_typed(const SharedParams &sp, const PrefillParams &pp,
 
 namespace {
 struct SharedLayout {
-  size_t plan, decode, ml, o, total;
+  size_t tables, decode, ml, o, total;
 };
 SharedLayout shared_layout(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int sms) {
   const size_t group = num_q_heads / num_kv_heads;
@@ -766,8 +796,8 @@ SharedLayout shared_layout(int num_seqs, int num_groups, int num_q_heads, int nu
   const size_t slots = 2 * (size_t)sms + tiles;
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   SharedLayout l;
-  l.plan = 0;
-  l.decode = up(sizeof(SharedPlan));
+  l.tables = 0;
+  l.decode = up(16 + (size_t)num_seqs * sizeof(SeqRecord));
   l.ml = l.decode + up(decode_workspace_counters_offset(num_seqs, num_q_heads, num_kv_heads));
   l.o = l.ml + up(slots * 128 * sizeof(float2));
   l.total = l.o + slots * 128 * kHeadDim * sizeof(float);
@@ -783,7 +813,7 @@ cudaError_t launch_decode_shared(SharedParams sp, const PrefillParams &pp, Decod
                                  const CUtensorMap *maps, int dtype, int group, int sms, cudaStream_t stream) {
   const SharedLayout l = shared_layout(dp.num_seqs, sp.num_groups, dp.num_q_heads, dp.num_kv_heads, sms);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  sp.plan = ws + l.plan;
+  sp.tables = ws + l.tables;
   sp.ws_ml = reinterpret_cast<float2 *>(ws + l.ml);
   sp.ws_o = reinterpret_cast<float *>(ws + l.o);
   decode_workspace_carve(ws + l.decode, SIZE_MAX, dp.num_seqs, dp.num_q_heads, dp.num_kv_heads, dp);

@@ -39,15 +39,22 @@ decode_scores_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
   }
   FormArgs fa;
   fa.scores = scores;
-  fa.max_len = max_len;
   griddep_wait();
-  scan_form_pages<NW * 32, kFormScores>(p, fa, prefix, warp_tot, blockIdx.x == 0);
+  scan_pages_of<NW * 32>(p.num_seqs, prefix, warp_tot, [&](int s) {
+    const int ctx = __ldg(p.context_lens + s);
+    if (ctx >= 1 && ctx <= p.max_blocks_per_seq * kBlock && ctx <= max_len) return (ctx + kBlock - 1) / kBlock;
+    if (blockIdx.x == 0) set_error(p.err, PA_ERR_RANGE, s);
+    return 0;
+  });
   const int64_t P = (int64_t)prefix[p.num_seqs] * p.num_kv_heads;
   const int64_t W = P < p.num_workers ? P : p.num_workers;
   const int w = blockIdx.x * NW + warp;
   if (blockIdx.x == 0 && warp == 0)  // for the pass that joins the fragments
     for (int i = lane; i <= p.num_seqs; i += 32) p.meta[i] = prefix[i];
-  if (w < W) split_worker16<T, G, NW, kFormScores>(kmap, vmap, p, fa, smem, prefix, warp, w, P, W);
+  if (w < W)
+    split_worker16<T, G, kFormScores>(kmap, vmap, p, fa, smem + Sm::kStagesOff + warp * kStages * STAGE,
+                                      reinterpret_cast<uint64_t *>(smem + Sm::kBarsOff) + warp * kStages, prefix, w,
+                                      P, W);
   griddep_launch_dependents();
 }
 

@@ -831,10 +831,6 @@ pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, const pa
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
-namespace {
-constexpr int kSharedMaxSeqs = 6000;  // the suffix kernel's page prefix in shared memory
-}
-
 size_t pa_decode_shared_workspace_bytes(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
                                         int32_t num_kv_heads) {
   if (num_seqs < 0 || num_seqs > kSharedMaxSeqs || num_groups < 0 || num_groups > kMaxPrefixGroups ||
@@ -867,11 +863,11 @@ pa_status pa_paged_attn_decode_shared(const void *q, const pa_kv_pool *pool, con
   if ((st = device_state(&d)) != PA_OK) return st;  // also readies the tensor-map encoder
   if (workspace_bytes < shared_workspace_bytes(num_seqs, num_groups, num_q_heads, pool->num_kv_heads, d->sm_count))
     return PA_ERR_WORKSPACE;
-  CUtensorMap maps[5];
-  if (!pool_map(&maps[0], pool, pool->k_cache, false) || !pool_map_vpages(&maps[1], pool, pool->v_cache) ||
-      !query_map(&maps[2], q, pool->dtype, num_q_heads, num_seqs, group) || !pool_map_vpages(&maps[3], pool, pool->k_cache))
+  CUtensorMap maps[4];
+  if (!pool_map(&maps[0], pool, pool->k_cache, false) || !pool_map_vpages(&maps[1], pool, pool->k_cache) ||
+      !pool_map_vpages(&maps[2], pool, pool->v_cache) ||
+      !query_map(&maps[3], q, pool->dtype, num_q_heads, num_seqs, group))
     return PA_ERR_CUDA;
-  maps[4] = maps[1];
   SharedParams sp{};
   sp.group_sizes = group_sizes;
   sp.prefix_lens = prefix_lens;

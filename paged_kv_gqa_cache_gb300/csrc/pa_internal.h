@@ -264,6 +264,7 @@ cudaError_t launch_prefill8(const PrefillParams &p, const CUtensorMap &kmap, con
 
 // ---- decode over prefixes shared by groups of sequences (16-bit pools) -----------
 constexpr int kMaxPrefixGroups = 256;
+constexpr int kSharedMaxSeqs = 6000;  // their page prefix in shared memory
 struct SharedParams {
   const int32_t *group_sizes;   // [num_groups]
   const int32_t *prefix_lens;   // [num_groups]
@@ -272,13 +273,12 @@ struct SharedParams {
   int32_t num_kv_heads;
   int32_t max_blocks_per_seq;
   int *err;
-  void *plan;                   // workspace: the prefix kernel's plan, for the join
+  void *tables;                 // workspace: per sequence, what the join needs
   float2 *ws_ml;                //   per prefix piece and row: (max, sum)
   float *ws_o;                  //   per prefix piece: [dims / 4][128 rows][4] unnormalised outputs
 };
 size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int sms);
-// maps: K (2 KB half boxes), V (4 KB pages) and q for the prefix, K and V (4 KB
-// swizzled pages) for the suffix.
+// maps: K in 2 KB half boxes (prefix), K in 4 KB pages (suffix), V in 4 KB pages, q.
 cudaError_t launch_decode_shared(SharedParams sp, const PrefillParams &pp, DecodeParams dp, void *workspace,
                                  const CUtensorMap *maps, int dtype, int group, int sms, cudaStream_t stream);
 
