@@ -39,15 +39,19 @@ namespace {
 
 constexpr int kGroups = kMaxPrefixGroups;
 constexpr int kPhaseBarrier = 5;  // named barrier (4: the registers')
-constexpr int kPVStages = 2;
+// Two stages of K and three of V: a K tile is free again once S is computed, a V
+// tile only after the softmax and P V (K 3 and V 2, both issued in one order by
+// the same warps, left 1.9 us between key tiles where HBM's share is 1.5).
+constexpr int kPKStages = 2, kPVStages = 3;
+constexpr int kKLoad = 4, kVLoad = kLoadWarps - kKLoad;  // loader warps of each
 constexpr int P_OFF_Q = 0;
 constexpr int P_OFF_K = 2 * kHalf;
-constexpr int P_OFF_V = P_OFF_K + kKStages * 2 * kHalf;
+constexpr int P_OFF_V = P_OFF_K + kPKStages * 2 * kHalf;
 constexpr int P_OFF_X = P_OFF_V + kPVStages * 2 * kHalf;  // (m, l) exchange [unit parity][half][128]
 constexpr int P_OFF_PLAN = P_OFF_X + 2 * 2 * 128 * 8;
 struct PBars {
   uint64_t q_full, q_free;
-  uint64_t k_full[kKStages], s_full[kKStages];
+  uint64_t k_full[kPKStages], s_full[kPKStages];
   uint64_t v_full[kPVStages], p_full[kPVStages], pv_done[kPVStages];
   uint64_t x_full, o_free, drain;
   uint64_t page[kSoftmaxWarps][kStages];  // the suffix workers' stages
@@ -255,12 +259,12 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     tma_prefetch_desc(&qmap);
     mbar_init(&bars.q_full, 1);
     mbar_init(&bars.q_free, 1);
-    for (int i = 0; i < kKStages; ++i) {
-      mbar_init(&bars.k_full[i], kLoadWarps);
+    for (int i = 0; i < kPKStages; ++i) {
+      mbar_init(&bars.k_full[i], kKLoad);
       mbar_init(&bars.s_full[i], 1);
     }
     for (int i = 0; i < kPVStages; ++i) {
-      mbar_init(&bars.v_full[i], kLoadWarps);
+      mbar_init(&bars.v_full[i], kVLoad);
       mbar_init(&bars.p_full[i], kSoftmaxThreads);
       mbar_init(&bars.pv_done[i], 1);
     }
@@ -337,8 +341,8 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       const int span = U.len - 1;
       float m_ref = -INFINITY, l = 0.f;
       for (int kt = U.ka; kt < U.kb; ++kt, ++c) {
-        const int sb = c & 1, ks = c % kKStages, vs = c % kPVStages;
-        if (!mbar_wait(&bars.s_full[ks], (c / kKStages) & 1)) {
+        const int sb = c & 1, ks = c % kPKStages, vs = c % kPVStages;
+        if (!mbar_wait(&bars.s_full[ks], (c / kPKStages) & 1)) {
           timed_out = true;
           break;
         }
@@ -476,12 +480,15 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     if (suffix_first) named_barrier(kPhaseBarrier, kThreads);
     if (warp != kWarpMma) {
       // ---------------- loader warps ----------------
-      // Boxes lw, lw + 7, .. of a key tile's 16 K boxes (the 64-dim half b % 2 of
-      // page b / 2) and pages (lw + 5) % 7, + 7 of V, issued from parallel lanes.
-      // The block ids of 4 key tiles sit one per lane, the next 4 tiles' already
-      // on their way: a table read per tile would hold up every copy by an L2 trip.
+      // Warps 0 .. 3 load K, each 4 of a key tile's 16 boxes (the 64-dim half b %
+      // 2 of page b / 2), warps 4 .. 6 V, pages lw - 4, + 3, .., from parallel
+      // lanes.  The block ids of 4 key tiles sit one per lane, the next 4 tiles'
+      // already on their way: a table read per tile would hold up every copy by
+      // an L2 trip.
       const int lw = warp - kWarpLoad0;
-      const int kbox = lw + kLoadWarps * lane, vpage = (lw + 5) % kLoadWarps + kLoadWarps * lane;
+      const bool for_k = lw < kKLoad;
+      const int box = for_k ? lw + kKLoad * lane : lw - kKLoad + kVLoad * lane;
+      const int boxes = for_k ? 16 : 8, page = for_k ? box >> 1 : box;
       const int32_t *bt = nullptr;
       int npages = 0, wbase = 0;
       int32_t win = -1, win_next = -1;
@@ -493,7 +500,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         win = ids_from(wbase);
         win_next = ids_from(wbase + 32);
       };
-      // The id of the key tile's page (every lane; -1 past the prefix), and whether it can be read.
+      // The id of a key tile's page (every lane; -1 past the prefix).
       auto id_of = [&](int t, int page) { return __shfl_sync(FULL, win, (t * 8 + page - wbase) & 31); };
       PUnit U;
       if (x0 < x1) {
@@ -521,7 +528,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           tb.records[i] = r;
         }
       }
-      int c = 0, ui = 0, k_issued = 0, v_issued = 0;
+      int c = 0, ui = 0, issued = 0;
       for (int x = x0; x < x1 && !timed_out; ++ui) {
         if (ui > 0) {
           U = punit_at<G>(pl, x, x1);
@@ -537,63 +544,50 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         timed_out = __any_sync(FULL, timed_out);
         for (int t = U.ka; t < U.kb && !timed_out; ++t, ++c) {
-          const int ks = c % kKStages, vs = c % kPVStages;
           if (t * 8 >= wbase + 32) {
             wbase += 32;
             win = win_next;
             win_next = ids_from(wbase + 32);
           }
-          const int kid = id_of(t, kbox >> 1), vid = id_of(t, vpage);
-          {
-            const bool in = kbox < 16 && t * 8 + (kbox >> 1) < npages;
-            const bool ok = in && (unsigned)kid < (unsigned)p.num_blocks;
-            const unsigned okmask = __ballot_sync(FULL, ok);
-            if (c >= kKStages && !mbar_wait(&bars.s_full[ks], ((c - kKStages) / kKStages) & 1)) timed_out = true;
-            if (__any_sync(FULL, timed_out)) {
-              timed_out = true;
-              break;
-            }
-            uint8_t *box = smem + P_OFF_K + ks * 2 * kHalf + (kbox & 1) * kHalf + (kbox >> 1) * 2048;
-            if (in && !ok) {  // rare: keep the products finite
-              if ((kbox & 1) == 0) set_error(p.err, PA_ERR_RANGE, U.seq0);
-              for (int i = 0; i < 128; ++i) reinterpret_cast<uint4 *>(box)[i] = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-            }
-            __syncwarp();  // the zeroed boxes are written before the arrival below releases them
-            if (lane == 0) mbar_arrive_expect_tx(&bars.k_full[ks], (uint32_t)__popc(okmask) * 2048u);
-            __syncwarp();
-            if (ok) tma_load_4d(box, &kmap, &bars.k_full[ks], (kbox & 1) * 64, U.h, 0, kid);
-            k_issued = c + 1;
+          const int id = id_of(t, page);
+          const bool in = box < boxes && t * 8 + page < npages;  // (the softmax warps zero V past the prefix)
+          const bool ok = in && (unsigned)id < (unsigned)p.num_blocks;
+          const unsigned okmask = __ballot_sync(FULL, ok);
+          const int st = for_k ? c % kPKStages : c % kPVStages;
+          // the stage is free: S of the key tile two before, P V of the one three before
+          if (for_k ? c >= kPKStages && !mbar_wait(&bars.s_full[st], ((c - kPKStages) / kPKStages) & 1)
+                    : c >= kPVStages && !mbar_wait(&bars.pv_done[st], ((c - kPVStages) / kPVStages) & 1))
+            timed_out = true;
+          if (__any_sync(FULL, timed_out)) {
+            timed_out = true;
+            break;
           }
-          {
-            const bool in = vpage < 8 && t * 8 + vpage < npages;  // (the softmax warps zero the rows past the prefix)
-            const bool ok = in && (unsigned)vid < (unsigned)p.num_blocks;
-            const unsigned okmask = __ballot_sync(FULL, ok);
-            if (c >= kPVStages && !mbar_wait(&bars.pv_done[vs], ((c - kPVStages) / kPVStages) & 1)) timed_out = true;
-            if (__any_sync(FULL, timed_out)) {
-              timed_out = true;
-              break;
-            }
-            uint8_t *box = smem + P_OFF_V + vs * 2 * kHalf + vpage * kVPage;
-            if (in && !ok) {
-              set_error(p.err, PA_ERR_RANGE, U.seq0);
-              for (int i = 0; i < kVPage / 16; ++i) reinterpret_cast<uint4 *>(box)[i] = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&bars.v_full[vs], (uint32_t)__popc(okmask) * (uint32_t)kVPage);
-            __syncwarp();
-            if (ok) tma_load_5d(box, &vmap, &bars.v_full[vs], 0, 0, 0, U.h, vid);
-            v_issued = c + 1;
+          const uint32_t bytes = for_k ? 2048u : (uint32_t)kVPage;
+          uint8_t *dst = for_k ? smem + P_OFF_K + st * 2 * kHalf + (box & 1) * kHalf + page * 2048
+                               : smem + P_OFF_V + st * 2 * kHalf + page * kVPage;
+          uint64_t *bar = for_k ? &bars.k_full[st] : &bars.v_full[st];
+          if (in && !ok) {  // rare: keep the products finite
+            set_error(p.err, PA_ERR_RANGE, U.seq0);
+            for (uint32_t i = 0; i < bytes / 16; ++i) reinterpret_cast<uint4 *>(dst)[i] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
           }
+          __syncwarp();  // the zeroed boxes are written before the arrival below releases them
+          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(okmask) * bytes);
+          __syncwarp();
+          if (ok) {
+            if (for_k)
+              tma_load_4d(dst, &kmap, bar, (box & 1) * 64, U.h, 0, id);
+            else
+              tma_load_5d(dst, &vmap, bar, 0, 0, 0, U.h, id);
+          }
+          issued = c + 1;
         }
       }
       if (timed_out) {  // a short, bounded chance for this warp's copies in flight to land
         if (lw == 0 && ui > 0) mbar_wait(&bars.q_full, (ui - 1) & 1, kWaitLimitNs / 8);
-        for (int t = k_issued - kKStages > 0 ? k_issued - kKStages : 0; t < k_issued; ++t)
-          mbar_wait(&bars.k_full[t % kKStages], (t / kKStages) & 1, kWaitLimitNs / 8);
-        for (int t = v_issued - kPVStages > 0 ? v_issued - kPVStages : 0; t < v_issued; ++t)
-          mbar_wait(&bars.v_full[t % kPVStages], (t / kPVStages) & 1, kWaitLimitNs / 8);
+        const int n = for_k ? kPKStages : kPVStages;
+        for (int t = issued - n > 0 ? issued - n : 0; t < issued; ++t)
+          mbar_wait(for_k ? &bars.k_full[t % n] : &bars.v_full[t % n], (t / n) & 1, kWaitLimitNs / 8);
       }
     } else {
       // ---------------- MMA issuer (warp-uniform loop, one elected lane issues) ----------------
@@ -646,8 +640,8 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           break;
         }
         for (int kt = U.ka; kt < U.kb; ++kt, ++c) {
-          const int ks = c % kKStages;
-          if (!wait_all(&bars.k_full[ks], (c / kKStages) & 1)) {
+          const int ks = c % kPKStages;
+          if (!wait_all(&bars.k_full[ks], (c / kPKStages) & 1)) {
             timed_out = true;
             break;
           }
