@@ -143,17 +143,17 @@ __device__ __forceinline__ void decode_page16(uint32_t stage, int nv, const uint
   // lane l addresses row l % 8 of matrix l / 8: keys 8 (matrix / 2) .., chunk 2 step + matrix % 2
   const int mrow = lane & 7, mkey = ((lane >> 4) << 3) + mrow, mchunk = (lane >> 3) & 1;
   const uint32_t row = stage + mkey * 128;
-  float c[2][2][4] = {};
+  float c[2][4] = {};
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks) {
     uint32_t b[4];
     ldsm4(b, row + (ks >> 2) * 2048 + (((2 * (ks & 3) + mchunk) ^ mrow) << 4));
-    mma16<T>(c[0][ks & 1], qa[ks][0], 0u, qa[ks][1], 0u, b[0], b[1]);
-    mma16<T>(c[1][ks & 1], qa[ks][0], 0u, qa[ks][1], 0u, b[2], b[3]);
+    mma16<T>(c[0], qa[ks][0], 0u, qa[ks][1], 0u, b[0], b[1]);
+    mma16<T>(c[1], qa[ks][0], 0u, qa[ks][1], 0u, b[2], b[3]);
   }
   float s[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s[i] = (c[i >> 1][0][i & 1] + c[i >> 1][1][i & 1]) * scale_log2;
+  for (int i = 0; i < 4; ++i) s[i] = c[i >> 1][i & 1] * scale_log2;
   const bool full = nv == kBlock;  // (warp-uniform)
   if (!full) {
 #pragma unroll
@@ -249,43 +249,42 @@ struct JoinState {
   }
 };
 
-// Shared memory of NWC split workers: per warp kStages stages and their
-// barriers; then the page prefix (num_seqs + 1 ints).
-template <int NWC>
-struct SplitSmem16 {
-  static constexpr int kStagesOff = 0;
-  static constexpr int kBarsOff = NWC * kStages * STAGE;
-  static constexpr int kPrefixOff = kBarsOff + NWC * kStages * 8;
-};
-
+// ---- a split worker: a producer warp that fetches its pages, a consumer warp ----
 // Worker w of W (as decode_split_worker): the pages [w P / W, (w + 1) P / W) of
-// the global numbering, by one warp with kStages stages (1024-byte aligned) and
-// their barriers in shared memory of its own; prefix: the page prefix over
-// sequences.  kmap, vmap: the pool's K and V in whole-page boxes, 128-byte
-// swizzled.  Returns false if a wait gave up (reported).
-template <typename T, int G, int FORM>
-__device__ __forceinline__ bool split_worker16(const CUtensorMap &kmap, const CUtensorMap &vmap,
-                                               const DecodeParams &p, const FormArgs &fa, uint8_t *stages,
-                                               uint64_t *bars, const int32_t *prefix, int64_t w, int64_t P,
-                                               int64_t W) {
+// the global numbering, through a ring of kStages stages.  Two warps, because
+// one that did both spent 480 of its 2450 cycles a page on the cursor, the block
+// id and the two tensor copies.
+struct PageRing {
+  uint64_t full[kStages];  // the page landed (or cannot be read: bad)
+  uint64_t free[kStages];  // the consumer has read it
+  int32_t bad[kStages];
+};
+__device__ __forceinline__ void init_ring(PageRing &r) {  // one thread, before a barrier of both warps
+#pragma unroll
+  for (int st = 0; st < kStages; ++st) {
+    mbar_init(&r.full[st], 1);
+    mbar_init(&r.free[st], 1);
+  }
+}
+
+// kmap, vmap: the pool's K and V in whole-page boxes, 128-byte swizzled; stages:
+// kStages stages, 1024-byte aligned; prefix: the page prefix over sequences.
+// Returns false if a wait gave up (reported by the caller).
+template <int G, int FORM>
+__device__ __forceinline__ bool split_producer16(const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                                 const DecodeParams &p, const FormArgs fa, uint8_t *stages,
+                                                 PageRing &ring, const int32_t *prefix, int64_t w, int64_t P,
+                                                 int64_t W) {
   const int lane = threadIdx.x & 31;
   const int n = p.num_seqs, hkv = p.num_kv_heads;
-  if (lane == 0) {
-#pragma unroll
-    for (int st = 0; st < kStages; ++st) mbar_init(&bars[st], 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
   const int64_t x0 = w * P / W;
-  const int64_t npages = (w + 1) * P / W - x0;
+  const int npages = (int)((w + 1) * P / W - x0);
   Cursor ic = locate(prefix, n, hkv, x0);
-  Cursor cc = ic;
-
-  // ---- producer: lane 0 issues, every lane tracks the cursor and holds one of 32 block ids
   int win_s = -1, win_base = -1, win_first = 0;
-  int32_t win = -1;
-  uint32_t bad_mask = 0;
-  auto issue = [&](int st) {
+  int32_t win = -1;  // one of 32 block ids per lane
+  int st = 0, phase = 1;  // a fresh ring is free: the first waits pass
+  bool ok_all = true;
+  for (int x = 0; x < npages; ++x) {
     const int base = ic.page & ~31;
     if (ic.s != win_s || base != win_base) {
       if constexpr (FORM == kFormSuffix)
@@ -296,35 +295,58 @@ __device__ __forceinline__ bool split_worker16(const CUtensorMap &kmap, const CU
                 ? __ldg(p.block_tables + (int64_t)ic.s * p.max_blocks_per_seq + win_first + base + lane)
                 : -1;
     }
+    if (ic.page == 0 && x > 0 && lane < 2 * G) {  // a new item: its query rows towards L2, pages ahead of their use
+      const char *q = static_cast<const char *>(p.q) +
+                      ((int64_t)ic.s * p.num_q_heads + (int64_t)ic.h * G) * (kHeadDim * 2) + lane * 128;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+    }
     const int blk = __shfl_sync(FULL, win, ic.page & 31);
     const bool ok = (unsigned)blk < (unsigned)p.num_blocks;
+    if (!mbar_wait(&ring.free[st], phase)) ok_all = false;
+    if (!__all_sync(FULL, ok_all)) {  // give the copies still in flight a short, bounded chance to land
+      for (int y = x - kStages > 0 ? x - kStages : 0; y < x; ++y)
+        mbar_wait(&ring.full[y % kStages], (y / kStages) & 1, kWaitLimitNs / 8);
+      return false;
+    }
     if (lane == 0) {
+      ring.bad[st] = ok ? 0 : 1;
       if (ok) {
-        mbar_arrive_expect_tx(&bars[st], STAGE);
-        tma_load_5d(stages + st * STAGE, &kmap, &bars[st], 0, 0, 0, ic.h, blk);
-        tma_load_5d(stages + st * STAGE + STAGE / 2, &vmap, &bars[st], 0, 0, 0, ic.h, blk);
+        mbar_arrive_expect_tx(&ring.full[st], STAGE);
+        tma_load_5d(stages + st * STAGE, &kmap, &ring.full[st], 0, 0, 0, ic.h, blk);
+        tma_load_5d(stages + st * STAGE + STAGE / 2, &vmap, &ring.full[st], 0, 0, 0, ic.h, blk);
       } else {
         set_error(p.err, PA_ERR_RANGE, ic.s);
-        mbar_arrive(&bars[st]);
+        mbar_arrive(&ring.full[st]);
       }
     }
-    bad_mask = ok ? (bad_mask & ~(1u << st)) : (bad_mask | (1u << st));
+    __syncwarp();
     advance(ic, prefix, n, hkv);
-  };
-  const int npre = (int)(npages < kStages ? npages : kStages);
-  for (int g = 0; g < npre; ++g) issue(g);
+    if (++st == kStages) st = 0, phase ^= 1;
+  }
+  return true;
+}
 
-  // ---- consumer
+template <typename T, int G, int FORM>
+__device__ __forceinline__ bool split_consumer16(const DecodeParams &p, const FormArgs fa, const uint8_t *stages,
+                                                 PageRing &ring, const int32_t *prefix, int64_t w, int64_t P,
+                                                 int64_t W) {
+  const int lane = threadIdx.x & 31;
+  const int n = p.num_seqs, hkv = p.num_kv_heads;
+  const int64_t x0 = w * P / W;
+  const int npages = (int)((w + 1) * P / W - x0);
+  Cursor cc = locate(prefix, n, hkv, x0);
   uint32_t qa[8][2];
   Mma16 st16;
-  int ctx = 0, first = 0;
+  int ctx = 0, first = 0, st = 0, phase = 0;
   bool open = false, whole = false;
-  for (int64_t x = 0; x < npages; ++x) {
-    const int st = (int)(x % kStages);
+  const uint32_t stage0 = smem_u32(stages);
+  float *scores = nullptr;
+  if constexpr (FORM == kFormScores) scores = fa.scores + x0 * (kBlock * G);
+  for (int x = 0; x < npages; ++x) {
     if (!open) {
       load_q16<T, G>(reinterpret_cast<const T *>(p.q) +
                          ((int64_t)cc.s * p.num_q_heads + (int64_t)cc.h * G) * kHeadDim,
-                     lane, qa);
+                     lane, qa);  // (from L2: the producer asked for them pages ago)
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) st16.acc[mt][0] = st16.acc[mt][1] = st16.acc[mt][2] = st16.acc[mt][3] = 0.f;
       st16.m = -INFINITY;
@@ -334,23 +356,17 @@ __device__ __forceinline__ bool split_worker16(const CUtensorMap &kmap, const CU
       whole = cc.page == 0;
       open = true;
     }
-    if (!mbar_wait(&bars[st], (uint32_t)((x / kStages) & 1))) {
-      if (lane == 0) set_error(p.err, PA_ERR_TIMEOUT, cc.s);
-      // give the copies still in flight a short, bounded chance to land
-      for (int64_t r = x + 1; r < (npages < x + kStages ? npages : x + kStages); ++r)
-        mbar_wait(&bars[r % kStages], (uint32_t)((r / kStages) & 1), kWaitLimitNs / 8);
-      return false;
-    }
-    float *scores = nullptr;
-    if constexpr (FORM == kFormScores) scores = fa.scores + (x0 + x) * (kBlock * G);
-    if (!((bad_mask >> st) & 1u)) {
-      decode_page16<T, G>(smem_u32(stages + st * STAGE), min(kBlock, ctx - (first + cc.page) * kBlock), qa,
-                          p.scale_log2, st16, lane, scores);
+    if (!mbar_wait(&ring.full[st], phase)) return false;
+    if (!ring.bad[st]) {
+      decode_page16<T, G>(stage0 + st * STAGE, min(kBlock, ctx - (first + cc.page) * kBlock), qa, p.scale_log2, st16,
+                          lane, scores);
     } else if constexpr (FORM == kFormScores) {  // a page that could not be read has no weight
       for (int i = lane; i < kBlock * G; i += 32) scores[i] = -INFINITY;
     }
+    if constexpr (FORM == kFormScores) scores += kBlock * G;
     __syncwarp();  // every lane has read the stage
-    if (x + kStages < npages) issue(st);
+    if (lane == 0) mbar_arrive(&ring.free[st]);
+    if (++st == kStages) st = 0, phase ^= 1;
 
     const bool last_of_item = cc.page == cc.pages - 1;
     if (last_of_item || x == npages - 1) {

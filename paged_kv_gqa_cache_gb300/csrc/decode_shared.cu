@@ -22,10 +22,10 @@
 //           the CTAs that need the same keys run at the same time and all but one
 //           of them read L2.
 //           Suffix: the rest of each sequence, by the split workers of
-//           decode_mma.cuh on the 8 softmax warps.  Their stages (8 x 3 x 8 KB)
-//           take the very 192 KB of the query tile and the K and V rings, so a
-//           warp goes over to its pages as soon as its last query tile is
-//           stored.  (As a kernel of its own behind the prefix the suffix paid a
+//           decode_mma.cuh: the softmax warps consume, the loader and MMA warps
+//           produce.  Their stages (8 x 3 x 8 KB) take the very 192 KB of the query
+//           tile and the K and V rings, so the first pages are on their way when
+//           the last P V has completed, while the query tile is still stored.  (As a kernel of its own behind the prefix the suffix paid a
 //           launch, a schedule and a first trip to HBM, 57 us for 32 sequences
 //           and 32768 shared tokens; beside it on SMs of its own 54, but 139
 //           against 122 us where groups are large: its stream pushed the shared
@@ -38,7 +38,6 @@ namespace pa {
 namespace {
 
 constexpr int kGroups = kMaxPrefixGroups;
-constexpr int kPhaseBarrier = 5;  // named barrier (4: the registers')
 // Two stages of K and three of V: a K tile is free again once S is computed, a V
 // tile only after the softmax and P V (K 3 and V 2, both issued in one order by
 // the same warps, left 1.9 us between key tiles where HBM's share is 1.5).
@@ -54,10 +53,11 @@ struct PBars {
   uint64_t k_full[kPKStages], s_full[kPKStages];
   uint64_t v_full[kPVStages], p_full[kPVStages], pv_done[kPVStages];
   uint64_t x_full, o_free, drain;
-  uint64_t page[kSoftmaxWarps][kStages];  // the suffix workers' stages
+  uint64_t idle;  // every MMA of the prefix has completed
+  PageRing page[kSoftmaxWarps];  // the suffix workers' rings
   uint32_t tmem_base;
 };
-constexpr int kBarBytes = 512;
+constexpr int kBarBytes = 1024;
 static_assert(sizeof(PBars) <= kBarBytes, "barriers");
 static_assert(kSoftmaxWarps * kStages * STAGE <= P_OFF_X, "the suffix workers' stages fit the rings");
 
@@ -67,7 +67,6 @@ static_assert(kSoftmaxWarps * kStages * STAGE <= P_OFF_X, "the suffix workers' s
 // at most `share` key tiles when the group has several query tiles, else all.
 struct SharedPlan {
   int32_t num_groups, share, ctas, total;  // total: pairs of all groups; ctas: the CTAs that share them
-  int32_t many;                            // a group has several query tiles
   int32_t end[kGroups], len[kGroups];
   int32_t pairs[kGroups + 1], units[kGroups + 1];
 };
@@ -149,14 +148,12 @@ __device__ __forceinline__ void make_plan(SharedPlan &pl, int num_groups, int hk
   for (int round = 0; round < 2; ++round) {  // the pairs, then (with the share known) the units
     int32_t *out = round ? pl.units : pl.pairs;
     int carry = 0;
-    bool many = false;
     for (int g0 = 0; g0 < num_groups; g0 += 32) {
       const int g = g0 + lane;
       int mine = 0;
       if (g < num_groups && pl.len[g] > 0) {
         const GroupShape s = group_shape<G>(pl.end[g] - (g ? pl.end[g - 1] : 0), pl.len[g], round ? pl.share : 1);
         mine = hkv * s.mt * (round ? s.blocks : s.kt);
-        many = many || s.mt > 1;
       }
       int incl = mine;
 #pragma unroll
@@ -167,7 +164,6 @@ __device__ __forceinline__ void make_plan(SharedPlan &pl, int num_groups, int hk
       if (g < num_groups) out[g] = carry + incl - mine;
       carry += __shfl_sync(FULL, incl, 31);
     }
-    many = __any_sync(FULL, many);
     if (lane == 0) {
       out[num_groups] = carry;
       if (!round) {
@@ -175,7 +171,6 @@ __device__ __forceinline__ void make_plan(SharedPlan &pl, int num_groups, int hk
         pl.total = carry;
         pl.ctas = carry < grid ? carry : grid;  // so that no share is empty
         pl.share = carry > 0 ? (carry + pl.ctas - 1) / pl.ctas : 1;
-        pl.many = many;
       }
     }
     __syncwarp();
@@ -222,6 +217,29 @@ __device__ __forceinline__ PUnit punit_at(const SharedPlan &pl, int x, int x_end
   return u;
 }
 
+// The suffix's workers: consumer warp i and producer warp 8 + i.  Their numbers
+// run from the last CTA down: with few pairs and pages the CTAs without pairs
+// take the pages.
+template <typename T, int G, bool CONSUME>
+__device__ __forceinline__ bool suffix_worker(const CUtensorMap &kpage, const CUtensorMap &vmap, const SharedParams &sp,
+                                              const DecodeParams &dp, const SharedPlan &pl, uint8_t *smem, PBars &bars,
+                                              const int32_t *prefix) {
+  const int64_t P = (int64_t)prefix[sp.num_seqs] * sp.num_kv_heads;
+  const int64_t W0 = (int64_t)gridDim.x * kSoftmaxWarps, W = P < W0 ? P : W0;
+  const int i = (threadIdx.x >> 5) % kSoftmaxWarps;
+  const int64_t w = (int64_t)((int)gridDim.x - 1 - (int)blockIdx.x) * kSoftmaxWarps + i;
+  if (w >= W) return true;
+  FormArgs fa;
+  fa.group_end = pl.end;
+  fa.group_len = pl.len;
+  fa.num_groups = sp.num_groups;
+  uint8_t *stages = smem + i * (kStages * STAGE);
+  if constexpr (CONSUME)
+    return split_consumer16<T, G, kFormSuffix>(dp, fa, stages, bars.page[i], prefix, w, P, W);
+  else
+    return split_producer16<G, kFormSuffix>(kpage, vmap, dp, fa, stages, bars.page[i], prefix, w, P, W);
+}
+
 // ---- the shared kernel ----
 // The roles of prefill_kernel.cuh, each looping over the CTA's runs of pairs
 // with a key-tile counter c that runs on across them: warps 0..7 softmax and
@@ -232,9 +250,7 @@ __device__ __forceinline__ PUnit punit_at(const SharedPlan &pl, int x, int x_end
 // P goes into P V rounded to the 16-bit type where a group has several query
 // tiles (tensor-bound), and in two terms where it has one (HBM-bound: the 8
 // more MMAs per key tile, 0.26 us, find the tensor core idle).
-// The softmax warps then are the suffix's split workers.  Where a group has
-// several query tiles, the upper half of the CTAs takes its suffix first, so
-// that tensor-bound and HBM-bound work run side by side.
+// Then warp i < 8 consumes and warp 8 + i fetches the pages of a suffix worker.
 template <typename T, int G>
 __global__ void __launch_bounds__(kThreads, 1)
 shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kpage,
@@ -271,6 +287,8 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     mbar_init(&bars.x_full, kSoftmaxThreads);
     mbar_init(&bars.o_free, kSoftmaxThreads);
     mbar_init(&bars.drain, 1);
+    mbar_init(&bars.idle, 1);
+    for (int i = 0; i < kSoftmaxWarps; ++i) init_ring(bars.page[i]);
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
@@ -298,36 +316,12 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   tc::fence_after_sync();
   const uint32_t tmem = bars.tmem_base;
   const int x0 = share_start(b, pl.total, pl.ctas), x1 = share_start(b + 1, pl.total, pl.ctas);
-  const bool suffix_first = pl.many && 2 * b >= (int)gridDim.x;
   bool timed_out = false;
 
   if (warp < kSoftmaxWarps) {
     regs_inc<kRegsSoftmax>();
     regs_taken();
     griddep_wait();
-#pragma unroll 1
-    for (int phase = 0; phase < 2; ++phase) {
-    if ((phase == 0) == suffix_first) {
-      // ---------------- the suffix: this warp's pages ----------------
-      // Worker numbers run from the last CTA down: with few pairs and pages the
-      // CTAs without pairs take the pages.  The rings are idle: every copy was
-      // consumed by an MMA, and the last P V, which this warp saw complete, came
-      // after all of them (or, suffix first, nothing has been copied yet).
-      const int64_t P = (int64_t)prefix[sp.num_seqs] * sp.num_kv_heads;
-      const int64_t W0 = (int64_t)gridDim.x * kSoftmaxWarps, W = P < W0 ? P : W0;
-      const int64_t w = (int64_t)((int)gridDim.x - 1 - b) * kSoftmaxWarps + warp;
-      if (w < W && !timed_out) {
-        FormArgs fa;
-        fa.group_end = pl.end;
-        fa.group_len = pl.len;
-        fa.num_groups = sp.num_groups;
-        if (!split_worker16<T, G, kFormSuffix>(kpage, vmap, dp, fa, smem + warp * (kStages * STAGE), bars.page[warp],
-                                               prefix, w, P, W))
-          timed_out = true;
-      }
-      if (suffix_first) named_barrier(kPhaseBarrier, kThreads);  // the rings are the loaders' again
-      continue;
-    }
     // ---------------- softmax + epilogue (warps 0..7), run after run ----------------
     const int quad = warp & 3, ch = warp >> 2;
     const int r = quad * 32 + lane;
@@ -472,12 +466,13 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (ch == 0) sp.ws_ml[slot * 128 + r] = make_float2(M, l0 * f0 + l1 * f1);
       }
     }
-    }
+    // ---------------- the suffix: the worker whose producer is warp 8 + warp ----------------
+    if (!timed_out && !suffix_worker<T, G, true>(kpage, vmap, sp, dp, pl, smem, bars, prefix)) timed_out = true;
     regs_dec<128>();
   } else {
     // every loader and MMA warp runs this one decrease (setmaxnreg acts on whole warpgroups)
     regs_dec<kRegsOther>();
-    if (suffix_first) named_barrier(kPhaseBarrier, kThreads);
+    griddep_wait();  // Q, K and V may come from the kernels before
     if (warp != kWarpMma) {
       // ---------------- loader warps ----------------
       // Warps 0 .. 3 load K, each 4 of a key tile's 16 boxes (the 64-dim half b %
@@ -507,7 +502,6 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         U = punit_at<G>(pl, x0, x1);
         open_run(U);
       }
-      griddep_wait();  // Q, K and V may come from the kernels before
       if (scribe) {  // the join's tables (after the wait: the previous call's join may still read them)
         const SharedTables tb = shared_tables(sp.tables);
         const int i0 = lw * 32 + lane;
@@ -670,12 +664,19 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
       }
       if (!timed_out && pc >= 0 && !issue_pv()) timed_out = true;
+      if (!timed_out && leader && x0 < x1) tc::commit(&bars.idle);
+      __syncwarp();
       if (timed_out) {  // every MMA issued so far, bounded, before the tensor memory is freed
         if (leader) tc::commit(&bars.drain);
         __syncwarp();
         mbar_wait(&bars.drain, 0, kWaitLimitNs / 8);
       }
     }
+    // ---------------- the suffix: this warp fetches consumer warp - 8's pages ----------------
+    // The rings are idle once every MMA has completed: each copy was consumed by one.
+    if (x0 < x1 && !timed_out && !mbar_wait(&bars.idle, 0)) timed_out = true;
+    timed_out = __any_sync(FULL, timed_out);
+    if (!timed_out && !suffix_worker<T, G, false>(kpage, vmap, sp, dp, pl, smem, bars, prefix)) timed_out = true;
     regs_wait_taken();  // (the softmax warps hold their registers by now)
     regs_inc<128>();
   }

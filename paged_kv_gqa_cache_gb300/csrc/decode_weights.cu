@@ -23,24 +23,33 @@ constexpr int kWeightThreads = 256;
 constexpr int kKeysPerThread = kChunkKeys / kWeightThreads;
 static_assert(kWeightThreads / 32 >= 8, "a warp per query head of a KV head");
 
+// Per CTA kWorkers consumer warps, then their producer warps; per worker its
+// stages and ring, then the page prefix.
+constexpr int kWorkers = 4;
+constexpr int kScoreThreads = 2 * kWorkers * 32;
+constexpr int kRingOff = kWorkers * kStages * STAGE;
+constexpr int kPrefixOff = (kRingOff + kWorkers * (int)sizeof(PageRing) + 15) / 16 * 16;
+
 template <typename T, int G>
-__global__ void __launch_bounds__(NW * 32, 2)
+__global__ void __launch_bounds__(kScoreThreads, 2)
 decode_scores_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const DecodeParams p, float *scores, int max_len) {
-  using Sm = SplitSmem16<NW>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ int warp_tot[NW];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int32_t *prefix = reinterpret_cast<int32_t *>(smem + Sm::kPrefixOff);
+  __shared__ int warp_tot[kScoreThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = warp % kWorkers;
+  PageRing *rings = reinterpret_cast<PageRing *>(smem + kRingOff);
+  int32_t *prefix = reinterpret_cast<int32_t *>(smem + kPrefixOff);
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
+    for (int i = 0; i < kWorkers; ++i) init_ring(rings[i]);
+    fence_mbar_init();
   }
   FormArgs fa;
   fa.scores = scores;
   griddep_wait();
-  scan_pages_of<NW * 32>(p.num_seqs, prefix, warp_tot, [&](int s) {
+  scan_pages_of<kScoreThreads>(p.num_seqs, prefix, warp_tot, [&](int s) {
     const int ctx = __ldg(p.context_lens + s);
     if (ctx >= 1 && ctx <= p.max_blocks_per_seq * kBlock && ctx <= max_len) return (ctx + kBlock - 1) / kBlock;
     if (blockIdx.x == 0) set_error(p.err, PA_ERR_RANGE, s);
@@ -48,13 +57,16 @@ decode_scores_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
   });
   const int64_t P = (int64_t)prefix[p.num_seqs] * p.num_kv_heads;
   const int64_t W = P < p.num_workers ? P : p.num_workers;
-  const int w = blockIdx.x * NW + warp;
+  const int w = blockIdx.x * kWorkers + slot;
   if (blockIdx.x == 0 && warp == 0)  // for the pass that joins the fragments
     for (int i = lane; i <= p.num_seqs; i += 32) p.meta[i] = prefix[i];
-  if (w < W)
-    split_worker16<T, G, kFormScores>(kmap, vmap, p, fa, smem + Sm::kStagesOff + warp * kStages * STAGE,
-                                      reinterpret_cast<uint64_t *>(smem + Sm::kBarsOff) + warp * kStages, prefix, w,
-                                      P, W);
+  if (w < W) {
+    uint8_t *stages = smem + slot * kStages * STAGE;
+    const bool ok = warp < kWorkers
+                        ? split_consumer16<T, G, kFormScores>(p, fa, stages, rings[slot], prefix, w, P, W)
+                        : split_producer16<G, kFormScores>(kmap, vmap, p, fa, stages, rings[slot], prefix, w, P, W);
+    if (!ok) set_error(p.err, PA_ERR_TIMEOUT, w);
+  }
   griddep_launch_dependents();
 }
 
@@ -166,19 +178,19 @@ template <typename T, int G>
 cudaError_t launch_weights_typed(const DecodeParams &p0, const CUtensorMap &kmap, const CUtensorMap &vmap,
                                  const DecodeWeightsParams &wp, int sms, cudaStream_t stream) {
   DecodeParams p = p0;
-  const int smem = 1024 + SplitSmem16<NW>::kPrefixOff + (p.num_seqs + 1) * 4;
+  const int smem = 1024 + kPrefixOff + (p.num_seqs + 1) * 4;
   static KernelSetup setup;
   int per_sm = 0;
-  cudaError_t e = kernel_setup(setup, decode_scores_kernel<T, G>, smem, NW * 32, &per_sm);
+  cudaError_t e = kernel_setup(setup, decode_scores_kernel<T, G>, smem, kScoreThreads, &per_sm);
   if (e != cudaSuccess) return e;
   int grid = sms * per_sm;
   const int64_t pages = (int64_t)p.num_seqs * p.num_kv_heads * ((wp.max_len + kBlock - 1) / kBlock);
-  const int64_t want = ((pages + 3) / 4 + NW - 1) / NW;  // at least 4 pages per warp
+  const int64_t want = ((pages + 3) / 4 + kWorkers - 1) / kWorkers;  // at least 4 pages per worker
   if (want < grid) grid = (int)want;
   if (grid < 1) grid = 1;
-  if (grid * NW > kDecodeMaxWorkers) grid = kDecodeMaxWorkers / NW;
-  p.num_workers = grid * NW;
-  e = launch_pdl(decode_scores_kernel<T, G>, dim3(grid), dim3(NW * 32), smem, stream, kmap, vmap, p, wp.scores,
+  if (grid * kWorkers > kDecodeMaxWorkers) grid = kDecodeMaxWorkers / kWorkers;
+  p.num_workers = grid * kWorkers;
+  e = launch_pdl(decode_scores_kernel<T, G>, dim3(grid), dim3(kScoreThreads), smem, stream, kmap, vmap, p, wp.scores,
                  wp.max_len);
   if (e != cudaSuccess) return e;
   const dim3 wgrid(1 + (wp.max_len + kChunkKeys - 1) / kChunkKeys, p.num_seqs * p.num_kv_heads);
