@@ -215,21 +215,21 @@ __device__ __forceinline__ void decode_page16(uint32_t stage, int nv, const uint
 }
 
 // The join of online-softmax pieces for one head's 4 dims: pieces (m, l) with o
-// come kJoinPieces at a time (m = -inf: none).
-constexpr int kJoinPieces = 8;
+// come U at a time (m = -inf: none).
 struct JoinState {
   float M = -INFINITY, L = 0.f;
   float4 O = {0.f, 0.f, 0.f, 0.f};
-  __device__ __forceinline__ void add(const float2 (&ml)[kJoinPieces], const float4 (&o)[kJoinPieces]) {
+  template <int U>
+  __device__ __forceinline__ void add(const float2 (&ml)[U], const float4 (&o)[U]) {
     float mx = M;
 #pragma unroll
-    for (int u = 0; u < kJoinPieces; ++u) mx = fmaxf(mx, ml[u].x);
+    for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
     if (mx == -INFINITY) return;
     const float f = ex2(M - mx);
     L *= f;
     O.x *= f, O.y *= f, O.z *= f, O.w *= f;
 #pragma unroll
-    for (int u = 0; u < kJoinPieces; ++u) {
+    for (int u = 0; u < U; ++u) {
       const float w = ex2(ml[u].x - mx);
       L = fmaf(ml[u].y, w, L);
       O.x = fmaf(o[u].x, w, O.x);

@@ -38,6 +38,7 @@ namespace pa {
 namespace {
 
 constexpr int kGroups = kMaxPrefixGroups;
+constexpr int kJoinPieces = 8;  // pieces in flight in the join
 // Two stages of K and three of V: a K tile is free again once S is computed, a V
 // tile only after the softmax and P V (K 3 and V 2, both issued in one order by
 // the same warps, left 1.9 us between key tiles where HBM's share is 1.5).
@@ -472,7 +473,6 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   } else {
     // every loader and MMA warp runs this one decrease (setmaxnreg acts on whole warpgroups)
     regs_dec<kRegsOther>();
-    griddep_wait();  // Q, K and V may come from the kernels before
     if (warp != kWarpMma) {
       // ---------------- loader warps ----------------
       // Warps 0 .. 3 load K, each 4 of a key tile's 16 boxes (the 64-dim half b %
@@ -502,6 +502,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         U = punit_at<G>(pl, x0, x1);
         open_run(U);
       }
+      griddep_wait();  // Q, K and V may come from the kernels before
       if (scribe) {  // the join's tables (after the wait: the previous call's join may still read them)
         const SharedTables tb = shared_tables(sp.tables);
         const int i0 = lw * 32 + lane;
@@ -585,6 +586,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
     } else {
       // ---------------- MMA issuer (warp-uniform loop, one elected lane issues) ----------------
+      griddep_wait();  // (for the suffix's pages)
       const bool leader = elect_one();
       auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, mbar_wait(bar, parity)) != 0; };
       const uint64_t qdesc = tc::desc_sw128(smem_u32(smem + P_OFF_Q), 16, 1024);
@@ -697,6 +699,7 @@ __global__ void __launch_bounds__(128)
 shared_join_kernel(const SharedParams sp, const DecodeParams p) {
   constexpr int TQ = 128 / G, QW = 32 / G;  // dim quads per warp
   griddep_wait();
+  griddep_launch_dependents();  // (it writes nothing that a kernel may read before its own wait)
   const int wid = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int hkv = p.num_kv_heads;
   if (wid >= p.num_seqs * hkv * G) return;

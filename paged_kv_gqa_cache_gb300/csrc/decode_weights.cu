@@ -19,6 +19,7 @@ namespace pa {
 namespace {
 
 constexpr int kChunkKeys = 2048;
+constexpr int kJoinPieces = 8;  // fragments in flight (4: weights-long 4 us slower)
 constexpr int kWeightThreads = 256;
 constexpr int kKeysPerThread = kChunkKeys / kWeightThreads;
 static_assert(kWeightThreads / 32 >= 8, "a warp per query head of a KV head");
@@ -76,6 +77,7 @@ decode_weights_kernel(const DecodeParams p, const float *scores, const float *we
                       int64_t weights_stride) {
   __shared__ float s_m[G], s_inv[G];
   griddep_wait();
+  griddep_launch_dependents();  // (it writes nothing that a kernel may read before its own wait)
   const int item = blockIdx.y, hkv = p.num_kv_heads;
   const int s = item / hkv, h = item % hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
