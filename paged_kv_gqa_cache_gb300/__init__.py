@@ -759,34 +759,46 @@ ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = range(5)
 
 
-def _complain(t, name, dtype, dev):
-    _need(t, name, dtype)
-    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+# The small calls of this section last a few microseconds on the GPU, so their
+# checks are written for the interpreter: one pass of cheap tests over the
+# tensors, and only where one fails the full story.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _check_all(dev: int, *specs) -> None:
-    """Every (tensor, name, dtype) is a contiguous tensor of its type on the
-    current device (the library launches there); dtype None: any."""
+    """Raise for the first (tensor, name, dtype) that is not a contiguous tensor
+    of its type on the current device (the library launches there); dtype None: any."""
     for t, name, dtype in specs:
-        if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous() or \
-                (dtype is not None and t.dtype is not dtype):
-            _complain(t, name, dtype, dev)
+        _need(t, name, dtype)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _fine(dev: int, dtype, *tensors) -> bool:
+    """Whether all are contiguous tensors of the type on the current device."""
+    try:
+        for t in tensors:
+            if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+                return False
+    except AttributeError:
+        return False
+    return True
 
 
 def _pool_of(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: int) -> KVPool:
     """make_pool on the current device."""
-    _check_all(dev, (k_cache, "k_cache", None), (v_cache, "v_cache", k_cache.dtype))
+    dt = getattr(k_cache, "dtype", None)
+    if not _fine(dev, dt, k_cache, v_cache):
+        _check_all(dev, (k_cache, "k_cache", None), (v_cache, "v_cache", dt))
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, num_kv_heads, head_dim]")
-    return KVPool(k_cache.data_ptr(), v_cache.data_ptr(), *shape, _dtype_code(k_cache))
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return KVPool(k_cache.data_ptr(), v_cache.data_ptr(), *shape, PA_BF16 if dt is torch.bfloat16 else _dtype_code(k_cache))
 
 
 def _stream_of(stream, dev: int) -> int:
-    """_stream, by the short way where torch has it (a fifth of a small call's host time else)."""
+    """_stream, by the short way where torch has it."""
     if stream is None and _raw_stream is not None:
         return _raw_stream(dev)
     return _stream(stream)
@@ -822,32 +834,34 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
     [T, Hkv, 128] to ``positions``, after an RMSNorm where the weights are given,
     and write the rotated k and the unchanged v into their slots.
     ``inv_freq`` (float64 [rotary_dim / 2]) sets how much of the head turns."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     pool = _pool_of(k_cache, v_cache, dev)
     dt, hkv, d = k_cache.dtype, pool.num_kv_heads, pool.head_dim
     fresh = q_out is None
     if fresh:
         q_out = torch.empty_like(q)
-    _check_all(dev, (q, "q", dt), (k, "k", dt), (v, "v", dt), (inv_freq, "inv_freq", torch.float64),
-               (positions, "positions", torch.int32), (slot_mapping, "slot_mapping", torch.int64),
-               (q_out, "q_out", dt))
-    T, hq = q.shape[0], q.shape[1] if q.dim() == 3 else 0
-    rows = (T, hkv, d)
-    if q.shape != (T, hq, d) or k.shape != rows or v.shape != rows or positions.shape != (T,) \
-            or slot_mapping.shape != (T,) or inv_freq.dim() != 1:
+    if not (_fine(dev, dt, q, k, v, q_out) and _fine(dev, torch.float64, inv_freq) and
+            _fine(dev, torch.int32, positions) and _fine(dev, torch.int64, slot_mapping)):
+        _check_all(dev, (q, "q", dt), (k, "k", dt), (v, "v", dt), (inv_freq, "inv_freq", torch.float64),
+                   (positions, "positions", torch.int32), (slot_mapping, "slot_mapping", torch.int64),
+                   (q_out, "q_out", dt))
+    qshape = q.shape
+    T, hq = qshape[0], qshape[1] if len(qshape) == 3 else 0
+    rows, each = (T, hkv, d), (T,)
+    if qshape != (T, hq, d) or k.shape != rows or v.shape != rows or positions.shape != each \
+            or slot_mapping.shape != each or inv_freq.dim() != 1:
         raise ValueError("q [T, Hq, 128], k/v [T, Hkv, 128], positions/slot_mapping [T], inv_freq [rotary_dim / 2]")
-    if q_out.shape != q.shape:
+    if not fresh and q_out.shape != qshape:
         raise ValueError("q_out must have the shape of q")
     wq = wk = None
-    for name, t in (("q_norm_weight", q_norm_weight), ("k_norm_weight", k_norm_weight)):
-        if t is not None:
-            _check_all(dev, (t, name, dt))
-            if t.shape != (d,):
-                raise ValueError(f"{name} must be [{d}]")
-    if q_norm_weight is not None:
-        wq = q_norm_weight.data_ptr()
-    if k_norm_weight is not None:
-        wk = k_norm_weight.data_ptr()
+    if q_norm_weight is not None or k_norm_weight is not None:
+        for name, t in (("q_norm_weight", q_norm_weight), ("k_norm_weight", k_norm_weight)):
+            if t is not None:
+                _check_all(dev, (t, name, dt))
+                if t.shape != (d,):
+                    raise ValueError(f"{name} must be [{d}]")
+        wq = None if q_norm_weight is None else q_norm_weight.data_ptr()
+        wk = None if k_norm_weight is None else k_norm_weight.data_ptr()
     rope = Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], ROPE_INTERLEAVED if interleaved else ROPE_HALF,
                 attention_factor)
     _check((_lib or load_library()).pa_rope_kv_write(
@@ -878,17 +892,19 @@ def paged_attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: to
     prefixes: group g is the next ``group_sizes[g]`` sequences (int32 [groups]),
     which share their first ``prefix_lens[g]`` tokens (int32 [groups], multiples
     of 16), read once through the group's first block table."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     pool = _pool_of(k_cache, v_cache, dev)
     S, hq, mb, mcl, out, fresh = _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out)
-    _check_all(dev, (group_sizes, "group_sizes", torch.int32), (prefix_lens, "prefix_lens", torch.int32))
+    if not _fine(dev, torch.int32, group_sizes, prefix_lens):
+        _check_all(dev, (group_sizes, "group_sizes", torch.int32), (prefix_lens, "prefix_lens", torch.int32))
     if group_sizes.dim() != 1 or prefix_lens.shape != group_sizes.shape:
         raise ValueError("group_sizes and prefix_lens must both be [groups]")
     n = group_sizes.shape[0]
     if workspace is None:
         workspace = alloc_decode_shared_workspace(S, n, hq, pool.num_kv_heads, q.device)
         fresh.append(workspace)
-    _check_all(dev, (workspace, "workspace", None))
+    if not _fine(dev, torch.uint8, workspace):
+        _check_all(dev, (workspace, "workspace", None))
     _check((_lib or load_library()).pa_paged_attn_decode_shared(
         q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq, mcl, scale,
         group_sizes.data_ptr(), prefix_lens.data_ptr(), n, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
@@ -917,8 +933,9 @@ def _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out)
     if out is None:
         out = torch.empty_like(q)
         fresh.append(out)
-    _check_all(dev, (q, "q", dt), (block_tables, "block_tables", torch.int32),
-               (context_lens, "context_lens", torch.int32), (out, "out", dt))
+    if not (_fine(dev, dt, q, out) and _fine(dev, torch.int32, block_tables, context_lens)):
+        _check_all(dev, (q, "q", dt), (block_tables, "block_tables", torch.int32),
+                   (context_lens, "context_lens", torch.int32), (out, "out", dt))
     shape = q.shape
     if len(shape) != 3 or shape[2] != pool.head_dim:
         raise ValueError(f"q must be [S, Hq, {pool.head_dim}]")
@@ -942,15 +959,17 @@ def paged_attn_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     bound]; the same tensor: in place; ``weights_in`` None: zeros).  Entries from
     a sequence's length on are not touched.  ``max_context_len`` defaults to what
     both the block tables and the weights hold.  Returns (out, weights_out)."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     pool = _pool_of(k_cache, v_cache, dev)
     S, hq, mb, mcl, out, fresh = _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out)
-    _check_all(dev, (weights_out, "weights_out", torch.float32))
+    if not _fine(dev, torch.float32, weights_out):
+        _check_all(dev, (weights_out, "weights_out", torch.float32))
     wshape = weights_out.shape
     if len(wshape) != 3 or wshape[0] != S or wshape[1] != pool.num_kv_heads:
         raise ValueError(f"weights_out must be [{S}, {pool.num_kv_heads}, stride]")
     if weights_in is not None:
-        _check_all(dev, (weights_in, "weights_in", torch.float32))
+        if not _fine(dev, torch.float32, weights_in):
+            _check_all(dev, (weights_in, "weights_in", torch.float32))
         if weights_in.shape != wshape:
             raise ValueError("weights_in and weights_out must have one shape")
     if max_context_len is None:
@@ -958,7 +977,8 @@ def paged_attn_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     if workspace is None:
         workspace = alloc_decode_weights_workspace(S, hq, pool.num_kv_heads, mcl, q.device)
         fresh.append(workspace)
-    _check_all(dev, (workspace, "workspace", None))
+    if not _fine(dev, torch.uint8, workspace):
+        _check_all(dev, (workspace, "workspace", None))
     _check((_lib or load_library()).pa_paged_attn_decode_weights(
         q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq, mcl, scale,
         None if weights_in is None else weights_in.data_ptr(), weights_out.data_ptr(), wshape[2], out.data_ptr(),
@@ -981,13 +1001,14 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
     (default: in place).  Returns (kept int32 [S, Hkv, budget] with -1 past the
     new length, new context lengths int32 [S]).  ``max_context_len`` is a host
     bound on ``context_lens`` for the check that the weights cover it."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     pool = _pool_of(k_cache, v_cache, dev)
     dst = block_tables if dst_block_tables is None else dst_block_tables
     w_out = weights if weights_out is None else weights_out
     i32, f32 = torch.int32, torch.float32
-    _check_all(dev, (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
-               (weights, "weights", f32), (dst, "dst_block_tables", i32), (w_out, "weights_out", f32))
+    if not (_fine(dev, i32, block_tables, context_lens, dst) and _fine(dev, f32, weights, w_out)):
+        _check_all(dev, (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
+                   (weights, "weights", f32), (dst, "dst_block_tables", i32), (w_out, "weights_out", f32))
     if block_tables.dim() != 2 or dst.dim() != 2 or weights.dim() != 3 or w_out.dim() != 3:
         raise ValueError("block_tables and dst_block_tables must be [S, max_blocks], the weights [S, Hkv, stride]")
     S, mb = block_tables.shape
@@ -999,12 +1020,13 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
         raise ValueError(f"weights hold {ws[2]} tokens, max_context_len is {max_context_len}")
     fresh = []
     if kept is None:
-        kept = torch.empty((S, hkv, max(budget, 0)), dtype=i32, device=k_cache.device)
+        kept = block_tables.new_empty((S, hkv, max(budget, 0)))
         fresh.append(kept)
     if new_context_lens is None:
-        new_context_lens = torch.empty((S,), dtype=i32, device=k_cache.device)
+        new_context_lens = torch.empty_like(context_lens)
         fresh.append(new_context_lens)
-    _check_all(dev, (kept, "kept", i32), (new_context_lens, "new_context_lens", i32))
+    if not _fine(dev, i32, kept, new_context_lens):
+        _check_all(dev, (kept, "kept", i32), (new_context_lens, "new_context_lens", i32))
     if kept.shape != (S, hkv, budget) or new_context_lens.shape != (S,):
         raise ValueError(f"kept must be [{S}, {hkv}, {budget}], new_context_lens [{S}]")
     _check((_lib or load_library()).pa_kv_evict(
