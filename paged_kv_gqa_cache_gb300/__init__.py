@@ -1020,7 +1020,7 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
         raise ValueError(f"weights hold {ws[2]} tokens, max_context_len is {max_context_len}")
     fresh = []
     if kept is None:
-        kept = block_tables.new_empty((S, hkv, max(budget, 0)))
+        kept = torch.empty((S, hkv, max(budget, 0)), dtype=i32, device=block_tables.device)
         fresh.append(kept)
     if new_context_lens is None:
         new_context_lens = torch.empty_like(context_lens)
