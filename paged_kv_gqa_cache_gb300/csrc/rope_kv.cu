@@ -22,15 +22,22 @@
 // plus pi * 2^-25 from the conversion to fp32.
 //
 // HBM-bound: one pass over q, k and v (24.6 KB in and out per token at 32 / 8
-// heads).  16 lanes hold one head row, 8 values each, chosen so that a lane
-// holds both values of its 4 pairs: dims 4 l .. and d / 2 + 4 l .. of the
-// rotated part in the half layout (two 8-byte accesses), 8 l .. in the
-// interleaved one, so that no value crosses a lane and a lane's 4 (cos, sin)
-// stay in registers for all rows of the token.  A CTA takes 4 tokens at a time
-// (2 warps each), or, when there are too few tokens to fill the GPU so, one
-// (8 warps): its threads compute the tokens' angles once for all heads, through
-// shared memory (two buffers, one barrier per step), while the first rows'
-// loads are on their way.
+// heads), if the issue slots allow it.  16 lanes hold one head row, 8 values
+// each, chosen so that a lane holds both values of its 4 pairs: dims 4 l .. and
+// d / 2 + 4 l .. of the rotated part in the half layout (two 8-byte accesses),
+// 8 l .. in the interleaved one, so that no value crosses a lane and a lane's 4
+// (cos, sin) stay in registers for all rows of the token.  Queries, keys and
+// values are swept one kind after the other, so that a row costs no address
+// beyond a constant offset and the norm's weights are widened once per kind,
+// and two fp32 values go through one instruction.  A CTA takes 4 tokens at a
+// time (2 warps each), or, when there are too few tokens to fill the GPU so,
+// one (8 warps): its threads compute the tokens' angles once for all heads,
+// through shared memory (two buffers, one barrier per step), while the first
+// rows' loads are on their way.
+// 16383 tokens of 32 / 8 heads with the norm, bf16: 64.6 us, 6.24 TB/s; with
+// all rows in one loop, addresses and weights per row, it was issue-bound at
+// 76.8, and with 4 CTAs on an SM, 64 registers and spills, 72.  512 tokens,
+// without: 3.4 us; 8 tokens of 16 / 8 heads: 1.7.
 #include "pa_device.cuh"
 
 namespace pa {
@@ -38,7 +45,7 @@ namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kRopeKvThreads = 256;
-constexpr int kBatch = 4;  // rows per half-warp whose loads are in flight together
+constexpr int kBatchQ = 4, kBatchKv = 2;  // rows per half-warp whose loads are in flight together: queries; keys and values
 
 // kPairs: a lane holds both values of its pairs (interleaved, or half with
 // rotary_dim a multiple of 8); kExchange: any even rotary_dim in the half
@@ -51,32 +58,64 @@ __device__ __forceinline__ long long turns_fixed(double inv_freq) {
   return __double2ll_rn((t - rint(t)) * 18446744073709551616.0);
 }
 
+// Two fp32 values in one operation.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+  return reinterpret_cast<float2 &>(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+  return reinterpret_cast<float2 &>(d);
+}
+__device__ __forceinline__ float2 twice(float a) { return make_float2(a, a); }
+
 // TOK tokens per CTA and step, 8 / TOK warps each.
 template <typename T, int MODE, bool NORM, int TOK>
-__global__ void __launch_bounds__(kRopeKvThreads, 4) rope_kv_kernel(const RopeKvParams p) {
+__global__ void __launch_bounds__(kRopeKvThreads, 3) rope_kv_kernel(const RopeKvParams p) {
   constexpr int kWarps = kRopeKvThreads / 32 / TOK;  // warps per token
   constexpr int kStep = 2 * kWarps;                  // rows per pass of them
   __shared__ __align__(16) float2 cs_buf[2][TOK][kHeadDim / 2];
-  __shared__ float stage_buf[MODE == kHalfExchange ? kRopeKvThreads / 16 * kHeadDim : 1];
+  __shared__ __align__(16) float stage_buf[MODE == kHalfExchange ? kRopeKvThreads / 16 * kHeadDim : 1];
   const int tid = threadIdx.x, lane = tid & 31, l16 = lane & 15;
-  const int hq = p.num_q_heads, hkv = p.num_kv_heads;
-  const int rows = hq + 2 * hkv, d = p.rotary_dim;
+  const int hq = p.num_q_heads, hkv = p.num_kv_heads, d = p.rotary_dim;
   // this lane's values: dims d0 .. d0 + 3 and d1 .. d1 + 3; its pairs' angles: pair 4 l16 + i
   const bool split = MODE == kHalfPairs && 8 * l16 < d;
   const int d0 = split ? 4 * l16 : 8 * l16, d1 = split ? d / 2 + 4 * l16 : 8 * l16 + 4;
   float *stage = stage_buf + (MODE == kHalfExchange ? (tid >> 4) * kHeadDim : 0);
-  const int tok = tid / (32 * kWarps);                          // this warp's token of the step
-  const int r_first = ((tid >> 5) % kWarps) * 2 + (lane >> 4);  // this half-warp's first row
+  const int tok = tid / (32 * kWarps);  // this warp's token of the step
+  // The first rows of this warp's pair of half-warps: of the queries and keys,
+  // and of the values, which start with the other half of the warps.
+  const int w_qk = ((tid >> 5) % kWarps) * 2, w_v = (w_qk + kStep / 2) % kStep;
+  const int r_qk = w_qk + (lane >> 4), r_v = w_v + (lane >> 4);
   griddep_wait();  // q, k, v may be the previous kernel's output; the pool may be read by it
   long long turns = 0;
   if (tid < TOK * 64 && (tid & 63) < d / 2) turns = turns_fixed(__ldg(p.inv_freq + (tid & 63)));
-  uint2 wq[2], wk[2];
-  if constexpr (NORM) {
-    wq[0] = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p.q_weight) + d0);
-    wq[1] = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p.q_weight) + d1);
-    wk[0] = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p.k_weight) + d0);
-    wk[1] = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p.k_weight) + d1);
-  }
+  auto read = [&](const T *src, uint2 (&x)[2]) {
+    if constexpr (MODE == kHalfPairs) {
+      x[0] = *reinterpret_cast<const uint2 *>(src + d0);
+      x[1] = *reinterpret_cast<const uint2 *>(src + d1);
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4 *>(src + d0);
+      x[0] = make_uint2(u.x, u.y);
+      x[1] = make_uint2(u.z, u.w);
+    }
+  };
+  auto write = [&](T *dst, const uint2 (&x)[2]) {
+    if constexpr (MODE == kHalfPairs) {
+      *reinterpret_cast<uint2 *>(dst + d0) = x[0];
+      *reinterpret_cast<uint2 *>(dst + d1) = x[1];
+    } else {
+      *reinterpret_cast<uint4 *>(dst + d0) = make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
+    }
+  };
+  auto widen = [](const uint2 (&u)[2], float2 (&x)[4]) {
+    x[0] = Pack<T>::to_f2(u[0].x), x[1] = Pack<T>::to_f2(u[0].y);
+    x[2] = Pack<T>::to_f2(u[1].x), x[3] = Pack<T>::to_f2(u[1].y);
+  };
   int buf = 0;
   for (int t0 = blockIdx.x * TOK; t0 < p.num_tokens; t0 += gridDim.x * TOK) {  // (block-uniform)
     const int t = t0 + tok;
@@ -84,27 +123,22 @@ __global__ void __launch_bounds__(kRopeKvThreads, 4) rope_kv_kernel(const RopeKv
     const int64_t slot = t < p.num_tokens ? __ldg(p.slots + t) : -1;
     const bool ok = pos >= 0 && slot >= 0 && slot < p.num_slots;  // else nothing of the token is written
     if (!ok && t < p.num_tokens && tid % (32 * kWarps) == 0) set_error(p.err, PA_ERR_RANGE, t);
-    auto load = [&](int r, uint2 (&x)[2]) {
-      const T *src = r < hq         ? static_cast<const T *>(p.q) + ((int64_t)t * hq + r) * kHeadDim
-                     : r < hq + hkv ? static_cast<const T *>(p.k) + ((int64_t)t * hkv + (r - hq)) * kHeadDim
-                                    : static_cast<const T *>(p.v) + ((int64_t)t * hkv + (r - hq - hkv)) * kHeadDim;
-      if constexpr (MODE == kHalfPairs) {
-        x[0] = *reinterpret_cast<const uint2 *>(src + d0);
-        x[1] = *reinterpret_cast<const uint2 *>(src + d1);
-      } else {
-        const uint4 u = *reinterpret_cast<const uint4 *>(src + d0);
-        x[0] = make_uint2(u.x, u.y);
-        x[1] = make_uint2(u.z, u.w);
-      }
-    };
-    uint2 raw[kBatch][2];
+    const T *q = static_cast<const T *>(p.q) + ((int64_t)t * hq + r_qk) * kHeadDim;
+    const T *k = static_cast<const T *>(p.k) + ((int64_t)t * hkv + r_qk) * kHeadDim;
+    const T *v = static_cast<const T *>(p.v) + ((int64_t)t * hkv + r_v) * kHeadDim;
+    // the first rows of each kind, all on their way together
+    uint2 raw_q[kBatchQ][2] = {}, raw_k[kBatchKv][2] = {}, raw_v[kBatchKv][2] = {};
+    if (ok) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = r_first + i * kStep;
-      raw[i][0] = raw[i][1] = make_uint2(0, 0);
-      if (ok && r < rows) load(r, raw[i]);
+      for (int i = 0; i < kBatchQ; ++i)
+        if (r_qk + i * kStep < hq) read(q + i * kStep * kHeadDim, raw_q[i]);
+#pragma unroll
+      for (int i = 0; i < kBatchKv; ++i) {
+        if (r_qk + i * kStep < hkv) read(k + i * kStep * kHeadDim, raw_k[i]);
+        if (r_v + i * kStep < hkv) read(v + i * kStep * kHeadDim, raw_v[i]);
+      }
     }
-    // the step's angles, while the rows are on their way
+    // the step's angles, meanwhile
     if (tid < TOK * 64 && (tid & 63) < d / 2) {
       const int at = t0 + (tid >> 6);
       const int pa = at < p.num_tokens ? __ldg(p.positions + at) : 0;
@@ -115,98 +149,89 @@ __global__ void __launch_bounds__(kRopeKvThreads, 4) rope_kv_kernel(const RopeKv
     }
     __syncthreads();
     if (ok) {  // (warp-uniform)
-      float2 cs[4];
+      float2 c[2], s[2], ns[2];  // of this lane's 4 pairs: cos, sin, -sin
       if constexpr (MODE != kHalfExchange) {
         const float4 *src = reinterpret_cast<const float4 *>(cs_buf[buf][tok] + 4 * l16);
-        const float4 u = src[0], v = src[1];  // (pairs past rotary_dim / 2 are not used)
-        cs[0] = make_float2(u.x, u.y), cs[1] = make_float2(u.z, u.w);
-        cs[2] = make_float2(v.x, v.y), cs[3] = make_float2(v.z, v.w);
+        const float4 a = src[0], b = src[1];  // (pairs past rotary_dim / 2 are not used)
+        c[0] = make_float2(a.x, a.z), s[0] = make_float2(a.y, a.w), ns[0] = make_float2(-a.y, -a.w);
+        c[1] = make_float2(b.x, b.z), s[1] = make_float2(b.y, b.w), ns[1] = make_float2(-b.y, -b.w);
       }
-      for (int r0 = 0; r0 < rows; r0 += kStep * kBatch) {
+      float2 weight[4];  // of the norm, for the kind of row at hand
+      auto rotate = [&](uint2 (&u)[2]) {
+        float2 x[4];
+        widen(u, x);
+        if constexpr (NORM) {
+          const float2 sq = fma2(x[3], x[3], fma2(x[2], x[2], fma2(x[1], x[1], mul2(x[0], x[0]))));
+          float ss = sq.x + sq.y;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = r0 + r_first + i * kStep;
-          if (r0 + i * kStep + ((tid >> 5) % kWarps) * 2 >= rows) break;  // (warp-uniform)
-          uint2 out[2] = {raw[i][0], raw[i][1]};
-          if (r0 + i * kStep + ((tid >> 5) % kWarps) * 2 < hq + hkv) {  // the warp holds a query or key row
-            float x[8];
+          for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(FULL, ss, off);
+          const float2 inv = twice(rsqrtf(ss * (1.f / kHeadDim) + p.eps));
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float2 f = Pack<T>::to_f2(raw[i][k].x), g = Pack<T>::to_f2(raw[i][k].y);
-              x[4 * k] = f.x, x[4 * k + 1] = f.y, x[4 * k + 2] = g.x, x[4 * k + 3] = g.y;
-            }
-            float inv = 1.f;
-            if constexpr (NORM) {
-              float ss = 0.f;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
-#pragma unroll
-              for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(FULL, ss, off);
-              inv = rsqrtf(ss * (1.f / kHeadDim) + p.eps);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint2 w = r < hq ? wq[k] : wk[k];
-                const float2 f = Pack<T>::to_f2(w.x), g = Pack<T>::to_f2(w.y);
-                x[4 * k] *= f.x * inv, x[4 * k + 1] *= f.y * inv;
-                x[4 * k + 2] *= g.x * inv, x[4 * k + 3] *= g.y * inv;
-              }
-            }
-            if constexpr (MODE == kInterleaved) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (8 * l16 + 2 * k < d) {
-                  const float a = x[2 * k], b = x[2 * k + 1];
-                  x[2 * k] = a * cs[k].x - b * cs[k].y;
-                  x[2 * k + 1] = b * cs[k].x + a * cs[k].y;
-                }
-            } else if constexpr (MODE == kHalfPairs) {
-              if (split) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float a = x[k], b = x[4 + k];
-                  x[k] = a * cs[k].x - b * cs[k].y;
-                  x[4 + k] = b * cs[k].x + a * cs[k].y;
-                }
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) stage[8 * l16 + k] = x[k];
-              __syncwarp();
-              const int half = d >> 1;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int j = 8 * l16 + k;
-                if (j < d) {
-                  const bool low = j < half;
-                  const float2 c = cs_buf[buf][tok][low ? j : j - half];
-                  const float y = stage[low ? j + half : j - half];
-                  x[k] = x[k] * c.x + (low ? -y : y) * c.y;
-                }
-              }
-              __syncwarp();
-            }
-            if (r < hq + hkv) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                out[k] = make_uint2(Pack<T>::from_f2(x[4 * k], x[4 * k + 1]),
-                                    Pack<T>::from_f2(x[4 * k + 2], x[4 * k + 3]));
-            }
-          }
-          if (r < rows) {
-            T *dst = r < hq         ? static_cast<T *>(p.q_out) + ((int64_t)t * hq + r) * kHeadDim
-                     : r < hq + hkv ? static_cast<T *>(p.k_cache) + (slot * hkv + (r - hq)) * kHeadDim
-                                    : static_cast<T *>(p.v_cache) + (slot * hkv + (r - hq - hkv)) * kHeadDim;
-            if constexpr (MODE == kHalfPairs) {
-              *reinterpret_cast<uint2 *>(dst + d0) = out[0];
-              *reinterpret_cast<uint2 *>(dst + d1) = out[1];
-            } else {
-              *reinterpret_cast<uint4 *>(dst + d0) = make_uint4(out[0].x, out[0].y, out[1].x, out[1].y);
-            }
-          }
-          const int rn = r + kStep * kBatch;  // this buffer's next row
-          if (rn < rows) load(rn, raw[i]);
+          for (int i = 0; i < 4; ++i) x[i] = mul2(mul2(x[i], inv), weight[i]);
         }
-      }
+        if constexpr (MODE == kInterleaved) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (8 * l16 + 2 * i < d) {
+              const float cc = i & 1 ? c[i >> 1].y : c[i >> 1].x, sc = i & 1 ? s[i >> 1].y : s[i >> 1].x;
+              x[i] = make_float2(x[i].x * cc - x[i].y * sc, x[i].y * cc + x[i].x * sc);
+            }
+        } else if constexpr (MODE == kHalfPairs) {
+          if (split) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float2 a = x[i], b = x[2 + i];
+              x[i] = fma2(b, ns[i], mul2(a, c[i]));
+              x[2 + i] = fma2(a, s[i], mul2(b, c[i]));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) reinterpret_cast<float2 *>(stage)[4 * l16 + i] = x[i];
+          __syncwarp();
+          const int half = d >> 1;
+          auto turned = [&](int j, float y) {
+            if (j >= d) return y;
+            const bool low = j < half;
+            const float2 w = cs_buf[buf][tok][low ? j : j - half];
+            const float z = stage[low ? j + half : j - half];
+            return y * w.x + (low ? -z : z) * w.y;
+          };
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = make_float2(turned(8 * l16 + 2 * i, x[i].x), turned(8 * l16 + 2 * i + 1, x[i].y));
+          __syncwarp();
+        }
+        u[0] = make_uint2(Pack<T>::from_f2(x[0].x, x[0].y), Pack<T>::from_f2(x[1].x, x[1].y));
+        u[1] = make_uint2(Pack<T>::from_f2(x[2].x, x[2].y), Pack<T>::from_f2(x[3].x, x[3].y));
+      };
+      // All rows of a kind: n of them, this warp's from w on, this half-warp's
+      // first at src and dst; a buffer's next row is fetched once it is free.
+      auto sweep = [&](auto &raw, const T *src, T *dst, int n, int w, auto &&compute) {
+        constexpr int B = sizeof(raw) / sizeof(raw[0]);
+        for (; w < n; w += B * kStep, src += B * kStep * kHeadDim, dst += B * kStep * kHeadDim) {
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            if (w + i * kStep >= n) break;  // (warp-uniform)
+            const int r = w + i * kStep + (lane >> 4);
+            compute(raw[i]);
+            if (r < n) write(dst + i * kStep * kHeadDim, raw[i]);
+            if (r + B * kStep < n) read(src + (B + i) * kStep * kHeadDim, raw[i]);
+          }
+        }
+      };
+      auto weigh = [&](const void *of) {
+        if constexpr (NORM) {
+          uint2 u[2];
+          read(static_cast<const T *>(of), u);
+          widen(u, weight);
+        }
+      };
+      weigh(p.q_weight);
+      sweep(raw_q, q, static_cast<T *>(p.q_out) + ((int64_t)t * hq + r_qk) * kHeadDim, hq, w_qk, rotate);
+      weigh(p.k_weight);
+      sweep(raw_k, k, static_cast<T *>(p.k_cache) + (slot * hkv + r_qk) * kHeadDim, hkv, w_qk, rotate);
+      sweep(raw_v, v, static_cast<T *>(p.v_cache) + (slot * hkv + r_v) * kHeadDim, hkv, w_v, [](uint2 (&)[2]) {});
     }
     buf ^= 1;  // a thread is at most one step ahead of the slowest (the barrier), so two buffers do
   }
@@ -232,7 +257,7 @@ cudaError_t launch_rope_kv_typed(const RopeKvParams &p, int grid, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_rope_kv(const RopeKvParams &p, int dtype, int sms, cudaStream_t stream) {
-  const int cap = sms * 4;  // one wave: 4 CTAs fit on an SM
+  const int cap = sms * 3;  // one wave: 3 CTAs fit on an SM
   if (p.num_tokens <= cap) {  // a token per CTA
     return dtype == PA_BF16 ? launch_rope_kv_typed<__nv_bfloat16, 1>(p, p.num_tokens, stream)
                             : launch_rope_kv_typed<__half, 1>(p, p.num_tokens, stream);
