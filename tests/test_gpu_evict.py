@@ -135,6 +135,35 @@ def test_slices_past_shared_memory_in_place():
     _check(c, recent=100, sinks=7, in_place=True)
 
 
+@pytest.mark.parametrize("ctx", [700, 5000, 140000])
+@pytest.mark.parametrize("more", [0, 1, 20, 300])
+def test_infinite_weights_beside_tokens_that_stay_anyway(ctx, more):
+    """The leading bits of +inf and of the largest numbers are those of no other weight, and are held apart from the
+    first and last tokens' whatever those weigh: as many heavy tokens as may stay, a few more, many more."""
+    rng = np.random.default_rng(ctx + more)
+    budget, recent, sinks = 100, 30, 10
+    c = _case([ctx], 2, "bf16", 31, budget)
+    mid = np.arange(sinks, ctx - recent)
+    for h in range(2):
+        heavy = rng.choice(mid, budget - recent - sinks + more, replace=False)
+        c["w"][0, h, heavy] = np.inf if h else np.float32(3.4e38)
+    c["dev"]["w"].copy_(torch.from_numpy(c["w"]))
+    _check(c, recent, sinks)
+
+
+@pytest.mark.parametrize("ctx", [3000, 20000, 150000])
+@pytest.mark.parametrize("ties", [2, 31, 32, 33, 200])
+def test_ties_at_the_border_among_distinct_weights(ctx, ties):
+    rng = np.random.default_rng(ctx + ties)
+    budget = 257
+    c = _case([ctx], 2, "f16", 41, budget, stride=ctx + 3)  # (rows that do not start on 16 bytes)
+    c["w"][0, :, :ctx] = np.float32(1) + rng.permutation(ctx).astype(np.float32) / ctx
+    order = np.argsort(-c["w"][0, 0, :ctx])
+    c["w"][0, :, order[budget - 5 - 1:budget - 5 - 1 + ties]] = c["w"][0, 0, order[budget - 6]]
+    c["dev"]["w"].copy_(torch.from_numpy(c["w"]))
+    _check(c, 0, 5)
+
+
 def test_wider_and_narrower_weights():
     c = _case([300, 20], 2, "f16", 5, 64, stride=513)
     _check(c, 8, 2, out_stride=200)
