@@ -214,6 +214,16 @@ __device__ __forceinline__ void decode_page16(uint32_t stage, int nv, const uint
   }
 }
 
+// 5-D tiled load with an L2 eviction-priority hint.
+__device__ __forceinline__ void tma_load_5d_hint(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1,
+                                                 int c2, int c3, int c4, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // The join of online-softmax pieces for one head's 4 dims: pieces (m, l) with o
 // come U at a time (m = -inf: none).
 struct JoinState {
@@ -282,6 +292,7 @@ __device__ __forceinline__ bool split_producer16(const CUtensorMap &kmap, const 
   Cursor ic = locate(prefix, n, hkv, x0);
   int win_s = -1, win_base = -1, win_first = 0;
   int32_t win = -1;  // one of 32 block ids per lane
+  const uint64_t once = policy_evict_first();  // (a page is read once: it leaves L2 to what is read again)
   int st = 0, phase = 1;  // a fresh ring is free: the first waits pass
   bool ok_all = true;
   for (int x = 0; x < npages; ++x) {
@@ -312,8 +323,8 @@ __device__ __forceinline__ bool split_producer16(const CUtensorMap &kmap, const 
       ring.bad[st] = ok ? 0 : 1;
       if (ok) {
         mbar_arrive_expect_tx(&ring.full[st], STAGE);
-        tma_load_5d(stages + st * STAGE, &kmap, &ring.full[st], 0, 0, 0, ic.h, blk);
-        tma_load_5d(stages + st * STAGE + STAGE / 2, &vmap, &ring.full[st], 0, 0, 0, ic.h, blk);
+        tma_load_5d_hint(stages + st * STAGE, &kmap, &ring.full[st], 0, 0, 0, ic.h, blk, once);
+        tma_load_5d_hint(stages + st * STAGE + STAGE / 2, &vmap, &ring.full[st], 0, 0, 0, ic.h, blk, once);
       } else {
         set_error(p.err, PA_ERR_RANGE, ic.s);
         mbar_arrive(&ring.full[st]);
