@@ -674,8 +674,8 @@ PA_API pa_status pa_paged_attn_decode_shared(const void *q, const pa_kv_pool *po
  *                 clobbered.  Calls sharing one must not overlap on the GPU.
  * Scores, weights and sums are fp32.  A page with a block id outside the pool is
  * reported and its tokens get no weight.  16-bit pools; num_seqs * num_kv_heads
- * at most 65535 (else PA_ERR_UNSUPPORTED).  Other arguments and errors as
- * pa_paged_attn_decode.
+ * at most 65535, max_context_len at most 2^30 (else PA_ERR_UNSUPPORTED).  Other
+ * arguments and errors as pa_paged_attn_decode.
  */
 PA_API size_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                                 int32_t max_context_len);
@@ -701,17 +701,17 @@ PA_API pa_status pa_paged_attn_decode_weights(const void *q, const pa_kv_pool *p
  * n <= i < min(ctx, weights_out_stride), the rest of it is left; new_context_lens[s] = n.
  *   weights           fp32 [num_seqs][num_kv_heads][weights_stride].
  *   block_tables      int32 [num_seqs][max_blocks_per_seq].
- *   dst_block_tables  int32 [num_seqs][dst_max_blocks].  In place: block_tables
- *                     itself, or entries equal to its entries.  Apart: blocks that
- *                     no sequence of the call reads.  Blocks that sequences share
+ *   dst_block_tables  int32 [num_seqs][dst_max_blocks].  Each block a sequence's
+ *                     tokens go to is in place (the same entry of its block_tables)
+ *                     or apart: a block that no sequence of the call reads.  Blocks that sequences share
  *                     must not be rewritten in place (pa_sequence_unshare first).
  *   weights_out       fp32 [num_seqs][num_kv_heads][weights_out_stride]: weights
  *                     itself with the same stride (in place), or apart from it.
  *   kept              int32 [num_seqs][num_kv_heads][budget].
  *   new_context_lens  int32 [num_seqs], apart from context_lens.
  * budget >= 1, recent, sinks >= 0, recent + sinks <= budget; num_seqs at most
- * 16384.  A sequence whose length is 0, beyond its table or beyond
- * weights_stride, or whose n does not fit dst_max_blocks or
+ * 16384, budget at most 2^30.  A sequence whose length is 0, beyond 2^30, its
+ * table or weights_stride, or whose n does not fit dst_max_blocks or
  * weights_out_stride, records PA_ERR_RANGE (detail: the sequence) and nothing
  * of it is written.  A block id outside the pool, in either table, is recorded
  * likewise and its rows are not moved.  The result does not depend on the

@@ -118,7 +118,7 @@ __device__ __forceinline__ void load_groups(const SharedParams &p, SharedPlan &p
       size = __ldg(p.group_sizes + g);
       n = __ldg(p.prefix_lens + g);
       const bool bad_size = size < 0 || size > p.num_seqs;
-      const bool bad_len = n < 0 || n % kBlock != 0 || n > p.max_blocks_per_seq * kBlock;
+      const bool bad_len = n < 0 || n % kBlock != 0 || n > (int64_t)p.max_blocks_per_seq * kBlock;
       bad = bad_size || bad_len;
       if (bad_size) size = 0;
       if (bad_len || size < 2) n = 0;
@@ -307,7 +307,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   scan_pages_of<kThreads>(sp.num_seqs, prefix, warp_tot, [&](int s) {
     const int ctx = __ldg(dp.context_lens + s);
     const int g = group_of(pl.end, sp.num_groups, s), len = g < sp.num_groups ? pl.len[g] : 0;
-    if (ctx >= 1 && ctx <= sp.max_blocks_per_seq * kBlock && ctx >= len)
+    if (ctx >= 1 && ctx <= (int64_t)sp.max_blocks_per_seq * kBlock && ctx >= len)
       return (ctx + kBlock - 1) / kBlock - len / kBlock;
     if (scribe) set_error(sp.err, PA_ERR_RANGE, s);
     return 0;
@@ -712,7 +712,7 @@ shared_join_kernel(const SharedParams sp, const DecodeParams p) {
   const int2 head = __ldcg(reinterpret_cast<const int2 *>(tb.head));
   const int ctx = __ldg(p.context_lens + s), len = rec.len;
   const int m0 = __ldcg(p.meta + s), m1 = __ldcg(p.meta + s + 1), mn = __ldcg(p.meta + p.num_seqs);
-  if (ctx < 1 || ctx > p.max_blocks_per_seq * kBlock || ctx < len) return;  // reported; its rows are left
+  if (ctx < 1 || ctx > (int64_t)p.max_blocks_per_seq * kBlock || ctx < len) return;  // reported; its rows are left
   // the suffix's pieces: slots item + wf ..
   const int pages = m1 - m0;
   const int64_t P = (int64_t)mn * hkv;

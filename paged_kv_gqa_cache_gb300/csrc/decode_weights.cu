@@ -52,7 +52,7 @@ decode_scores_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
   griddep_wait();
   scan_pages_of<kScoreThreads>(p.num_seqs, prefix, warp_tot, [&](int s) {
     const int ctx = __ldg(p.context_lens + s);
-    if (ctx >= 1 && ctx <= p.max_blocks_per_seq * kBlock && ctx <= max_len) return (ctx + kBlock - 1) / kBlock;
+    if (ctx >= 1 && ctx <= (int64_t)p.max_blocks_per_seq * kBlock && ctx <= max_len) return (ctx + kBlock - 1) / kBlock;
     if (blockIdx.x == 0) set_error(p.err, PA_ERR_RANGE, s);
     return 0;
   });

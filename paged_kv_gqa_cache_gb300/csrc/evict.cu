@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv_evict_kernel(const EvictPara
   griddep_wait();  // weights, lengths, tables and pool may come from the previous kernel
   const int ctx = __ldg(p.context_lens + s);
   const int n = min(ctx, p.budget);  // tokens that stay
-  if (ctx < 1 || (int64_t)ctx > (int64_t)p.max_blocks_per_seq * kBlock || ctx > p.weights_stride ||
+  if (ctx < 1 || ctx > kLongMaxTokens || (int64_t)ctx > (int64_t)p.max_blocks_per_seq * kBlock || ctx > p.weights_stride ||
       (int64_t)n > (int64_t)p.dst_max_blocks * kBlock || n > p.out_stride) {  // uniform over the cluster
     if (h == 0 && rank == 0 && tid == 0) set_error(p.err, PA_ERR_RANGE, s);
     return;

@@ -921,6 +921,7 @@ pa_status pa_paged_attn_decode_weights(const void *q, const pa_kv_pool *pool, co
   if (!weights_out) return PA_ERR_NULL;
   if (weights_stride < max_context_len) return PA_ERR_SHAPE;
   if ((int64_t)num_seqs * pool->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;  // a launch's second dimension
+  if (max_context_len > kLongMaxTokens) return PA_ERR_UNSUPPORTED;
   if (!aligned4(weights_in) || !aligned4(weights_out)) return PA_ERR_ALIGN;
   if (!workspace) return PA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PA_ERR_ALIGN;
@@ -974,7 +975,7 @@ pa_status pa_kv_evict(const pa_kv_pool *pool, const int32_t *block_tables, int32
   // in place, or apart: rows of another stride would overlap other rows of the source
   if (weights_out == weights && weights_out_stride != weights_stride) return PA_ERR_SHAPE;
   if (dst_block_tables == block_tables && dst_max_blocks != max_blocks_per_seq) return PA_ERR_SHAPE;
-  if (num_seqs > 16384) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 16384 || budget > kLongMaxTokens) return PA_ERR_UNSUPPORTED;
   if (!aligned4(block_tables) || !aligned4(context_lens) || !aligned4(weights) || !aligned4(dst_block_tables) ||
       !aligned4(weights_out) || !aligned4(kept) || !aligned4(new_context_lens))
     return PA_ERR_ALIGN;

@@ -60,6 +60,7 @@ def test_rope_kv_write_refusals(lib, kw, status):
     (dict(new=P), "PA_ERR_SHAPE"), (dict(w_out=P, out_stride=99), "PA_ERR_SHAPE"),
     (dict(dst=P, dst_blocks=3), "PA_ERR_SHAPE"), (dict(stride=0), "PA_ERR_SHAPE"), (dict(mb=0), "PA_ERR_SHAPE"),
     (dict(S=16385), "PA_ERR_UNSUPPORTED"), (dict(w=P + 2), "PA_ERR_ALIGN"), (dict(kept=P + 2), "PA_ERR_ALIGN"),
+    (dict(budget=2 ** 30 + 1), "PA_ERR_UNSUPPORTED"), (dict(budget=2 ** 31 - 1), "PA_ERR_UNSUPPORTED"),
     (dict(pool=_pool(num_blocks=0)), "PA_ERR_SHAPE"), (dict(pool=_pool(k_cache=0)), "PA_ERR_NULL"),
 ])
 def test_kv_evict_refusals(lib, kw, status):
@@ -77,12 +78,14 @@ def test_kv_evict_refusals(lib, kw, status):
     (dict(hq=12), "PA_ERR_SHAPE"), (dict(scale=0.0), "PA_ERR_SHAPE"), (dict(w_in=P + 2), "PA_ERR_ALIGN"),
     (dict(w_out=P + 2), "PA_ERR_ALIGN"), (dict(ws=P + 8), "PA_ERR_ALIGN"), (dict(S=9000, wsb=1 << 40), "PA_ERR_UNSUPPORTED"),
     (dict(pool=_pool(dtype=5)), "PA_ERR_DTYPE"),
+    (dict(mb=2 ** 27, mcl=2 ** 30 + 1, stride=2 ** 31 - 1, wsb=2 ** 62), "PA_ERR_UNSUPPORTED"),
+    (dict(mb=2 ** 27, mcl=2 ** 31 - 1, stride=2 ** 31 - 1, wsb=2 ** 62), "PA_ERR_UNSUPPORTED"),
 ])
 def test_decode_weights_refusals(lib, kw, status):
     S, mcl = kw.get("S", 4), kw.get("mcl", 256)
     need = lib.pa_decode_weights_workspace_bytes(max(S, 1), kw.get("hq", 16), 8, max(mcl, 1))
     wsb = kw.get("wsb", need)
-    st = lib.pa_paged_attn_decode_weights(kw.get("q", P), ctypes.byref(kw.get("pool", _pool())), P, 16, P, S,
+    st = lib.pa_paged_attn_decode_weights(kw.get("q", P), ctypes.byref(kw.get("pool", _pool())), P, kw.get("mb", 16), P, S,
                                           kw.get("hq", 16), mcl, kw.get("scale", 0.1), kw.get("w_in", P),
                                           kw.get("w_out", P), kw.get("stride", 256), P, kw.get("ws", P),
                                           need - 1 if wsb == -1 else wsb, None)
