@@ -666,7 +666,7 @@ PA_API pa_status pa_paged_attn_decode_shared(const void *q, const pa_kv_pool *po
  * for j < context_lens[s]; entries from context_lens[s] on are not touched.
  *   weights_in, weights_out  fp32 [num_seqs][num_kv_heads][weights_stride],
  *                 weights_stride >= max_context_len; weights_in NULL: zeros;
- *                 weights_out may be weights_in, else they must not overlap.
+ *                 weights_out may be weights_in, else they must not overlap (PA_ERR_SHAPE).
  *   max_context_len  also the longest sequence that is computed: a longer one
  *                 records PA_ERR_RANGE as one beyond its block table does.
  *   workspace     at least pa_decode_weights_workspace_bytes(...) bytes, 16-byte
@@ -708,7 +708,8 @@ PA_API pa_status pa_paged_attn_decode_weights(const void *q, const pa_kv_pool *p
  *   weights_out       fp32 [num_seqs][num_kv_heads][weights_out_stride]: weights
  *                     itself with the same stride (in place), or apart from it.
  *   kept              int32 [num_seqs][num_kv_heads][budget].
- *   new_context_lens  int32 [num_seqs], apart from context_lens.
+ *   new_context_lens  int32 [num_seqs], apart from context_lens.  (Weights or lengths
+ *                     that overlap otherwise: PA_ERR_SHAPE.)
  * budget >= 1, recent, sinks >= 0, recent + sinks <= budget; num_seqs at most
  * 16384, budget at most 2^30.  A sequence whose length is 0, beyond 2^30, its
  * table or weights_stride, or whose n does not fit dst_max_blocks or

@@ -289,6 +289,12 @@ pa_status decode_call(const void *q, int dtype, const pa_kv_pool *pool16, const 
 
 // The checks pa_paged_attn_decode makes before it looks at its workspace, in
 // the same order, for the allocation-free entry point (which has none).
+// Do two buffers of these many bytes share any?
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < na : x - y < nb;
+}
+
 pa_status decode_check_args(const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
                             int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
                             int32_t num_q_heads, int32_t max_context_len, float scale, void *out) {
@@ -923,6 +929,9 @@ pa_status pa_paged_attn_decode_weights(const void *q, const pa_kv_pool *pool, co
   if ((int64_t)num_seqs * pool->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;  // a launch's second dimension
   if (max_context_len > kLongMaxTokens) return PA_ERR_UNSUPPORTED;
   if (!aligned4(weights_in) || !aligned4(weights_out)) return PA_ERR_ALIGN;
+  const size_t weight_bytes = (size_t)num_seqs * pool->num_kv_heads * weights_stride * sizeof(float);
+  if (weights_in && weights_in != weights_out && overlap(weights_in, weight_bytes, weights_out, weight_bytes))
+    return PA_ERR_SHAPE;
   if (!workspace) return PA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PA_ERR_ALIGN;
   if (workspace_bytes < pa_decode_weights_workspace_bytes(num_seqs, num_q_heads, pool->num_kv_heads, max_context_len))
@@ -979,6 +988,11 @@ pa_status pa_kv_evict(const pa_kv_pool *pool, const int32_t *block_tables, int32
   if (!aligned4(block_tables) || !aligned4(context_lens) || !aligned4(weights) || !aligned4(dst_block_tables) ||
       !aligned4(weights_out) || !aligned4(kept) || !aligned4(new_context_lens))
     return PA_ERR_ALIGN;
+  const size_t rows = (size_t)num_seqs * pool->num_kv_heads, lens_bytes = (size_t)num_seqs * sizeof(int32_t);
+  if (weights_out != weights && overlap(weights, rows * weights_stride * sizeof(float), weights_out,
+                                        rows * weights_out_stride * sizeof(float)))
+    return PA_ERR_SHAPE;
+  if (overlap(context_lens, lens_bytes, new_context_lens, lens_bytes)) return PA_ERR_SHAPE;
   DeviceState *d = nullptr;
   if ((st = device_state(&d)) != PA_OK) return st;
   EvictParams p{};

@@ -61,6 +61,9 @@ def test_rope_kv_write_refusals(lib, kw, status):
     (dict(dst=P, dst_blocks=3), "PA_ERR_SHAPE"), (dict(stride=0), "PA_ERR_SHAPE"), (dict(mb=0), "PA_ERR_SHAPE"),
     (dict(S=16385), "PA_ERR_UNSUPPORTED"), (dict(w=P + 2), "PA_ERR_ALIGN"), (dict(kept=P + 2), "PA_ERR_ALIGN"),
     (dict(budget=2 ** 30 + 1), "PA_ERR_UNSUPPORTED"), (dict(budget=2 ** 31 - 1), "PA_ERR_UNSUPPORTED"),
+    (dict(w_out=P + 4), "PA_ERR_SHAPE"), (dict(w=P + (1 << 20), w_out=P + (1 << 20) - 4), "PA_ERR_SHAPE"),
+    (dict(w_out=P + 4 * 8 * 256 * 4 - 4), "PA_ERR_SHAPE"), (dict(new=P + 12), "PA_ERR_SHAPE"),
+    (dict(new=P - 12), "PA_ERR_SHAPE"),
     (dict(pool=_pool(num_blocks=0)), "PA_ERR_SHAPE"), (dict(pool=_pool(k_cache=0)), "PA_ERR_NULL"),
 ])
 def test_kv_evict_refusals(lib, kw, status):
@@ -78,6 +81,8 @@ def test_kv_evict_refusals(lib, kw, status):
     (dict(hq=12), "PA_ERR_SHAPE"), (dict(scale=0.0), "PA_ERR_SHAPE"), (dict(w_in=P + 2), "PA_ERR_ALIGN"),
     (dict(w_out=P + 2), "PA_ERR_ALIGN"), (dict(ws=P + 8), "PA_ERR_ALIGN"), (dict(S=9000, wsb=1 << 40), "PA_ERR_UNSUPPORTED"),
     (dict(pool=_pool(dtype=5)), "PA_ERR_DTYPE"),
+    (dict(w_out=P + 4), "PA_ERR_SHAPE"), (dict(w_out=P + 4 * 8 * 256 * 4 - 4), "PA_ERR_SHAPE"),
+    (dict(w_in=P + 512), "PA_ERR_SHAPE"),
     (dict(mb=2 ** 27, mcl=2 ** 30 + 1, stride=2 ** 31 - 1, wsb=2 ** 62), "PA_ERR_UNSUPPORTED"),
     (dict(mb=2 ** 27, mcl=2 ** 31 - 1, stride=2 ** 31 - 1, wsb=2 ** 62), "PA_ERR_UNSUPPORTED"),
 ])
