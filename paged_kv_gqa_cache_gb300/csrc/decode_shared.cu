@@ -25,12 +25,18 @@
 //           decode_mma.cuh: the softmax warps consume, the loader and MMA warps
 //           produce.  Their stages (8 x 3 x 8 KB) take the very 192 KB of the query
 //           tile and the K and V rings, so the first pages are on their way when
-//           the last P V has completed, while the query tile is still stored.  (As a kernel of its own behind the prefix the suffix paid a
-//           launch, a schedule and a first trip to HBM, 57 us for 32 sequences
-//           and 32768 shared tokens; beside it on SMs of its own 54, but 139
-//           against 122 us where groups are large: its stream pushed the shared
-//           keys out of L2.)
+//           the last P V has completed, while the query tile is still stored.
+//           (As a kernel of its own behind the prefix the suffix paid a launch, a
+//           schedule and a first trip to HBM: 57 us for 32 sequences and 32768
+//           shared tokens, 122 for 192 in three groups.  Beside the prefix on SMs
+//           of its own 54 and 139: its stream pushed the shared keys out of L2.
+//           With half of the CTAs starting with the suffix 49.7 and 100.5.)
 //   join    A warp per (sequence, KV head, part of the dims) adds up the pieces.
+// Measured, 32 / 8 heads, bf16: 32 sequences, 32768 shared tokens and up to 1000
+// each: 47.8 us (4.2 TB/s; HBM in both parts, and the ramps between them); 192 in
+// three groups of 4096 to 16384, up to 700 each: 99.0 us (a large group's keys
+// cross from L2 once per query tile, 64 KB a key tile).  4 sequences, 1024 shared,
+// up to 200 each, 16 / 8 heads: 9.7 us, a chain of latencies.
 #include "decode_mma.cuh"
 #include "prefill_kernel.cuh"
 
@@ -61,6 +67,7 @@ struct PBars {
 constexpr int kBarBytes = 1024;
 static_assert(sizeof(PBars) <= kBarBytes, "barriers");
 static_assert(kSoftmaxWarps * kStages * STAGE <= P_OFF_X, "the suffix workers' stages fit the rings");
+static_assert(kKLoad * kStages * STAGE <= P_OFF_V, "the K loaders' lie in front of V");
 
 // The groups and the order of the prefix work.  Group g: sequences end[g - 1]
 // .. end[g] - 1, len[g] shared tokens; its pairs start at pairs[g], its units
@@ -473,6 +480,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   } else {
     // every loader and MMA warp runs this one decrease (setmaxnreg acts on whole warpgroups)
     regs_dec<kRegsOther>();
+    int key_tiles = 0;  // a loader warp's, over all runs
     if (warp != kWarpMma) {
       // ---------------- loader warps ----------------
       // Warps 0 .. 3 load K, each 4 of a key tile's 16 boxes (the 64-dim half b %
@@ -578,6 +586,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           issued = c + 1;
         }
       }
+      key_tiles = c;
       if (timed_out) {  // a short, bounded chance for this warp's copies in flight to land
         if (lw == 0 && ui > 0) mbar_wait(&bars.q_full, (ui - 1) & 1, kWaitLimitNs / 8);
         const int n = for_k ? kPKStages : kPVStages;
@@ -675,8 +684,15 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       }
     }
     // ---------------- the suffix: this warp fetches consumer warp - 8's pages ----------------
-    // The rings are idle once every MMA has completed: each copy was consumed by one.
-    if (x0 < x1 && !timed_out && !mbar_wait(&bars.idle, 0)) timed_out = true;
+    // The rings are idle once every MMA has completed: each copy was consumed by
+    // one.  The K loaders' stages lie where Q and K were, idle when the last Q K^T
+    // has completed (they have seen the one two before, on the same barrier).
+    if (x0 < x1 && !timed_out) {
+      const int last = key_tiles - 1;
+      if (!(warp < kWarpLoad0 + kKLoad ? mbar_wait(&bars.s_full[last % kPKStages], (last / kPKStages) & 1)
+                                       : mbar_wait(&bars.idle, 0)))
+        timed_out = true;
+    }
     timed_out = __any_sync(FULL, timed_out);
     if (!timed_out && !suffix_worker<T, G, false>(kpage, vmap, sp, dp, pl, smem, bars, prefix)) timed_out = true;
     regs_wait_taken();  // (the softmax warps hold their registers by now)

@@ -13,13 +13,17 @@
 // takes kChunkKeys keys, first joining the (m, l) of the item's fragments
 // itself (a few hundred bytes), so that no CTA waits for another.
 // HBM-bound: K and V once; the scores and weights stream at 8 G + 8 bytes a key.
+// 32 sequences of 100 to 8192 tokens, 32 / 8 heads, bf16: 95.5 .. 96.3 us (5.4
+// TB/s; the split pass 86, at 6.0), 5 of 40000 to 100001, 32 / 4 heads: 153.8 ..
+// 155.4 (5.4 TB/s; the split pass 137).  One sequence of 777: 7.6 us, of which the
+// split pass takes 4.7.
 #include "decode_mma.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kChunkKeys = 2048;
-constexpr int kJoinPieces = 8;  // fragments in flight (4: weights-long 4 us slower)
+constexpr int kChunkKeys = 2048;  // (1024: 97.5 and 157.4 us for the two batches below, 4096: 96.6 and 153.5)
+constexpr int kJoinPieces = 8;    // fragments in flight (4: 97.3 and 161.4; 16: 98.3 and 154.7)
 constexpr int kWeightThreads = 256;
 constexpr int kKeysPerThread = kChunkKeys / kWeightThreads;
 static_assert(kWeightThreads / 32 >= 8, "a warp per query head of a KV head");
