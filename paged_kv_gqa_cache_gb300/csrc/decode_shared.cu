@@ -20,7 +20,7 @@
 //           then the key range is cut into blocks about as long as a CTA's share,
 //           the query tiles of a block next to each other in the order, so that
 //           the CTAs that need the same keys run at the same time and all but one
-//           of them read L2.
+//           of them read L2 (mostly: of 126 MB of shared keys 172 come from HBM).
 //           Suffix: the rest of each sequence, by the split workers of
 //           decode_mma.cuh: the softmax warps consume, the loader and MMA warps
 //           produce.  Their stages (8 x 3 x 8 KB) take the very 192 KB of the query
@@ -33,10 +33,11 @@
 //           With half of the CTAs starting with the suffix 49.7 and 100.5.)
 //   join    A warp per (sequence, KV head, part of the dims) adds up the pieces.
 // Measured, 32 / 8 heads, bf16: 32 sequences, 32768 shared tokens and up to 1000
-// each: 47.8 us (4.2 TB/s; HBM in both parts, and the ramps between them); 192 in
-// three groups of 4096 to 16384, up to 700 each: 99.0 us (a large group's keys
-// cross from L2 once per query tile, 64 KB a key tile).  4 sequences, 1024 shared,
-// up to 200 each, 16 / 8 heads: 9.7 us, a chain of latencies.
+// each: 46.8 us (4.3 TB/s; HBM in both parts, 1.6 us a pair, and the ramps; the
+// join takes 3 us); 192 in three groups of 4096 to 16384, up to 700 each: 98.6 us
+// (4.4 TB/s; a pair of a large group 1.0 us: 160 KB through shared memory, 64 in
+// by TMA, 64 to Q K^T and 32 to P V, are 0.67; the join takes 9).  4 sequences,
+// 1024 shared, up to 200 each, 16 / 8 heads: 9.7 us, a chain of latencies.
 #include "decode_mma.cuh"
 #include "prefill_kernel.cuh"
 

@@ -97,8 +97,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 // Add 1 to a word of shared memory if key < bound, by predicate.
 __device__ __forceinline__ void tally_below(uint32_t addr, uint32_t key, uint32_t bound) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %1, %2;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(addr), "r"(key), "r"(bound)
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %1, %2;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(addr), "r"(key),
+      "r"(bound)
+      : "memory");
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -141,8 +143,9 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv_evict_kernel(const EvictPara
   griddep_wait();  // weights, lengths, tables and pool may come from the previous kernel
   const int ctx = __ldg(p.context_lens + s);
   const int n = min(ctx, p.budget);  // tokens that stay
-  if (ctx < 1 || ctx > kLongMaxTokens || (int64_t)ctx > (int64_t)p.max_blocks_per_seq * kBlock || ctx > p.weights_stride ||
-      (int64_t)n > (int64_t)p.dst_max_blocks * kBlock || n > p.out_stride) {  // uniform over the cluster
+  if (ctx < 1 || ctx > kLongMaxTokens || (int64_t)ctx > (int64_t)p.max_blocks_per_seq * kBlock ||
+      ctx > p.weights_stride || (int64_t)n > (int64_t)p.dst_max_blocks * kBlock ||
+      n > p.out_stride) {  // uniform over the cluster
     if (h == 0 && rank == 0 && tid == 0) set_error(p.err, PA_ERR_RANGE, s);
     return;
   }
@@ -386,7 +389,8 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv_evict_kernel(const EvictPara
       const uint32_t ls = sure + is - __popc(ma), lt = tie + it - __popc(mb);  // before this lane's 32
       // of its ties the first left - lt stay
       uint32_t m = mb;  // (of this lane's 32 tokens)
-      for (int drop = (int)min((int64_t)__popc(mb), max((int64_t)0, (int64_t)lt + __popc(mb) - (int64_t)left)); drop > 0; --drop)
+      const int nb = __popc(mb);
+      for (int drop = (int)min((int64_t)nb, max((int64_t)0, (int64_t)lt + nb - (int64_t)left)); drop > 0; --drop)
         m &= ~(0x80000000u >> __clz(m));
       m |= ma;
       // The masks are written out by all lanes: of steps <= 2^lg masks each lane
@@ -426,7 +430,8 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv_evict_kernel(const EvictPara
   const int64_t row_vecs = (int64_t)hkv * (kHeadDim * 2 / 16);  // 16-byte vectors per token of a pool
   const uint4 *kin = static_cast<const uint4 *>(p.k_cache), *vin = static_cast<const uint4 *>(p.v_cache);
   uint4 *kout = static_cast<uint4 *>(p.k_cache), *vout = static_cast<uint4 *>(p.v_cache);
-  const int j_first = rank * kEvHalfWarps + hw, j_step = C * kEvHalfWarps;  // row i of group g: j_first + (g R + i) j_step
+  // row i of group g: j_first + (g R + i) j_step
+  const int j_first = rank * kEvHalfWarps + hw, j_step = C * kEvHalfWarps;
   auto move = [&](auto rows_per_group) {
     constexpr int R = decltype(rows_per_group)::value;
     const int group = R * j_step;  // new positions per group

@@ -263,7 +263,8 @@ cudaError_t launch_prefill8(const PrefillParams &p, const CUtensorMap &kmap, con
                             cudaStream_t stream);
 
 // ---- decode over prefixes shared by groups of sequences (16-bit pools) -----------
-constexpr int kLongMaxTokens = 1 << 30;  // of a sequence in pa_kv_evict and pa_paged_attn_decode_weights: token indices are 32-bit
+// Tokens of a sequence in pa_kv_evict and pa_paged_attn_decode_weights (indices are 32-bit).
+constexpr int kLongMaxTokens = 1 << 30;
 constexpr int kMaxPrefixGroups = 256;
 constexpr int kSharedMaxSeqs = 6000;  // their page prefix in shared memory
 struct SharedParams {

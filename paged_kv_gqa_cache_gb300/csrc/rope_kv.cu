@@ -45,7 +45,7 @@ namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kRopeKvThreads = 256;
-constexpr int kBatchQ = 4, kBatchKv = 2;  // rows per half-warp whose loads are in flight together: queries; keys and values
+constexpr int kBatchQ = 4, kBatchKv = 2;  // rows of a kind per half-warp whose loads are in flight together
 
 // kPairs: a lane holds both values of its pairs (interleaved, or half with
 // rotary_dim a multiple of 8); kExchange: any even rotary_dim in the half
@@ -58,19 +58,6 @@ __device__ __forceinline__ long long turns_fixed(double inv_freq) {
   return __double2ll_rn((t - rint(t)) * 18446744073709551616.0);
 }
 
-// Two fp32 values in one operation.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-  return reinterpret_cast<float2 &>(d);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(d)
-      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
-  return reinterpret_cast<float2 &>(d);
-}
 __device__ __forceinline__ float2 twice(float a) { return make_float2(a, a); }
 
 // TOK tokens per CTA and step, 8 / TOK warps each.
@@ -161,13 +148,15 @@ __global__ void __launch_bounds__(kRopeKvThreads, 3) rope_kv_kernel(const RopeKv
         float2 x[4];
         widen(u, x);
         if constexpr (NORM) {
-          const float2 sq = fma2(x[3], x[3], fma2(x[2], x[2], fma2(x[1], x[1], mul2(x[0], x[0]))));
+          float2 sq = __fmul2_rn(x[0], x[0]);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) sq = __ffma2_rn(x[i], x[i], sq);
           float ss = sq.x + sq.y;
 #pragma unroll
           for (int off = 8; off > 0; off >>= 1) ss += __shfl_xor_sync(FULL, ss, off);
           const float2 inv = twice(rsqrtf(ss * (1.f / kHeadDim) + p.eps));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = mul2(mul2(x[i], inv), weight[i]);
+          for (int i = 0; i < 4; ++i) x[i] = __fmul2_rn(__fmul2_rn(x[i], inv), weight[i]);
         }
         if constexpr (MODE == kInterleaved) {
 #pragma unroll
@@ -181,8 +170,8 @@ __global__ void __launch_bounds__(kRopeKvThreads, 3) rope_kv_kernel(const RopeKv
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float2 a = x[i], b = x[2 + i];
-              x[i] = fma2(b, ns[i], mul2(a, c[i]));
-              x[2 + i] = fma2(a, s[i], mul2(b, c[i]));
+              x[i] = __ffma2_rn(b, ns[i], __fmul2_rn(a, c[i]));
+              x[2 + i] = __ffma2_rn(a, s[i], __fmul2_rn(b, c[i]));
             }
           }
         } else {
