@@ -1022,13 +1022,15 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
     if kept is None:
         kept = torch.empty((S, hkv, max(budget, 0)), dtype=i32, device=block_tables.device)
         fresh.append(kept)
+    elif not _fine(dev, i32, kept) or kept.shape != (S, hkv, budget):
+        _check_all(dev, (kept, "kept", i32))
+        raise ValueError(f"kept must be [{S}, {hkv}, {budget}]")
     if new_context_lens is None:
         new_context_lens = torch.empty_like(context_lens)
         fresh.append(new_context_lens)
-    if not _fine(dev, i32, kept, new_context_lens):
-        _check_all(dev, (kept, "kept", i32), (new_context_lens, "new_context_lens", i32))
-    if kept.shape != (S, hkv, budget) or new_context_lens.shape != (S,):
-        raise ValueError(f"kept must be [{S}, {hkv}, {budget}], new_context_lens [{S}]")
+    elif not _fine(dev, i32, new_context_lens) or new_context_lens.shape != (S,):
+        _check_all(dev, (new_context_lens, "new_context_lens", i32))
+        raise ValueError(f"new_context_lens must be [{S}]")
     _check((_lib or load_library()).pa_kv_evict(
         ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, weights.data_ptr(), ws[2], budget,
         recent, sinks, dst.data_ptr(), dst.shape[1], w_out.data_ptr(), wos[2], kept.data_ptr(),
