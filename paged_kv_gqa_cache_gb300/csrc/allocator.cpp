@@ -25,6 +25,7 @@
 // library; a caller that keeps such a cache passes the shared blocks to
 // pa_sequence_adopt_prefix.
 #include <deque>
+#include <exception>
 #include <vector>
 
 #include "pagedattn.h"
@@ -225,6 +226,11 @@ pa_status pa_sequence_unshare(pa_sequence *seq, int32_t n) {
   size_t fresh = 0;
   for (int32_t i = 0; i < n; ++i) fresh += a->refcount[seq->blocks[i]] > 1;
   if (fresh > a->free_list.size()) return PA_ERR_NO_BLOCKS;
+  try {  // (nothing below allocates then: all or nothing, and no exception through a C entry)
+    a->copies.reserve(a->copies.size() + 2 * fresh);
+  } catch (const std::exception &) {
+    return PA_ERR_NO_BLOCKS;
+  }
   for (int32_t i = 0; i < n; ++i) {
     const int32_t src = seq->blocks[i];
     if (a->refcount[src] <= 1) continue;
