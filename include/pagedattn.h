@@ -634,10 +634,9 @@ PA_API pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, c
  *                 device: it depends on its SM count), 16-byte aligned; its
  *                 contents need no initialisation and are clobbered.  Calls
  *                 sharing one must not overlap on the GPU.
- * The query-key and probability-value products of the prefix run on the tensor
- * cores with fp32 accumulation; the probabilities enter the second rounded to
- * the pool dtype, as in pa_paged_attn_prefill_chunk, or, where a group has at
- * most 128 query rows per KV head, in two terms.  A negative group size, a
+ * The query-key and probability-value products run on the tensor cores with
+ * fp32 accumulation; the probabilities enter the second in two terms of the
+ * pool dtype, whatever the size of a group.  A negative group size, a
  * group past num_seqs, and a prefix length that is negative, not a multiple of
  * 16 or beyond the block table record PA_ERR_RANGE (detail: the group); such a
  * group shares nothing and its sequences are computed from their own tables.  A

@@ -33,11 +33,12 @@
 //           With half of the CTAs starting with the suffix 49.7 and 100.5.)
 //   join    A warp per (sequence, KV head, part of the dims) adds up the pieces.
 // Measured, 32 / 8 heads, bf16: 32 sequences, 32768 shared tokens and up to 1000
-// each: 46.8 us (4.3 TB/s; HBM in both parts, 1.6 us a pair, and the ramps; the
-// join takes 3 us); 192 in three groups of 4096 to 16384, up to 700 each: 98.6 us
-// (4.4 TB/s; a pair of a large group 1.0 us: 160 KB through shared memory, 64 in
-// by TMA, 64 to Q K^T and 32 to P V, are 0.67; the join takes 9).  4 sequences,
-// 1024 shared, up to 200 each, 16 / 8 heads: 9.7 us, a chain of latencies.
+// each: 46.1 us (4.3 TB/s; HBM in both parts, 1.6 us a pair, and the ramps; the
+// join takes 3 us); 192 in three groups of 4096 to 16384, up to 700 each: 100.5 us
+// (4.3 TB/s; a pair of a large group 1.0 us: 192 KB through shared memory, 64 in
+// by TMA, 64 to Q K^T and 64 to P V, are 0.8; the join takes 9; 98.5 us with P in
+// one term).  4 sequences, 1024 shared, up to 200 each, 16 / 8 heads: 9.7 us, a
+// chain of latencies.
 #include "decode_mma.cuh"
 #include "prefill_kernel.cuh"
 
@@ -195,7 +196,6 @@ __device__ __forceinline__ int share_owner(int y, int W, int n) {
 // A run of pairs of one unit: key tiles ka .. kb - 1 of query tile mt.
 struct PUnit {
   int g, h, mt, ka, kb, kt_last, unit, seq0, size, len;
-  bool two_terms;
 };
 template <int G>
 __device__ __forceinline__ PUnit punit_at(const SharedPlan &pl, int x, int x_end) {
@@ -222,7 +222,6 @@ __device__ __forceinline__ PUnit punit_at(const SharedPlan &pl, int x, int x_end
   u.kb = u.ka + min(bl - r, x_end - x);
   u.kt_last = s.kt - 1;
   u.unit = pl.units[lo] + (u.h * s.blocks + j) * s.mt + u.mt;
-  u.two_terms = s.mt == 1;
   return u;
 }
 
@@ -256,9 +255,10 @@ __device__ __forceinline__ bool suffix_worker(const CUtensorMap &kpage, const CU
 // load, warp 15 owns the tensor memory and issues the MMAs.  A run's Q is
 // loaded once the previous run's last Q K^T has completed (q_free); its first
 // P V product waits until the previous run's epilogue has read O (o_free).
-// P goes into P V rounded to the 16-bit type where a group has several query
-// tiles (tensor-bound), and in two terms where it has one (HBM-bound: the 8
-// more MMAs per key tile, 0.26 us, find the tensor core idle).
+// P goes into P V in two terms, P_hi = round(P) and P_lo = round(P - P_hi), like
+// the suffix's, whatever the group's size: a sequence's output does not lose
+// precision because others joined its group.  The 8 more MMAs per key tile are
+// 0.26 us of tensor time.
 // Then warp i < 8 consumes and warp 8 + i fetches the pages of a suffix worker.
 template <typename T, int G>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -358,9 +358,9 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         tc::wait_ld();
         const bool full = kb + 63 <= span;  // (the same in every thread of the half)
         const bool first = m_ref == -INFINITY;  // nothing accumulated for this row yet
-        const bool common = !U.two_terms && __all_sync(FULL, full && !first);
+        const bool common = __all_sync(FULL, full && !first);
         float mx = -INFINITY, ls = 0.f;
-        if (common) ls = exp_pack_store<T, false>(v, s_addr, sl2, m_ref, true, kb, span);
+        if (common) ls = exp_pack_store<T, true>(v, s_addr, sl2, m_ref, true, kb, span);
         if (!common || ls > kRescaleSum) {
           if (full) {
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -407,9 +407,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           }
         }
         if (first) m_ref = mc;
-        if (!common || redo)
-          ls = U.two_terms ? exp_pack_store<T, true>(v, s_addr, sl2, m_ref, full, kb, span)
-                           : exp_pack_store<T, false>(v, s_addr, sl2, m_ref, full, kb, span);
+        if (!common || redo) ls = exp_pack_store<T, true>(v, s_addr, sl2, m_ref, full, kb, span);
         l += ls;
         tc::wait_st();
         if (!mbar_wait(&bars.v_full[vs], (c / kPVStages) & 1)) {
@@ -606,7 +604,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       constexpr uint64_t kHalfStep = kHalf >> 4;
       // the P V product of key tile pc (pending), issued once P is ready
       int pc = -1, p_run = 0;
-      bool p_first = false, p_two = false;
+      bool p_first = false;
       auto issue_pv = [&]() -> bool {
         const int jv = pc % kPVStages;
         if (!wait_all(&bars.p_full[jv], (pc / kPVStages) & 1)) return false;
@@ -622,7 +620,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             const uint32_t a_hi = p_col + 32 * (kk >> 1) + 8 * (kk & 1);
             const uint64_t bdesc = vdesc + (uint64_t)(kk * (kVPage >> 4));
             tc::mma_f16_ts(o_col, a_hi, bdesc, IDESC_O, (kk & 3) > 0 ? 1u : acc0);
-            if (p_two) tc::mma_f16_ts(o_col, a_hi + 16, bdesc, IDESC_O, 1u);
+            tc::mma_f16_ts(o_col, a_hi + 16, bdesc, IDESC_O, 1u);
           }
           tc::commit(&bars.pv_done[jv]);
         }
@@ -672,7 +670,6 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           pc = c;
           p_run = ui;
           p_first = kt == U.ka;
-          p_two = U.two_terms;
         }
       }
       if (!timed_out && pc >= 0 && !issue_pv()) timed_out = true;
