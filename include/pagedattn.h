@@ -639,7 +639,8 @@ PA_API pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, c
  * pool dtype, whatever the size of a group.  A negative group size, a
  * group past num_seqs, and a prefix length that is negative, not a multiple of
  * 16 or beyond the block table record PA_ERR_RANGE (detail: the group); such a
- * group shares nothing and its sequences are computed from their own tables.  A
+ * group shares nothing and its sequences are computed from their own tables (a
+ * group past num_seqs has all that are left, and the groups behind it none).  A
  * sequence shorter than its group's prefix is treated as one with a bad length.
  * A block id outside the pool is reported (detail: the sequence whose table
  * holds it); the outputs that needed that page are undefined.  16-bit pools; at

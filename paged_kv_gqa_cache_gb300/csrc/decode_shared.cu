@@ -113,9 +113,11 @@ __device__ __forceinline__ GroupShape group_shape(int size, int len, int share) 
   return s;
 }
 
-// Every group's end and shared length (one warp).  A group with a bad size
-// counts as empty; one with a bad length, with a single sequence or that runs
-// past the sequences shares nothing.  Reported if asked.
+// Every group's end and shared length (one warp).  A group of negative size
+// counts as empty; one that runs past the sequences takes all that are left, so
+// that no later group gets any of them; that one, one with a bad length and one
+// with a single sequence share nothing.  Reported if asked (of the groups past
+// the sequences the first).
 __device__ __forceinline__ void load_groups(const SharedParams &p, SharedPlan &pl, bool report) {
   const int lane = threadIdx.x & 31;
   int carry = 0;
@@ -126,10 +128,9 @@ __device__ __forceinline__ void load_groups(const SharedParams &p, SharedPlan &p
     if (g < p.num_groups) {
       size = __ldg(p.group_sizes + g);
       n = __ldg(p.prefix_lens + g);
-      const bool bad_size = size < 0 || size > p.num_seqs;
       const bool bad_len = n < 0 || n % kBlock != 0 || n > (int64_t)p.max_blocks_per_seq * kBlock;
-      bad = bad_size || bad_len;
-      if (bad_size) size = 0;
+      bad = size < 0 || bad_len;
+      size = max(0, min(size, p.num_seqs + 1));  // (the ends of all groups then fit 32 bits)
       if (bad_len || size < 2) n = 0;
     }
     int e = size;
@@ -142,7 +143,7 @@ __device__ __forceinline__ void load_groups(const SharedParams &p, SharedPlan &p
     carry = __shfl_sync(FULL, e, 31);
     if (g < p.num_groups) {
       const bool over = e > p.num_seqs;
-      if (report && (bad || (over && size > 0))) set_error(p.err, PA_ERR_RANGE, g);
+      if (report && (bad || (over && e - size <= p.num_seqs))) set_error(p.err, PA_ERR_RANGE, g);
       pl.end[g] = min(e, p.num_seqs);
       pl.len[g] = over ? 0 : n;
     }
