@@ -636,7 +636,8 @@ PA_API pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, c
  *                 sharing one must not overlap on the GPU.
  * The query-key and probability-value products run on the tensor cores with
  * fp32 accumulation; the probabilities enter the second in two terms of the
- * pool dtype, whatever the size of a group.  A negative group size, a
+ * pool dtype, whatever the size of a group (2^-16 of each or better; over fp16
+ * pools beside it 2^-38 of the row's largest).  A negative group size, a
  * group past num_seqs, and a prefix length that is negative, not a multiple of
  * 16 or beyond the block table record PA_ERR_RANGE (detail: the group); such a
  * group shares nothing and its sequences are computed from their own tables (a
@@ -672,7 +673,9 @@ PA_API pa_status pa_paged_attn_decode_shared(const void *q, const pa_kv_pool *po
  *   workspace     at least pa_decode_weights_workspace_bytes(...) bytes, 16-byte
  *                 aligned; its contents need no initialisation and are
  *                 clobbered.  Calls sharing one must not overlap on the GPU.
- * Scores, weights and sums are fp32.  A page with a block id outside the pool is
+ * Scores, weights and sums are fp32; for the outputs the probabilities enter the
+ * tensor cores in two terms of the pool dtype (2^-16 of each or better; over fp16
+ * pools beside it 2^-40 of the row's largest).  A page with a block id outside the pool is
  * reported and its tokens get no weight.  16-bit pools; num_seqs * num_kv_heads
  * at most 65535, max_context_len at most 2^30 (else PA_ERR_UNSUPPORTED).  Other
  * arguments and errors as pa_paged_attn_decode.

@@ -15,7 +15,12 @@
 //   P is fed as two terms, P_hi = round(P) and P_lo = round(P - P_hi), to the
 //   16-bit type: one rounding of P would double the output's rounding variance
 //   (each weight off by up to half a step), two keep P to 2^-16 or better for 8
-//   more products per page, which the tensor cores have to spare.
+//   more products per page, which the tensor cores have to spare.  fp16 ends at
+//   2^-25 below and 65504 above, and the weights of a row may lie further apart
+//   (tens of thousands of keys 18 nats below one, which carry the row where that
+//   one's value is small): P is 2^15 at its largest there (kUnit), so that a weight
+//   is off by 2^-40 of the row's largest at most beside the 2^-22 of its own.  The
+//   factor stands in l and O alike and leaves both before they leave the warp.
 //
 // K and V pages land in the 128-byte swizzle (one 4 KB box each, the two
 // 64-dim halves 2 KB apart), which ldmatrix reads without bank conflicts: K
@@ -82,6 +87,10 @@ __device__ void scan_pages_of(int n, int32_t *prefix, int *warp_tot, Pages pages
   __syncthreads();
 }
 
+// The largest P of a row, a power of two.
+template <typename T>
+constexpr float kUnit = std::is_same<T, __half>::value ? 32768.f : 1.f;
+
 template <typename T>
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
@@ -115,7 +124,8 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
 
 // An item's running state: O^T fragments (lane (g, t) = (lane / 4, lane % 4):
 // heads 2t and 2t + 1 at dims 16 mt + g and 16 mt + g + 8), and for head g the
-// maximum (log2 domain, the same in its quad) and this lane's part of the sum.
+// maximum (log2 domain, the same in its quad) and this lane's part of the sum;
+// the sum and O are of kUnit 2^(s - m).
 struct Mma16 {
   float acc[8][4];
   float m, l;
@@ -172,7 +182,7 @@ __device__ __forceinline__ void decode_page16(uint32_t stage, int nv, const uint
   const float alpha = ex2(st.m - base);  // 0 while nothing was accumulated
   float p[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) p[i] = ex2(s[i] - base);
+  for (int i = 0; i < 4; ++i) p[i] = ex2(s[i] - base) * kUnit<T>;
   st.l = st.l * alpha + ((p[0] + p[1]) + (p[2] + p[3]));
   st.m = mn;
   // the accumulators hold heads 2t and 2t + 1: their factors come from those heads' quads
@@ -409,10 +419,10 @@ __device__ __forceinline__ bool split_consumer16(const DecodeParams &p, const Fo
             float *dst = p.ws_o + fslot * kHeadDim + g;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
-              dst[16 * mt] = st16.acc[mt][c];
-              dst[16 * mt + 8] = st16.acc[mt][2 + c];
+              dst[16 * mt] = st16.acc[mt][c] * (1.f / kUnit<T>);
+              dst[16 * mt + 8] = st16.acc[mt][2 + c] * (1.f / kUnit<T>);
             }
-            if (g == 0) *reinterpret_cast<float2 *>(p.ws_ml + fslot * 2) = make_float2(mh, lh);
+            if (g == 0) *reinterpret_cast<float2 *>(p.ws_ml + fslot * 2) = make_float2(mh, lh * (1.f / kUnit<T>));
           }
         }
       }

@@ -259,8 +259,28 @@ __device__ __forceinline__ bool suffix_worker(const CUtensorMap &kpage, const CU
 // P goes into P V in two terms, P_hi = round(P) and P_lo = round(P - P_hi), like
 // the suffix's, whatever the group's size: a sequence's output does not lose
 // precision because others joined its group.  The 8 more MMAs per key tile are
-// 0.26 us of tensor time.
+// 0.26 us of tensor time.  A row's reference m_ref is kBelow under a maximum, and
+// O is rescaled once a maximum is more than kTop above it.  bf16 has fp32's range:
+// 0 and kRescale.  fp16 has 2^-25 to 65504, all of it used so that small weights
+// are held nearly as in the suffix: P is 2^13 or more at the row's largest (a weight
+// is off by 2^-38 of that one at most) and under 2^16.  The 2.9 between the two
+// decide how often O is rescaled (192 sequences in three groups, fp16: 108.7 us; with
+// 14 and 15 in their place 118, 13 and 15 115.5, 12 and 15 108; bf16 100.3).
 // Then warp i < 8 consumes and warp 8 + i fetches the pages of a suffix worker.
+template <typename T>
+constexpr float kBelow = std::is_same<T, __half>::value ? 13.f : 0.f;
+template <typename T>
+constexpr float kTop = std::is_same<T, __half>::value ? 15.9f : kRescale;
+template <typename T>
+constexpr float kTopSum = std::is_same<T, __half>::value ? 61147.f : kRescaleSum;  // 2^kTop: a half-row sum bound
+// The reference for a maximum mc: kBelow under it while their difference is good to
+// 2^-4, so that P stays in fp16's range; past that mc itself (weights under 2^-25 of
+// the largest are then lost in fp16).
+template <typename T>
+__device__ __forceinline__ float reference_of(float mc) {
+  return kBelow<T> == 0.f || fabsf(mc) >= 1048576.f ? mc : mc - kBelow<T>;
+}
+
 template <typename T, int G>
 __global__ void __launch_bounds__(kThreads, 1)
 shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kpage,
@@ -362,7 +382,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const bool common = __all_sync(FULL, full && !first);
         float mx = -INFINITY, ls = 0.f;
         if (common) ls = exp_pack_store<T, true>(v, s_addr, sl2, m_ref, true, kb, span);
-        if (!common || ls > kRescaleSum) {
+        if (!common || ls > kTopSum<T>) {
           if (full) {
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -383,14 +403,14 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           }
         }
         const float mc = mx * sl2;
-        const bool need = !first && mc > m_ref + kRescale;
+        const bool need = !first && mc > m_ref + kTop<T>;
         const bool redo = __any_sync(FULL, need);
         if (redo) {  // warp-uniform; key tile c - 1 belongs to this run (first is false)
           if (common) tc::wait_st();
-          const float f = need ? ex2(m_ref - mc) : 1.f;
+          const float m_new = reference_of<T>(mc), f = need ? ex2(m_ref - m_new) : 1.f;
           if (need) {
             l *= f;
-            m_ref = mc;
+            m_ref = m_new;
           }
           if (!mbar_wait(&bars.pv_done[(c - 1) % kPVStages], ((c - 1) / kPVStages) & 1)) {
             timed_out = true;
@@ -407,7 +427,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             tc::st_32x32b_x32(o_self + cc * 32, ov);
           }
         }
-        if (first) m_ref = mc;
+        if (first) m_ref = reference_of<T>(mc);
         if (!common || redo) ls = exp_pack_store<T, true>(v, s_addr, sl2, m_ref, full, kb, span);
         l += ls;
         tc::wait_st();
