@@ -254,6 +254,27 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+def _fresh(stream, make, *args):
+    """``make(*args)``, a tensor that the call allocates for itself, in the order of
+    the stream it runs on: memory of another stream's pool may still be in use by
+    what that stream has queued, and a fill on that stream may come too late."""
+    if stream is None:
+        return make(*args)
+    with torch.cuda.stream(stream):
+        return make(*args)
+
+
+def _result(stream, make, *args):
+    """``_fresh`` for a tensor that the caller gets: it is used on the current
+    stream, so its memory must not go back before that is done either."""
+    t = _fresh(stream, make, *args)
+    if stream is not None and t.is_cuda:
+        current = torch.cuda.current_stream()
+        if stream != current:
+            t.record_stream(current)
+    return t
+
+
 def make_pool(k_cache: torch.Tensor, v_cache: torch.Tensor) -> KVPool:
     """Descriptor of one layer's pool: k_cache, v_cache [num_blocks, 16, Hkv, 128]."""
     _need(k_cache, "k_cache")
@@ -342,10 +363,10 @@ def paged_attn_decode_q8(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.
     mb = block_tables.shape[1]
     mcl = int(max_context_len) if max_context_len is not None else mb * pool.block_size
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(stream, torch.empty_like, q)
     _need(out, "out", q.dtype)
     if workspace is None:
-        workspace = alloc_decode_workspace(S, hq, pool.num_kv_heads, mcl, q.device)
+        workspace = _fresh(stream, alloc_decode_workspace, S, hq, pool.num_kv_heads, mcl, q.device)
     _need(workspace, "workspace")
     lib = load_library()
     wsb = workspace.numel() * workspace.element_size()
@@ -471,10 +492,10 @@ def _decode(q, k_cache, v_cache, block_tables, context_lens, scale, window, out,
     mb = block_tables.shape[1]
     mcl = int(max_context_len) if max_context_len is not None else mb * pool.block_size
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(stream, torch.empty_like, q)
     _need(out, "out", q.dtype)
     if workspace is None:
-        workspace = alloc_decode_workspace(S, hq, pool.num_kv_heads, mcl, q.device)
+        workspace = _fresh(stream, alloc_decode_workspace, S, hq, pool.num_kv_heads, mcl, q.device)
     _need(workspace, "workspace")
     lib = load_library()
     ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
@@ -517,7 +538,7 @@ def paged_attn_decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     mb = block_tables.shape[1]
     mcl = int(max_context_len) if max_context_len is not None else mb * pool.block_size
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(stream, torch.empty_like, q)
     _need(out, "out", q.dtype)
     _check(load_library().pa_paged_attn_decode_noalloc(
         q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq, mcl,
@@ -574,7 +595,7 @@ def _prefill(q, chunk_starts, chunk_lens, k_cache, v_cache, block_tables, contex
         raise ValueError("chunk metadata must have one entry (block-table row) per chunk")
     rows, hq, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(stream, torch.empty_like, q)
     _need(out, "out", q.dtype)
     lib = load_library()
     args = (q.data_ptr(), chunk_starts.data_ptr(), chunk_lens.data_ptr(), ctypes.byref(pool),
@@ -612,7 +633,7 @@ def paged_attn_prefill_chunk_q8(q: torch.Tensor, chunk_starts: torch.Tensor, chu
         raise ValueError("chunk metadata must have one entry (block-table row) per chunk")
     rows, hq, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(stream, torch.empty_like, q)
     _need(out, "out", q.dtype)
     _check(load_library().pa_paged_attn_prefill_chunk_q8(
         q.data_ptr(), _dtype_code(q), chunk_starts.data_ptr(), chunk_lens.data_ptr(), ctypes.byref(pool),
@@ -677,7 +698,7 @@ def mixed_step(k_cache: torch.Tensor, v_cache: torch.Tensor, scale: float, works
                         ("chunk_block_tables", chunk_block_tables), ("chunk_context_lens", chunk_context_lens)):
             _need(t, name, torch.int32)
         if out_chunks is None:
-            out_chunks = torch.empty_like(q_chunks)
+            out_chunks = _result(stream, torch.empty_like, q_chunks)
         _need(out_chunks, "out_chunks", q_chunks.dtype)
     if S:
         _need(q, "q", k_cache.dtype)
@@ -689,7 +710,7 @@ def mixed_step(k_cache: torch.Tensor, v_cache: torch.Tensor, scale: float, works
             _need(k_dec, "k_dec", k_cache.dtype)
             _need(v_dec, "v_dec", k_cache.dtype)
         if out is None:
-            out = torch.empty_like(q)
+            out = _result(stream, torch.empty_like, q)
         _need(out, "out", q.dtype)
     ptr = lambda t, on: t.data_ptr() if (on and t is not None) else None
     _check(load_library().pa_mixed_step(
@@ -742,7 +763,7 @@ def qk_norm_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_n
             or slot_mapping.shape != (T,) or cos_table.dim() != 2 or cos_table.shape != sin_table.shape:
         raise ValueError("q [T, Hq, 128], k/v [T, Hkv, 128], positions/slot_mapping [T], tables [max_pos, 128]")
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _result(stream, torch.empty_like, q)
     _need(q_out, "q_out", q.dtype)
     _check(load_library().pa_qk_norm_rope_kv_write(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_norm_weight.data_ptr(), k_norm_weight.data_ptr(), float(eps),
@@ -804,14 +825,6 @@ def _stream_of(stream, dev: int) -> int:
     return _stream(stream)
 
 
-def _hold(stream, *tensors) -> None:
-    """Tensors allocated here for a call on another stream than the current one:
-    the allocator must not hand their memory out before that stream is done with it."""
-    if stream is not None and stream != torch.cuda.current_stream():
-        for t in tensors:
-            t.record_stream(stream)
-
-
 def rope_inv_freq(rotary_dim: int, theta: float, scaling: int = ROPE_PLAIN, factor: float = 1.0,
                   trained_length: float = 1.0, slow: float = 1.0, fast: float = 32.0, device=None):
     """Inverse frequencies (float64 [rotary_dim / 2], on ``device``, default the
@@ -839,7 +852,7 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
     dt, hkv, d = k_cache.dtype, pool.num_kv_heads, pool.head_dim
     fresh = q_out is None
     if fresh:
-        q_out = torch.empty_like(q)
+        q_out = _result(stream, torch.empty_like, q)
     if not (_fine(dev, dt, q, k, v, q_out) and _fine(dev, torch.float64, inv_freq) and
             _fine(dev, torch.int32, positions) and _fine(dev, torch.int64, slot_mapping)):
         _check_all(dev, (q, "q", dt), (k, "k", dt), (v, "v", dt), (inv_freq, "inv_freq", torch.float64),
@@ -868,8 +881,6 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
         q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(rope), wq, wk, eps, positions.data_ptr(),
         slot_mapping.data_ptr(), T, hq, q_out.data_ptr(), ctypes.byref(pool), _stream_of(stream, dev)),
         "pa_rope_kv_write")
-    if fresh and stream is not None:
-        _hold(stream, q_out)
     return q_out
 
 
@@ -894,23 +905,20 @@ def paged_attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: to
     of 16), read once through the group's first block table."""
     dev = _device()
     pool = _pool_of(k_cache, v_cache, dev)
-    S, hq, mb, mcl, out, fresh = _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out)
+    S, hq, mb, mcl, out = _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out, stream)
     if not _fine(dev, torch.int32, group_sizes, prefix_lens):
         _check_all(dev, (group_sizes, "group_sizes", torch.int32), (prefix_lens, "prefix_lens", torch.int32))
     if group_sizes.dim() != 1 or prefix_lens.shape != group_sizes.shape:
         raise ValueError("group_sizes and prefix_lens must both be [groups]")
     n = group_sizes.shape[0]
     if workspace is None:
-        workspace = alloc_decode_shared_workspace(S, n, hq, pool.num_kv_heads, q.device)
-        fresh.append(workspace)
+        workspace = _fresh(stream, alloc_decode_shared_workspace, S, n, hq, pool.num_kv_heads, q.device)
     if not _fine(dev, torch.uint8, workspace):
         _check_all(dev, (workspace, "workspace", None))
     _check((_lib or load_library()).pa_paged_attn_decode_shared(
         q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq, mcl, scale,
         group_sizes.data_ptr(), prefix_lens.data_ptr(), n, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
         _stream_of(stream, dev)), "pa_paged_attn_decode_shared")
-    if stream is not None:
-        _hold(stream, *fresh)
     return out
 
 
@@ -925,14 +933,12 @@ def alloc_decode_weights_workspace(num_seqs: int, num_q_heads: int, num_kv_heads
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
-def _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out):
+def _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out, stream):
     """The checks these decode calls share; (sequences, query heads, table width,
-    length bound, the output, the tensors allocated here)."""
+    length bound, the output)."""
     dt = torch.float16 if pool.dtype == PA_F16 else torch.bfloat16
-    fresh = []
     if out is None:
-        out = torch.empty_like(q)
-        fresh.append(out)
+        out = _result(stream, torch.empty_like, q)
     if not (_fine(dev, dt, q, out) and _fine(dev, torch.int32, block_tables, context_lens)):
         _check_all(dev, (q, "q", dt), (block_tables, "block_tables", torch.int32),
                    (context_lens, "context_lens", torch.int32), (out, "out", dt))
@@ -945,7 +951,7 @@ def _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out)
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
         raise ValueError("block_tables must be [S, max_blocks], context_lens [S]")
     mb = block_tables.shape[1]
-    return S, hq, mb, mb * pool.block_size if max_context_len is None else max_context_len, out, fresh
+    return S, hq, mb, mb * pool.block_size if max_context_len is None else max_context_len, out
 
 
 def paged_attn_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -961,7 +967,7 @@ def paged_attn_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     both the block tables and the weights hold.  Returns (out, weights_out)."""
     dev = _device()
     pool = _pool_of(k_cache, v_cache, dev)
-    S, hq, mb, mcl, out, fresh = _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out)
+    S, hq, mb, mcl, out = _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out, stream)
     if not _fine(dev, torch.float32, weights_out):
         _check_all(dev, (weights_out, "weights_out", torch.float32))
     wshape = weights_out.shape
@@ -975,16 +981,13 @@ def paged_attn_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     if max_context_len is None:
         mcl = min(mcl, wshape[2])
     if workspace is None:
-        workspace = alloc_decode_weights_workspace(S, hq, pool.num_kv_heads, mcl, q.device)
-        fresh.append(workspace)
+        workspace = _fresh(stream, alloc_decode_weights_workspace, S, hq, pool.num_kv_heads, mcl, q.device)
     if not _fine(dev, torch.uint8, workspace):
         _check_all(dev, (workspace, "workspace", None))
     _check((_lib or load_library()).pa_paged_attn_decode_weights(
         q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq, mcl, scale,
         None if weights_in is None else weights_in.data_ptr(), weights_out.data_ptr(), wshape[2], out.data_ptr(),
         workspace.data_ptr(), workspace.nbytes, _stream_of(stream, dev)), "pa_paged_attn_decode_weights")
-    if stream is not None:
-        _hold(stream, *fresh)
     return out, weights_out
 
 
@@ -1018,16 +1021,13 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
         raise ValueError(f"sizes disagree: {S} sequences, {hkv} KV heads")
     if max_context_len is not None and max_context_len > ws[2]:
         raise ValueError(f"weights hold {ws[2]} tokens, max_context_len is {max_context_len}")
-    fresh = []
     if kept is None:
-        kept = torch.empty((S, hkv, max(budget, 0)), dtype=i32, device=block_tables.device)
-        fresh.append(kept)
+        kept = _result(stream, lambda: torch.empty((S, hkv, max(budget, 0)), dtype=i32, device=block_tables.device))
     elif not _fine(dev, i32, kept) or kept.shape != (S, hkv, budget):
         _check_all(dev, (kept, "kept", i32))
         raise ValueError(f"kept must be [{S}, {hkv}, {budget}]")
     if new_context_lens is None:
-        new_context_lens = torch.empty_like(context_lens)
-        fresh.append(new_context_lens)
+        new_context_lens = _result(stream, torch.empty_like, context_lens)
     elif not _fine(dev, i32, new_context_lens) or new_context_lens.shape != (S,):
         _check_all(dev, (new_context_lens, "new_context_lens", i32))
         raise ValueError(f"new_context_lens must be [{S}]")
@@ -1035,8 +1035,6 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
         ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, weights.data_ptr(), ws[2], budget,
         recent, sinks, dst.data_ptr(), dst.shape[1], w_out.data_ptr(), wos[2], kept.data_ptr(),
         new_context_lens.data_ptr(), _stream_of(stream, dev)), "pa_kv_evict")
-    if stream is not None:
-        _hold(stream, *fresh)
     return kept, new_context_lens
 
 
