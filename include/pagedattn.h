@@ -727,6 +727,20 @@ PA_API pa_status pa_kv_evict(const pa_kv_pool *pool, const int32_t *block_tables
                              const int32_t *dst_block_tables, int32_t dst_max_blocks, float *weights_out,
                              int32_t weights_out_stride, int32_t *kept, int32_t *new_context_lens,
                              pa_stream_t stream);
+/*
+ * kv_evict_ex — pa_kv_evict for outputs that were not initialised: with
+ *   PA_EVICT_MARK_KEPT     kept[s] of a sequence that records PA_ERR_RANGE is -1 throughout;
+ *   PA_EVICT_MARK_LENGTHS  its new_context_lens[s] is -1, a length that every call refuses.
+ * Other flags: PA_ERR_UNSUPPORTED.
+ */
+#define PA_EVICT_MARK_KEPT 1u
+#define PA_EVICT_MARK_LENGTHS 2u
+PA_API pa_status pa_kv_evict_ex(const pa_kv_pool *pool, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                const int32_t *context_lens, int32_t num_seqs, const float *weights,
+                                int32_t weights_stride, int32_t budget, int32_t recent, int32_t sinks,
+                                const int32_t *dst_block_tables, int32_t dst_max_blocks, float *weights_out,
+                                int32_t weights_out_stride, int32_t *kept, int32_t *new_context_lens, uint32_t flags,
+                                pa_stream_t stream);
 
 /*
  * ---- copy-on-write and the block-table builder [P1, qwen_serve/paged.py:

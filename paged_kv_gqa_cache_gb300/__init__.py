@@ -54,7 +54,7 @@ EXPORTS = ("pa_kv_cache_write", "pa_decode_workspace_bytes", "pa_paged_attn_deco
            "pa_qk_norm_rope_kv_write", "pa_paged_attn_decode_append", "pa_selftest_bounded_wait",
            "pa_paged_attn_decode_ex", "pa_paged_attn_decode_q8_ex", "pa_prefill_workspace_bytes",
            "pa_paged_attn_prefill_chunk_ex", "pa_paged_attn_prefill_chunk_q8", "pa_mixed_step",
-           "pa_mixed_step_workspace_bytes", "pa_rope_inv_freq", "pa_rope_kv_write", "pa_kv_evict",
+           "pa_mixed_step_workspace_bytes", "pa_rope_inv_freq", "pa_rope_kv_write", "pa_kv_evict", "pa_kv_evict_ex",
            "pa_decode_shared_workspace_bytes", "pa_paged_attn_decode_shared",
            "pa_decode_weights_workspace_bytes", "pa_paged_attn_decode_weights",
            "pa_sequence_unshare", "pa_sequence_truncate",
@@ -181,6 +181,8 @@ def load_library(path: str = LIB_PATH):
         lib.pa_paged_attn_decode_weights.restype = i32
         lib.pa_kv_evict.argtypes = [pool_p, P, i32, P, i32, P, i32, i32, i32, i32, P, i32, P, i32, P, P, P]
         lib.pa_kv_evict.restype = i32
+        lib.pa_kv_evict_ex.argtypes = lib.pa_kv_evict.argtypes[:-1] + [ctypes.c_uint32, P]
+        lib.pa_kv_evict_ex.restype = i32
         lib.pa_selftest_bounded_wait.argtypes = [ctypes.c_uint32, P]
         lib.pa_selftest_bounded_wait.restype = i32
         lib.pa_kv_block_copy.argtypes = [pool_p, i32, P, i32, P]
@@ -777,6 +779,7 @@ def qk_norm_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_n
 
 MAX_PREFIX_GROUPS = 256
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+EVICT_MARK_KEPT, EVICT_MARK_LENGTHS = 1, 2
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = range(5)
 
 
@@ -1002,7 +1005,9 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
     of the rest stay, in order.  The rows move within the pool to
     ``dst_block_tables`` (default: in place) and the weights to ``weights_out``
     (default: in place).  Returns (kept int32 [S, Hkv, budget] with -1 past the
-    new length, new context lengths int32 [S]).  ``max_context_len`` is a host
+    new length, new context lengths int32 [S]); a sequence that the device refuses
+    (its length is bad) gets -1 in both, or keeps what a ``kept`` or
+    ``new_context_lens`` of the caller's held.  ``max_context_len`` is a host
     bound on ``context_lens`` for the check that the weights cover it."""
     dev = _device()
     pool = _pool_of(k_cache, v_cache, dev)
@@ -1021,20 +1026,23 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
         raise ValueError(f"sizes disagree: {S} sequences, {hkv} KV heads")
     if max_context_len is not None and max_context_len > ws[2]:
         raise ValueError(f"weights hold {ws[2]} tokens, max_context_len is {max_context_len}")
+    flags = 0
     if kept is None:
+        flags |= EVICT_MARK_KEPT
         kept = _result(stream, lambda: torch.empty((S, hkv, max(budget, 0)), dtype=i32, device=block_tables.device))
     elif not _fine(dev, i32, kept) or kept.shape != (S, hkv, budget):
         _check_all(dev, (kept, "kept", i32))
         raise ValueError(f"kept must be [{S}, {hkv}, {budget}]")
     if new_context_lens is None:
+        flags |= EVICT_MARK_LENGTHS
         new_context_lens = _result(stream, torch.empty_like, context_lens)
     elif not _fine(dev, i32, new_context_lens) or new_context_lens.shape != (S,):
         _check_all(dev, (new_context_lens, "new_context_lens", i32))
         raise ValueError(f"new_context_lens must be [{S}]")
-    _check((_lib or load_library()).pa_kv_evict(
+    _check((_lib or load_library()).pa_kv_evict_ex(
         ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, weights.data_ptr(), ws[2], budget,
         recent, sinks, dst.data_ptr(), dst.shape[1], w_out.data_ptr(), wos[2], kept.data_ptr(),
-        new_context_lens.data_ptr(), _stream_of(stream, dev)), "pa_kv_evict")
+        new_context_lens.data_ptr(), flags, _stream_of(stream, dev)), "pa_kv_evict_ex")
     return kept, new_context_lens
 
 

@@ -146,7 +146,14 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv_evict_kernel(const EvictPara
   if (ctx < 1 || ctx > kLongMaxTokens || (int64_t)ctx > (int64_t)p.max_blocks_per_seq * kBlock ||
       ctx > p.weights_stride || (int64_t)n > (int64_t)p.dst_max_blocks * kBlock ||
       n > p.out_stride) {  // uniform over the cluster
-    if (h == 0 && rank == 0 && tid == 0) set_error(p.err, PA_ERR_RANGE, s);
+    if (h == 0 && rank == 0 && tid == 0) {
+      set_error(p.err, PA_ERR_RANGE, s);
+      if (p.flags & PA_EVICT_MARK_LENGTHS) p.new_lens[s] = -1;
+    }
+    if (p.flags & PA_EVICT_MARK_KEPT) {
+      int32_t *row = p.kept + ((int64_t)s * hkv + h) * p.budget;
+      for (int i = rank * kEvThreads + tid; i < p.budget; i += C * kEvThreads) row[i] = -1;
+    }
     return;
   }
   const float *w = p.weights + ((int64_t)s * hkv + h) * p.weights_stride;

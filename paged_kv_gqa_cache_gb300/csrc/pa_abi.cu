@@ -966,13 +966,14 @@ pa_status pa_paged_attn_decode_weights(const void *q, const pa_kv_pool *pool, co
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
-pa_status pa_kv_evict(const pa_kv_pool *pool, const int32_t *block_tables, int32_t max_blocks_per_seq,
-                      const int32_t *context_lens, int32_t num_seqs, const float *weights, int32_t weights_stride,
-                      int32_t budget, int32_t recent, int32_t sinks, const int32_t *dst_block_tables,
-                      int32_t dst_max_blocks, float *weights_out, int32_t weights_out_stride, int32_t *kept,
-                      int32_t *new_context_lens, pa_stream_t stream) {
+pa_status pa_kv_evict_ex(const pa_kv_pool *pool, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                         const int32_t *context_lens, int32_t num_seqs, const float *weights, int32_t weights_stride,
+                         int32_t budget, int32_t recent, int32_t sinks, const int32_t *dst_block_tables,
+                         int32_t dst_max_blocks, float *weights_out, int32_t weights_out_stride, int32_t *kept,
+                         int32_t *new_context_lens, uint32_t flags, pa_stream_t stream) {
   pa_status st = check_pool(pool);
   if (st != PA_OK) return st;
+  if (flags & ~(uint32_t)(PA_EVICT_MARK_KEPT | PA_EVICT_MARK_LENGTHS)) return PA_ERR_UNSUPPORTED;
   if (num_seqs < 0) return PA_ERR_SHAPE;
   if (num_seqs == 0) return PA_OK;
   if (!block_tables || !context_lens || !weights || !dst_block_tables || !weights_out || !kept || !new_context_lens)
@@ -1016,8 +1017,19 @@ pa_status pa_kv_evict(const pa_kv_pool *pool, const int32_t *block_tables, int32
   p.budget = budget;
   p.recent = recent;
   p.sinks = sinks;
+  p.flags = flags;
   cudaError_t e = launch_evict(p, d->sm_count, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+pa_status pa_kv_evict(const pa_kv_pool *pool, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                      const int32_t *context_lens, int32_t num_seqs, const float *weights, int32_t weights_stride,
+                      int32_t budget, int32_t recent, int32_t sinks, const int32_t *dst_block_tables,
+                      int32_t dst_max_blocks, float *weights_out, int32_t weights_out_stride, int32_t *kept,
+                      int32_t *new_context_lens, pa_stream_t stream) {
+  return pa_kv_evict_ex(pool, block_tables, max_blocks_per_seq, context_lens, num_seqs, weights, weights_stride, budget,
+                        recent, sinks, dst_block_tables, dst_max_blocks, weights_out, weights_out_stride, kept,
+                        new_context_lens, 0, stream);
 }
 
 pa_status pa_kv_block_copy(const pa_kv_pool *pools, int32_t num_layers, const int32_t *pairs, int32_t num_pairs,

@@ -122,6 +122,7 @@ struct EvictParams {
   int32_t budget;
   int32_t recent;
   int32_t sinks;
+  uint32_t flags;                   // PA_EVICT_MARK_*
 };
 cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream);
 
