@@ -599,7 +599,8 @@ PA_API pa_status pa_rope_inv_freq(int32_t scaling, int32_t rotary_dim, double th
  * dtype (pa_qk_norm_rope_kv_write rounds after every step as the page's model
  * does, and takes 16-bit tables).  Angles are exact to fp32 at any position:
  * the fraction of a turn is taken in 64-bit fixed point.
- *   q, q_out      [num_tokens][num_q_heads][128], pool dtype; q_out may be q.
+ *   q, q_out      [num_tokens][num_q_heads][128], pool dtype; q_out may be q, and
+ *                 overlaps none of q, k and v otherwise (PA_ERR_SHAPE).
  *   k, v          [num_tokens][num_kv_heads][128], pool dtype.
  *   rope          HOST descriptor, read during the call (its inv_freq is device memory).
  *   positions     int32 [num_tokens]; the cache index of a token plays no part,

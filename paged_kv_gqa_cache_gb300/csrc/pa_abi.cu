@@ -810,6 +810,12 @@ pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, const pa
       !aligned16(k_norm_weight) || !aligned4(positions) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) ||
       (reinterpret_cast<uintptr_t>(rope->inv_freq) & 7u))
     return PA_ERR_ALIGN;
+  // rows of other tokens, which other CTAs still read, must not be written
+  const size_t row = kHeadDim * 2, q_bytes = (size_t)num_tokens * num_q_heads * row;
+  const size_t kv_bytes = (size_t)num_tokens * pool->num_kv_heads * row;
+  if ((q_out != q && overlap(q_out, q_bytes, q, q_bytes)) || overlap(q_out, q_bytes, k, kv_bytes) ||
+      overlap(q_out, q_bytes, v, kv_bytes))
+    return PA_ERR_SHAPE;
   DeviceState *d = nullptr;
   if ((st = device_state(&d)) != PA_OK) return st;
   RopeKvParams p{};
