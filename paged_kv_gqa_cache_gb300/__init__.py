@@ -862,7 +862,7 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
                    (positions, "positions", torch.int32), (slot_mapping, "slot_mapping", torch.int64),
                    (q_out, "q_out", dt))
     qshape = q.shape
-    T, hq = qshape[0], qshape[1] if len(qshape) == 3 else 0
+    T, hq = qshape[:2] if len(qshape) == 3 else (0, 0)
     rows, each = (T, hkv, d), (T,)
     if qshape != (T, hq, d) or k.shape != rows or v.shape != rows or positions.shape != each \
             or slot_mapping.shape != each or inv_freq.dim() != 1:

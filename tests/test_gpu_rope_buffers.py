@@ -42,3 +42,10 @@ def test_overlaps_are_refused():
         torch.cuda.synchronize()
         assert all(torch.equal(a.view(torch.int16), b.view(torch.int16))
                    for a, b in zip((q, k, out, c["kc"]), before))
+
+
+@pytest.mark.parametrize("shape", [(), (DIM,), (6, 4 * DIM), (6, 4, 1, DIM)])
+def test_queries_that_are_no_rows_of_heads(shape):
+    c = rope._case(6, 4, 2, "f16", 128, seed=2)
+    with pytest.raises(ValueError):
+        rope._run(dict(c, q=torch.zeros(shape, device=DEV).half()), False)
