@@ -646,7 +646,7 @@ PA_API pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, c
  * sequence shorter than its group's prefix is treated as one with a bad length.
  * A block id outside the pool is reported (detail: the sequence whose table
  * holds it); the outputs that needed that page are undefined.  16-bit pools; at
- * most 6000 sequences.  group_sizes and prefix_lens are read before the
+ * most 6000 sequences and 2^31 - 1 block-table entries.  group_sizes and prefix_lens are read before the
  * dependency wait, as block_tables are.  Other arguments and errors as
  * pa_paged_attn_decode.
  */
@@ -678,7 +678,8 @@ PA_API pa_status pa_paged_attn_decode_shared(const void *q, const pa_kv_pool *po
  * tensor cores in two terms of the pool dtype (2^-16 of each or better; over fp16
  * pools beside it 2^-40 of the row's largest).  A page with a block id outside the pool is
  * reported and its tokens get no weight.  16-bit pools; num_seqs * num_kv_heads
- * at most 65535, max_context_len at most 2^30 (else PA_ERR_UNSUPPORTED).  Other
+ * at most 65535, max_context_len at most 2^30, the pages that num_seqs such contexts
+ * fill at most 2^31 - 1 (else PA_ERR_UNSUPPORTED).  Other
  * arguments and errors as pa_paged_attn_decode.
  */
 PA_API size_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,

@@ -868,6 +868,7 @@ pa_status pa_paged_attn_decode_shared(const void *q, const pa_kv_pool *pool, con
   // the prefix work is counted in 32 bits: (query tile, key tile) pairs
   const int64_t tiles = (int64_t)pool->num_kv_heads * (num_groups + (int64_t)num_seqs * group / 128);
   if (tiles * (((int64_t)max_blocks_per_seq * kBlock + 127) / 128) > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)num_seqs * max_blocks_per_seq > INT32_MAX) return PA_ERR_UNSUPPORTED;  // and so are the pages
   if (!aligned4(group_sizes) || !aligned4(prefix_lens)) return PA_ERR_ALIGN;
   if (!workspace) return PA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PA_ERR_ALIGN;
@@ -934,6 +935,8 @@ pa_status pa_paged_attn_decode_weights(const void *q, const pa_kv_pool *pool, co
   if (weights_stride < max_context_len) return PA_ERR_SHAPE;
   if ((int64_t)num_seqs * pool->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;  // a launch's second dimension
   if (max_context_len > kLongMaxTokens) return PA_ERR_UNSUPPORTED;
+  // the pages of the call are counted in 32 bits
+  if (num_seqs * (((int64_t)max_context_len + kBlock - 1) / kBlock) > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if (!aligned4(weights_in) || !aligned4(weights_out)) return PA_ERR_ALIGN;
   const size_t weight_bytes = (size_t)num_seqs * pool->num_kv_heads * weights_stride * sizeof(float);
   if (weights_in && weights_in != weights_out && overlap(weights_in, weight_bytes, weights_out, weight_bytes))
