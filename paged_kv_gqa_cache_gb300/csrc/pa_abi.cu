@@ -287,14 +287,15 @@ pa_status decode_call(const void *q, int dtype, const pa_kv_pool *pool16, const 
 
 }  // namespace
 
-// The checks pa_paged_attn_decode makes before it looks at its workspace, in
-// the same order, for the allocation-free entry point (which has none).
 // Do two buffers of these many bytes share any?
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y ? y - x < na : x - y < nb;
 }
 
+// The checks pa_paged_attn_decode makes before it looks at its workspace, in
+// the same order, for the allocation-free entry point (which has none) and for
+// the long-context decodes (whose workspaces have other sizes).
 pa_status decode_check_args(const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
                             int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
                             int32_t num_q_heads, int32_t max_context_len, float scale, void *out) {

@@ -202,7 +202,7 @@ bool decode_workspace_carve(void *ws, size_t bytes, int num_seqs, int num_q_head
 
 // ---- decode that accumulates the attention weights (16-bit pools) -----------------
 struct DecodeWeightsParams {
-  float *scores;             // workspace: [pages of the call][16][G]
+  float *scores;             // workspace: [pages of the call][G][16 keys]
   const float *weights_in;   // [S][Hkv][weights_stride], null: zeros
   float *weights_out;        // may be weights_in
   int64_t weights_stride;
