@@ -273,12 +273,17 @@ template <typename T>
 constexpr float kTop = std::is_same<T, __half>::value ? 15.9f : kRescale;
 template <typename T>
 constexpr float kTopSum = std::is_same<T, __half>::value ? 61147.f : kRescaleSum;  // 2^kTop: a half-row sum bound
-// The reference for a maximum mc: kBelow under it while their difference is good to
-// 2^-4, so that P stays in fp16's range; past that mc itself (weights under 2^-25 of
-// the largest are then lost in fp16).
+// The reference for a maximum mc, and what a maximum mc may reach above the
+// reference: kBelow under it and kTop, while such sums are good to 2^-4; past that
+// mc itself and nothing, since fp16 has no room for their roundings (weights under
+// 2^-25 of the largest are then lost in fp16).
 template <typename T>
 __device__ __forceinline__ float reference_of(float mc) {
   return kBelow<T> == 0.f || fabsf(mc) >= 1048576.f ? mc : mc - kBelow<T>;
+}
+template <typename T>
+__device__ __forceinline__ float top_of(float mc) {
+  return kBelow<T> != 0.f && fabsf(mc) >= 1048576.f ? 0.f : kTop<T>;
 }
 
 template <typename T, int G>
@@ -403,7 +408,7 @@ shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           }
         }
         const float mc = mx * sl2;
-        const bool need = !first && mc > m_ref + kTop<T>;
+        const bool need = !first && mc > m_ref + top_of<T>(mc);
         const bool redo = __any_sync(FULL, need);
         if (redo) {  // warp-uniform; key tile c - 1 belongs to this run (first is false)
           if (common) tc::wait_st();

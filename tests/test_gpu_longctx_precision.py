@@ -115,3 +115,22 @@ def test_very_large_scores(dtype, large):
         out, _ = pa.paged_attn_decode_weights(x["q"], x["kc"], x["vc"], x["bt"], x["lens"], DIM ** -0.5, None, w)
         assert torch.equal(out, want)
         assert torch.equal(w.sum(-1), torch.full((40, 2), 4.0, device=DEV)) and bool((w[:, :, at] == 4.0).all())
+
+
+@pytest.mark.parametrize("dtype,step", [("f16", 0.5), ("bf16", 4.0)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_large_scores_that_rise_by_about_the_type_s_range(dtype, step, sign):
+    """Scores of 2^21 (log2 units), where fp32 has steps of 0.125 to 0.25, that rise by 14 to 22 (fp16) or 112
+    to 178 from one key tile to the next: what enters the tensor cores must stay finite.  (A weight is only good to some tens of percent there, so
+    the outputs are held to the range of the values that weigh.)"""
+    groups = 132  # (so that a CTA takes several key tiles in a row)
+    c = shared._case([(512, [1, 5])] * groups, 4, 2, dtype, seed=21)
+    c["kc"][~c["kc"].isnan()] = sign * 512.0
+    heads = torch.as_tensor(c["bt_h"][::2, :32], device=DEV).long()
+    for tile in range(1, 4):
+        c["kc"][heads[:, 8 * tile:8 * tile + 8].flatten(), :, :, :tile] = sign * 512.0 + step
+    q = 220 + 2 * (torch.arange(2 * groups, device=DEV) // 4)  # 220 to 350, exact in both types
+    c["q"][:] = q[:, None, None].to(c["q"].dtype)
+    out = shared._run(c).float()
+    top = c["vc"].float().nan_to_num().abs().max()
+    assert bool(out.isfinite().all()) and bool((out.abs() <= 1.01 * top).all())
