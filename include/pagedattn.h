@@ -638,7 +638,10 @@ PA_API pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, c
  * The query-key and probability-value products run on the tensor cores with
  * fp32 accumulation; the probabilities enter the second in two terms of the
  * pool dtype, whatever the size of a group (2^-16 of each or better; over fp16
- * pools beside it 2^-38 of the row's largest).  A negative group size, a
+ * pools beside it 2^-38 of the row's largest; an infinite value that a query sees
+ * makes its output NaN).  The call is worth its set-up from about 10000 tokens on that are
+ * not read again, (members - 1) x prefix at 8 KV heads; below, pa_paged_attn_decode
+ * over the same tables is faster.  A negative group size, a
  * group past num_seqs, and a prefix length that is negative, not a multiple of
  * 16 or beyond the block table record PA_ERR_RANGE (detail: the group); such a
  * group shares nothing and its sequences are computed from their own tables (a
@@ -676,7 +679,8 @@ PA_API pa_status pa_paged_attn_decode_shared(const void *q, const pa_kv_pool *po
  *                 clobbered.  Calls sharing one must not overlap on the GPU.
  * Scores, weights and sums are fp32; for the outputs the probabilities enter the
  * tensor cores in two terms of the pool dtype (2^-16 of each or better; over fp16
- * pools beside it 2^-40 of the row's largest).  A page with a block id outside the pool is
+ * pools beside it 2^-40 of the row's largest; an infinite value that a query sees
+ * makes its output NaN).  A page with a block id outside the pool is
  * reported and its tokens get no weight.  16-bit pools; num_seqs * num_kv_heads
  * at most 65535, max_context_len at most 2^30, the pages that num_seqs such contexts
  * fill at most 2^31 - 1 (else PA_ERR_UNSUPPORTED).  Other
@@ -841,7 +845,8 @@ PA_API pa_status pa_sequence_fork(pa_sequence *seq, const pa_sequence *other);
 PA_API pa_status pa_sequence_unshare(pa_sequence *seq, int32_t n);
 /* Shortens the sequence to its first n committed tokens (0 <= n <= length, else
  * PA_ERR_SHAPE; nothing may be reserved: PA_ERR_STATE), releasing the blocks
- * past them: after pa_kv_evict, n is the sequence's new length. */
+ * past them: after pa_kv_evict, n is the sequence's new length.  Recorded copies
+ * are taken first (pa_allocator_take_copies): they may go to a released block. */
 PA_API pa_status pa_sequence_truncate(pa_sequence *seq, int32_t n);
 /* Releases every block; the sequence is empty again. */
 PA_API pa_status pa_sequence_release(pa_sequence *seq);

@@ -905,7 +905,8 @@ def paged_attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: to
     """Decode attention (as :func:`paged_attn_decode`) for sequences that share
     prefixes: group g is the next ``group_sizes[g]`` sequences (int32 [groups]),
     which share their first ``prefix_lens[g]`` tokens (int32 [groups], multiples
-    of 16), read once through the group's first block table."""
+    of 16), read once through the group's first block table.  Worth it from about
+    10000 tokens on that are not read again ((members - 1) x prefix, 8 KV heads)."""
     dev = _device()
     pool = _pool_of(k_cache, v_cache, dev)
     S, hq, mb, mcl, out = _decode_args(dev, pool, q, block_tables, context_lens, max_context_len, out, stream)

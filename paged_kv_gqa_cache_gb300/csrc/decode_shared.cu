@@ -38,7 +38,12 @@
 // (4.3 TB/s; a pair of a large group 1.0 us: 192 KB through shared memory, 64 in
 // by TMA, 64 to Q K^T and 64 to P V, are 0.8; the join takes 9; 98.5 us with P in
 // one term).  4 sequences, 1024 shared, up to 200 each, 16 / 8 heads: 9.7 us, a
-// chain of latencies.
+// chain of latencies.  A sequence more than fills whole query tiles costs one more
+// (16384 shared, 32 / 8 heads, 32 and 33 sequences: 31.6 and 41.5 us).  Against the
+// plain decode, which reads the prefix once per sequence, it is the faster from about
+// (sequences - 1) x shared tokens = 10000 on at 8 KV heads (2 sequences, 4096 shared:
+// 14.9 and 13.8 us, 16384: 24.4 and 29.2; 16, 256: 9.4 and 6.0, 1024: 11.2 and 12.5;
+// 32, 1024: 14.7 and 25.3).
 #include "decode_mma.cuh"
 #include "prefill_kernel.cuh"
 

@@ -50,7 +50,10 @@
 // the selection and ranking (13 us) leave HBM idle; the 4 long ones, cut to 16384:
 // 121 us, 4.6 TB/s (22 us; then 256-byte rows apart from one another).  One
 // sequence of 1000 cut to 512: 8.5 us, a chain of latencies (select 3.8, rank 1.7,
-// move 2.1).
+// move 2.1).  The cluster's size goes by the number of (sequence, KV head) items
+// alone: 5 sequences of 131072 with 8 heads take 4 CTAs each, whose slices of 32768
+// keys fit shared memory by half, and 239 us (floor 103; 4 sequences, 8 CTAs each:
+// 123, floor 82; 8 sequences 293, floor 165).
 #include <type_traits>
 
 #include "pa_device.cuh"
