@@ -617,6 +617,24 @@ PA_API pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, c
                                   int32_t num_q_heads, void *q_out, const pa_kv_pool *pool, pa_stream_t stream);
 
 /*
+ * rope_kv_write_axes — pa_rope_kv_write for positions of several axes (time,
+ * height and width of images and video): pair i of a row turns by the position of
+ * its token on axis pair_axes[i],
+ *   angle_i = positions[pair_axes[i]][t] * rope->inv_freq[i].
+ *   positions     int32 [num_axes][num_tokens].
+ *   pair_axes     HOST uint8 [rotary_dim / 2], each below num_axes; read during the call.
+ *   num_axes      1 .. PA_ROPE_MAX_AXES (else PA_ERR_SHAPE).
+ * A token with a negative position on any axis is refused as there.  Other
+ * arguments and errors as pa_rope_kv_write, which one axis gives.
+ */
+#define PA_ROPE_MAX_AXES 4
+PA_API pa_status pa_rope_kv_write_axes(const void *q, const void *k, const void *v, const pa_rope *rope,
+                                       const uint8_t *pair_axes, int32_t num_axes, const void *q_norm_weight,
+                                       const void *k_norm_weight, float eps, const int32_t *positions,
+                                       const int64_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                                       void *q_out, const pa_kv_pool *pool, pa_stream_t stream);
+
+/*
  * paged_attn_decode_shared — pa_paged_attn_decode for sequences that share
  * prefixes by groups (their first blocks adopted by reference,
  * pa_sequence_adopt_prefix or pa_sequence_fork): each group's prefix is read
@@ -747,6 +765,103 @@ PA_API pa_status pa_kv_evict_ex(const pa_kv_pool *pool, const int32_t *block_tab
                                 const int32_t *dst_block_tables, int32_t dst_max_blocks, float *weights_out,
                                 int32_t weights_out_stride, int32_t *kept, int32_t *new_context_lens, uint32_t flags,
                                 pa_stream_t stream);
+
+/*
+ * ---- trees of drafted tokens --------------------------------------------------
+ * Speculative decoding: a step drafts several continuations of each sequence as a
+ * tree, attends all of them in one call, and keeps the path that the model's own
+ * choices confirm.  The n = tree_lens[s] drafted tokens of sequence s are the last n
+ * of its context_lens[s] cached ones, token i at position context_lens[s] - n + i of the
+ * block table (written first, their rotary positions by depth: pa_rope_kv_write), in an
+ * order with parents in front of children.  No counterpart on the pages: library
+ * additions.
+ *   tree_lens     int32 [num_seqs], each in [0, PA_MAX_TREE_LEN] (0: nothing drafted; the
+ *                 sequence has no rows and its length is not looked at).
+ *   parents       int32 [num_tokens], the trees one after the other in the order of the
+ *                 sequences: the index within its tree of each token's parent, less than
+ *                 its own; -1: none (it follows the committed context directly).
+ */
+#define PA_MAX_TREE_LEN 256
+#define PA_MAX_TREE_SEQS 2048
+
+/*
+ * paged_attn_tree — attention of the drafted tokens: token i of sequence s sees the
+ * context_lens[s] - n committed tokens, its ancestors in the tree and itself,
+ *   out[i][g] = softmax_j(scale * q[i][g] . K_j) V_j over those.
+ *   q, out        [num_tokens][num_q_heads][128], pool dtype, packed as parents.
+ *   context_lens  the whole lengths, drafted tokens included; at least tree_lens[s].
+ *   max_context_len  also the longest sequence that is computed.
+ *   num_tokens    rows of q, parents and out; rows behind the last tree are left as
+ *                 they are.
+ *   workspace     pa_tree_workspace_bytes() bytes (for the current device: it
+ *                 depends on its SM count), 16-byte aligned; its contents need no
+ *                 initialisation and are clobbered.  Calls sharing one must not
+ *                 overlap on the GPU.
+ * The query-key and probability-value products run on the tensor cores with fp32
+ * accumulation, the probabilities in two terms of the pool dtype (as
+ * pa_paged_attn_decode_shared).  Keys and values of drafted tokens that a row does not
+ * see have no effect on it, infinities and NaN among them; one that it sees with such
+ * a value makes its output NaN.  A tree length out of range, a context shorter than
+ * the tree or longer than max_context_len, and a tree that runs past num_tokens record
+ * PA_ERR_RANGE (detail: the sequence) and its rows are left as they are.  A parent out of
+ * range is recorded likewise and taken as -1.  A block id outside the pool is reported
+ * (detail: the sequence); the outputs that needed that page are undefined.  16-bit pools;
+ * num_seqs at most PA_MAX_TREE_SEQS, num_tokens at most 2^20 - 2, num_kv_heads * (num_seqs +
+ * num_tokens * num_q_heads / num_kv_heads / 128) * ceil(max_context_len / 128) below 2^31
+ * (else PA_ERR_UNSUPPORTED).  tree_lens is read before the dependency wait, as
+ * context_lens and block_tables are; parents after it.  Other arguments and errors as
+ * pa_paged_attn_decode.
+ */
+PA_API size_t pa_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads);
+PA_API pa_status pa_paged_attn_tree(const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
+                                    int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                                    int32_t num_q_heads, int32_t max_context_len, float scale,
+                                    const int32_t *tree_lens, const int32_t *parents, int32_t num_tokens, void *out,
+                                    void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * tree_accept — the drafted tokens that the model confirms, and the cache compacted
+ * to them.  A token is accepted if it has no parent, or if its parent is accepted and
+ * draft_tokens[i] == target_tokens[parent].  The deepest accepted token (of equally deep
+ * ones the lowest index) ends sequence s's path: path[s][0 .. len) its ancestors from
+ * the top down and itself, path[s][len .. path_stride) = -1, path_lens[s] = len,
+ * next_tokens[s] its target, new_context_lens[s] = context_lens[s] - n + len.  In each
+ * of num_layers pools the K and V rows of path[s][i] move to position
+ * context_lens[s] - n + i of the block table (bit for bit, in place); rows behind the new
+ * length are left.  A tree of no tokens: len 0, next token -1, the length unchanged.
+ *   draft_tokens, target_tokens  int64 [num_tokens]: the tokens, and the model's choice
+ *                 after each of them.
+ *   pools         HOST array [num_layers] of layer pools with one geometry (num_blocks,
+ *                 num_kv_heads, dtype); read during the call.  num_layers 0: nothing is
+ *                 moved (pools and block_tables are not read).
+ *   path          int32 [num_seqs][path_stride], path_stride >= 1.
+ *   path_lens     int32 [num_seqs]; next_tokens int64 [num_seqs]; new_context_lens int32
+ *                 [num_seqs], apart from context_lens (PA_ERR_SHAPE).
+ * The blocks of the drafted tokens must be the sequence's own (as reserved ones are).  With
+ * the allocator, then: pa_sequence_commit of the drafted tokens and pa_sequence_truncate
+ * to the new length.  A tree length outside [0, min(path_stride, PA_MAX_TREE_LEN)], a
+ * context shorter than the tree or beyond the block table, a tree that runs past
+ * num_tokens and a parent out of range record PA_ERR_RANGE (detail: the sequence):
+ * nothing of it moves, len = 0, next token and new length -1 (a length that every call
+ * refuses).  A block id outside the pool is recorded likewise and its rows are not
+ * moved.  All metadata is read after the dependency wait.  num_seqs at most 65536.
+ */
+PA_API pa_status pa_tree_accept(const int64_t *draft_tokens, const int64_t *target_tokens, const int32_t *parents,
+                                int32_t num_tokens, const int32_t *tree_lens, const int32_t *context_lens,
+                                int32_t num_seqs, const pa_kv_pool *pools, int32_t num_layers,
+                                const int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *path,
+                                int32_t path_stride, int32_t *path_lens, int64_t *next_tokens,
+                                int32_t *new_context_lens, pa_stream_t stream);
+/*
+ * tree_move — the cache compacted to paths found by other means (sampled
+ * verification): the moves and new lengths of pa_tree_accept for the given path
+ * and path_lens, which are read only (path_stride bounds the paths, not the trees).  A
+ * path that is longer than its tree, not ascending or out of range records PA_ERR_RANGE (detail: the sequence) as above.
+ */
+PA_API pa_status pa_tree_move(const int32_t *path, int32_t path_stride, const int32_t *path_lens,
+                              const int32_t *tree_lens, const int32_t *context_lens, int32_t num_seqs,
+                              const pa_kv_pool *pools, int32_t num_layers, const int32_t *block_tables,
+                              int32_t max_blocks_per_seq, int32_t *new_context_lens, pa_stream_t stream);
 
 /*
  * ---- copy-on-write and the block-table builder [P1, qwen_serve/paged.py:

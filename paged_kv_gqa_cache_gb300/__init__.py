@@ -19,6 +19,9 @@ Calls (see include/pagedattn.h for the full contract):
 * ``qk_norm_rope_kv_write``: q/k RMSNorm + rotary embedding fused into the KV write
 * ``rope_kv_write``: rotary embedding of any layout, width and frequencies (``rope_inv_freq``
   for the long-context scalings), with the KV write
+* ``rope_kv_write_axes``: the same for positions of several axes (``rope_axes``: time, height, width)
+* ``paged_attn_tree``: attention of drafted tokens that form a tree behind each sequence's context
+* ``tree_accept`` / ``tree_move``: the drafts that the model confirms, and every layer's cache compacted to them
 * ``paged_attn_decode_shared``: decode for sequences that share prefixes by groups, each computed once
 * ``paged_attn_decode_weights``: decode that accumulates the attention weight of every cached token
 * ``kv_evict``: a cache shortened to a budget by accumulated attention weight
@@ -57,7 +60,8 @@ EXPORTS = ("pa_kv_cache_write", "pa_decode_workspace_bytes", "pa_paged_attn_deco
            "pa_mixed_step_workspace_bytes", "pa_rope_inv_freq", "pa_rope_kv_write", "pa_kv_evict", "pa_kv_evict_ex",
            "pa_decode_shared_workspace_bytes", "pa_paged_attn_decode_shared",
            "pa_decode_weights_workspace_bytes", "pa_paged_attn_decode_weights",
-           "pa_sequence_unshare", "pa_sequence_truncate",
+           "pa_sequence_unshare", "pa_sequence_truncate", "pa_rope_kv_write_axes", "pa_tree_workspace_bytes",
+           "pa_paged_attn_tree", "pa_tree_accept", "pa_tree_move",
            "pa_allocator_create", "pa_allocator_destroy", "pa_allocator_allocate", "pa_allocator_retain",
            "pa_allocator_release", "pa_allocator_refcount", "pa_allocator_stats_get", "pa_allocator_take_copies",
            "pa_sequence_create", "pa_sequence_destroy", "pa_sequence_reserve", "pa_sequence_commit",
@@ -169,6 +173,18 @@ def load_library(path: str = LIB_PATH):
         lib.pa_rope_kv_write.argtypes = [P, P, P, ctypes.POINTER(Rope), P, P, ctypes.c_float, P, P, i32, i32, P,
                                          pool_p, P]
         lib.pa_rope_kv_write.restype = i32
+        lib.pa_rope_kv_write_axes.argtypes = [P, P, P, ctypes.POINTER(Rope), ctypes.c_char_p, i32, P, P, ctypes.c_float,
+                                              P, P, i32, i32, P, pool_p, P]
+        lib.pa_rope_kv_write_axes.restype = i32
+        lib.pa_tree_workspace_bytes.argtypes = [i32, i32, i32]
+        lib.pa_tree_workspace_bytes.restype = ctypes.c_size_t
+        lib.pa_paged_attn_tree.argtypes = [P, pool_p, P, i32, P, i32, i32, i32, ctypes.c_float, P, P, i32, P, P,
+                                           ctypes.c_size_t, P]
+        lib.pa_paged_attn_tree.restype = i32
+        lib.pa_tree_accept.argtypes = [P, P, P, i32, P, P, i32, pool_p, i32, P, i32, P, i32, P, P, P, P]
+        lib.pa_tree_accept.restype = i32
+        lib.pa_tree_move.argtypes = [P, i32, P, P, P, i32, pool_p, i32, P, i32, P, P]
+        lib.pa_tree_move.restype = i32
         lib.pa_decode_shared_workspace_bytes.argtypes = [i32, i32, i32, i32]
         lib.pa_decode_shared_workspace_bytes.restype = ctypes.c_size_t
         lib.pa_paged_attn_decode_shared.argtypes = [P, pool_p, P, i32, P, i32, i32, i32, ctypes.c_float, P, P, i32,
@@ -845,7 +861,8 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
                   positions: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   interleaved: bool = False, attention_factor: float = 1.0,
                   q_norm_weight: Optional[torch.Tensor] = None, k_norm_weight: Optional[torch.Tensor] = None,
-                  eps: float = 1e-6, q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                  eps: float = 1e-6, q_out: Optional[torch.Tensor] = None, stream=None,
+                  _axes: Optional[bytes] = None) -> torch.Tensor:
     """Rotate q [T, Hq, 128] (returned; ``q_out=q`` works in place) and k
     [T, Hkv, 128] to ``positions``, after an RMSNorm where the weights are given,
     and write the rotated k and the unchanged v into their slots.
@@ -864,8 +881,14 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
     qshape = q.shape
     T, hq = qshape[:2] if len(qshape) == 3 else (0, 0)
     rows, each = (T, hkv, d), (T,)
-    if qshape != (T, hq, d) or k.shape != rows or v.shape != rows or positions.shape != each \
-            or slot_mapping.shape != each or inv_freq.dim() != 1:
+    if _axes is not None:
+        if positions.dim() != 2 or positions.shape[1] != T:
+            raise ValueError(f"positions must be [axes, {T}]")
+        if len(_axes) != inv_freq.numel():
+            raise ValueError(f"pair_axes names {len(_axes)} pairs, inv_freq holds {inv_freq.numel()}")
+    elif positions.shape != each:
+        raise ValueError(f"positions must be [{T}]")
+    if qshape != (T, hq, d) or k.shape != rows or v.shape != rows or slot_mapping.shape != each or inv_freq.dim() != 1:
         raise ValueError("q [T, Hq, 128], k/v [T, Hkv, 128], positions/slot_mapping [T], inv_freq [rotary_dim / 2]")
     if not fresh and q_out.shape != qshape:
         raise ValueError("q_out must have the shape of q")
@@ -880,11 +903,46 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
         wk = None if k_norm_weight is None else k_norm_weight.data_ptr()
     rope = Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], ROPE_INTERLEAVED if interleaved else ROPE_HALF,
                 attention_factor)
+    if _axes is not None:
+        _check((_lib or load_library()).pa_rope_kv_write_axes(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(rope), _axes, positions.shape[0], wq, wk, eps,
+            positions.data_ptr(), slot_mapping.data_ptr(), T, hq, q_out.data_ptr(), ctypes.byref(pool),
+            _stream_of(stream, dev)), "pa_rope_kv_write_axes")
+        return q_out
     _check((_lib or load_library()).pa_rope_kv_write(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(rope), wq, wk, eps, positions.data_ptr(),
         slot_mapping.data_ptr(), T, hq, q_out.data_ptr(), ctypes.byref(pool), _stream_of(stream, dev)),
         "pa_rope_kv_write")
     return q_out
+
+
+ROPE_MAX_AXES = 4
+
+
+def rope_axes(sections, woven: bool = False) -> bytes:
+    """The axis of every rotated pair (``pair_axes`` of :func:`rope_kv_write_axes`) when
+    axis a turns ``sections[a]`` of the pairs: section after section, or ``woven``,
+    the axes in turn, each as long as its section lasts.  Made once per model."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= ROPE_MAX_AXES or min(left) < 0 or not 1 <= sum(left) <= 64:
+        raise ValueError(f"sections must be 1 to {ROPE_MAX_AXES} counts with 1 to 64 pairs in all")
+    if not woven:
+        return b"".join(bytes([a]) * n for a, n in enumerate(left))
+    return bytes(a for i in range(max(left)) for a, n in enumerate(left) if i < n)
+
+
+def rope_kv_write_axes(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: torch.Tensor,
+                       positions: torch.Tensor, pair_axes: bytes, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                       v_cache: torch.Tensor, interleaved: bool = False, attention_factor: float = 1.0,
+                       q_norm_weight: Optional[torch.Tensor] = None, k_norm_weight: Optional[torch.Tensor] = None,
+                       eps: float = 1e-6, q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """:func:`rope_kv_write` for ``positions`` of several axes, int32 [axes, T] (time,
+    height, width of images and video): pair i turns by the position on axis
+    ``pair_axes[i]`` (bytes [rotary_dim / 2], see :func:`rope_axes`)."""
+    if not isinstance(pair_axes, bytes):
+        raise TypeError("pair_axes must be bytes (see rope_axes)")
+    return rope_kv_write(q, k, v, inv_freq, positions, slot_mapping, k_cache, v_cache, interleaved, attention_factor,
+                         q_norm_weight, k_norm_weight, eps, q_out, stream, _axes=pair_axes)
 
 
 def decode_shared_workspace_bytes(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int) -> int:
@@ -1045,6 +1103,153 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
         recent, sinks, dst.data_ptr(), dst.shape[1], w_out.data_ptr(), wos[2], kept.data_ptr(),
         new_context_lens.data_ptr(), flags, _stream_of(stream, dev)), "pa_kv_evict_ex")
     return kept, new_context_lens
+
+
+# ---- trees of drafted tokens -------------------------------------------------------------
+
+MAX_TREE_LEN, MAX_TREE_SEQS = 256, 2048
+
+
+def tree_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int) -> int:
+    return int(load_library().pa_tree_workspace_bytes(num_seqs, num_q_heads, num_kv_heads))
+
+
+def alloc_tree_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, device=None) -> torch.Tensor:
+    n = tree_workspace_bytes(num_seqs, num_q_heads, num_kv_heads)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_attn_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                    context_lens: torch.Tensor, tree_lens: torch.Tensor, parents: torch.Tensor, scale: float,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    max_context_len: Optional[int] = None, stream=None) -> torch.Tensor:
+    """Attention of drafted tokens: q [T, Hq, 128] (the sequences' drafts packed in
+    order) to out, same shape.  The last ``tree_lens[s]`` (int32 [S]) of sequence s's
+    ``context_lens[s]`` cached tokens are its drafts; ``parents`` (int32 [T]) gives each
+    token's parent as an index within its tree (less than its own; -1: none).  A token
+    sees the committed context, its ancestors and itself.  ``max_context_len`` (default:
+    the block table's capacity) is also the longest sequence that is computed."""
+    dev = _device()
+    pool = _pool_of(k_cache, v_cache, dev)
+    dt, i32 = k_cache.dtype, torch.int32
+    fresh = out is None
+    if fresh:
+        out = _result(stream, torch.empty_like, q)
+    if not (_fine(dev, dt, q, out) and _fine(dev, i32, block_tables, context_lens, tree_lens, parents)):
+        _check_all(dev, (q, "q", dt), (block_tables, "block_tables", i32), (context_lens, "context_lens", i32),
+                   (tree_lens, "tree_lens", i32), (parents, "parents", i32), (out, "out", dt))
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != pool.head_dim:
+        raise ValueError(f"q must be [T, Hq, {pool.head_dim}]")
+    if not fresh and out.shape != shape:
+        raise ValueError("out must have the shape of q")
+    T, hq, _ = shape
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [S, max_blocks]")
+    S, mb = block_tables.shape
+    if context_lens.shape != (S,) or tree_lens.shape != (S,) or parents.shape != (T,):
+        raise ValueError(f"context_lens and tree_lens must be [{S}], parents [{T}]")
+    if workspace is None:
+        workspace = _fresh(stream, alloc_tree_workspace, S, hq, pool.num_kv_heads, q.device)
+    if not _fine(dev, torch.uint8, workspace):
+        _check_all(dev, (workspace, "workspace", None))
+    _check((_lib or load_library()).pa_paged_attn_tree(
+        q.data_ptr(), ctypes.byref(pool), block_tables.data_ptr(), mb, context_lens.data_ptr(), S, hq,
+        mb * pool.block_size if max_context_len is None else max_context_len, scale, tree_lens.data_ptr(),
+        parents.data_ptr(), T, out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_of(stream, dev)),
+        "pa_paged_attn_tree")
+    return out
+
+
+class LayerPools:
+    """Descriptors of every layer's pool (see :func:`layer_pools`); keeps their tensors alive."""
+
+    def __init__(self, pools):
+        self.tensors = [(k, v) for k, v in pools]
+        descs = [make_pool(k, v) for k, v in self.tensors]
+        self.count = len(descs)
+        self.array = (KVPool * max(self.count, 1))(*descs)
+        devices = {t.get_device() for pair in self.tensors for t in pair}
+        if len(devices) > 1:
+            raise ValueError("the layers' pools must be on one device")
+        self.device = devices.pop() if devices else None
+
+
+def layer_pools(pools) -> LayerPools:
+    """Descriptors of the layers' pools, (k_cache, v_cache) each and of one geometry,
+    made once and kept with the cache (:func:`tree_accept`, :func:`tree_move`)."""
+    return LayerPools(pools)
+
+
+def _layer_args(dev: int, pools: Optional[LayerPools], block_tables: Optional[torch.Tensor], S: int):
+    """(pools, layers, block tables, their width) as the library takes them."""
+    if pools is None:
+        return None, 0, None, 0
+    if not isinstance(pools, LayerPools):
+        raise TypeError("pools must come from layer_pools")
+    if pools.count and pools.device != dev:
+        raise ValueError(f"the pools are on cuda:{pools.device}, the current device is cuda:{dev}")
+    if not _fine(dev, torch.int32, block_tables):
+        _check_all(dev, (block_tables, "block_tables", torch.int32))
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError(f"block_tables must be [{S}, max_blocks]")
+    return pools.array, pools.count, block_tables.data_ptr(), block_tables.shape[1]
+
+
+def tree_accept(draft_tokens: torch.Tensor, target_tokens: torch.Tensor, parents: torch.Tensor,
+                tree_lens: torch.Tensor, context_lens: torch.Tensor, pools: Optional[LayerPools] = None,
+                block_tables: Optional[torch.Tensor] = None, max_tree_len: int = MAX_TREE_LEN, stream=None):
+    """The drafted tokens (packed int64 [T], trees as in :func:`paged_attn_tree`) that
+    the model's choices ``target_tokens`` (int64 [T], after each of them) confirm, and
+    every layer's cache compacted to them in place (``pools`` from
+    :func:`layer_pools`; None: nothing is moved).  Returns (path int32 [S, max_tree_len],
+    -1 past its end; path lengths int32 [S]; the next tokens int64 [S]; new context
+    lengths int32 [S]); a refused sequence gets an empty path, and -1 in the others."""
+    dev = _device()
+    i32, i64 = torch.int32, torch.int64
+    if not (_fine(dev, i64, draft_tokens, target_tokens) and _fine(dev, i32, parents, tree_lens, context_lens)):
+        _check_all(dev, (draft_tokens, "draft_tokens", i64), (target_tokens, "target_tokens", i64),
+                   (parents, "parents", i32), (tree_lens, "tree_lens", i32), (context_lens, "context_lens", i32))
+    if draft_tokens.dim() != 1 or tree_lens.dim() != 1:
+        raise ValueError("draft_tokens must be [T], tree_lens [S]")
+    T, S = draft_tokens.shape[0], tree_lens.shape[0]
+    if target_tokens.shape != (T,) or parents.shape != (T,) or context_lens.shape != (S,):
+        raise ValueError(f"target_tokens and parents must be [{T}], context_lens [{S}]")
+    if max_tree_len < 1:
+        raise ValueError("max_tree_len must be at least 1")
+    array, layers, tables, mb = _layer_args(dev, pools, block_tables, S)
+    path = _result(stream, lambda: torch.empty((S, max_tree_len), dtype=i32, device=tree_lens.device))
+    path_lens = _result(stream, torch.empty_like, tree_lens)
+    next_tokens = _result(stream, lambda: torch.empty((S,), dtype=i64, device=tree_lens.device))
+    new_lens = _result(stream, torch.empty_like, tree_lens)
+    _check((_lib or load_library()).pa_tree_accept(
+        draft_tokens.data_ptr(), target_tokens.data_ptr(), parents.data_ptr(), T, tree_lens.data_ptr(),
+        context_lens.data_ptr(), S, array, layers, tables, mb, path.data_ptr(), max_tree_len, path_lens.data_ptr(),
+        next_tokens.data_ptr(), new_lens.data_ptr(), _stream_of(stream, dev)), "pa_tree_accept")
+    return path, path_lens, next_tokens, new_lens
+
+
+def tree_move(path: torch.Tensor, path_lens: torch.Tensor, tree_lens: torch.Tensor, context_lens: torch.Tensor,
+              pools: LayerPools, block_tables: torch.Tensor, stream=None) -> torch.Tensor:
+    """Every layer's cache compacted to paths found by other means: the first
+    ``path_lens[s]`` of ``path[s]`` (int32 [S, stride], ascending indices within the
+    tree).  Returns the new context lengths (-1: refused)."""
+    dev = _device()
+    i32 = torch.int32
+    if not _fine(dev, i32, path, path_lens, tree_lens, context_lens):
+        _check_all(dev, (path, "path", i32), (path_lens, "path_lens", i32), (tree_lens, "tree_lens", i32),
+                   (context_lens, "context_lens", i32))
+    if path.dim() != 2:
+        raise ValueError("path must be [S, stride]")
+    S, stride = path.shape
+    if path_lens.shape != (S,) or tree_lens.shape != (S,) or context_lens.shape != (S,):
+        raise ValueError(f"path_lens, tree_lens and context_lens must be [{S}]")
+    array, layers, tables, mb = _layer_args(dev, pools, block_tables, S)
+    new_lens = _result(stream, torch.empty_like, context_lens)
+    _check((_lib or load_library()).pa_tree_move(
+        path.data_ptr(), stride, path_lens.data_ptr(), tree_lens.data_ptr(), context_lens.data_ptr(), S, array, layers,
+        tables, mb, new_lens.data_ptr(), _stream_of(stream, dev)), "pa_tree_move")
+    return new_lens
 
 
 # ---- copy-on-write block copy and the host-side block-table builder ---------------------

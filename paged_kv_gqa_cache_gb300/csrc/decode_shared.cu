@@ -45,7 +45,7 @@
 // 14.9 and 13.8 us, 16384: 24.4 and 29.2; 16, 256: 9.4 and 6.0, 1024: 11.2 and 12.5;
 // 32, 1024: 14.7 and 25.3).
 #include "decode_mma.cuh"
-#include "prefill_kernel.cuh"
+#include "piece_softmax.cuh"
 
 namespace pa {
 namespace {
@@ -264,33 +264,8 @@ __device__ __forceinline__ bool suffix_worker(const CUtensorMap &kpage, const CU
 // P goes into P V in two terms, P_hi = round(P) and P_lo = round(P - P_hi), like
 // the suffix's, whatever the group's size: a sequence's output does not lose
 // precision because others joined its group.  The 8 more MMAs per key tile are
-// 0.26 us of tensor time.  A row's reference m_ref is kBelow under a maximum, and
-// O is rescaled once a maximum is more than kTop above it.  bf16 has fp32's range:
-// 0 and kRescale.  fp16 has 2^-25 to 65504, all of it used so that small weights
-// are held nearly as in the suffix: P is 2^13 or more at the row's largest (a weight
-// is off by 2^-38 of that one at most) and under 2^16.  The 2.9 between the two
-// decide how often O is rescaled (192 sequences in three groups, fp16: 108.7 us; with
-// 14 and 15 in their place 118, 13 and 15 115.5, 12 and 15 108; bf16 100.3).
+// 0.26 us of tensor time.  The rows' references: piece_softmax.cuh.
 // Then warp i < 8 consumes and warp 8 + i fetches the pages of a suffix worker.
-template <typename T>
-constexpr float kBelow = std::is_same<T, __half>::value ? 13.f : 0.f;
-template <typename T>
-constexpr float kTop = std::is_same<T, __half>::value ? 15.9f : kRescale;
-template <typename T>
-constexpr float kTopSum = std::is_same<T, __half>::value ? 61147.f : kRescaleSum;  // 2^kTop: a half-row sum bound
-// The reference for a maximum mc, and what a maximum mc may reach above the
-// reference: kBelow under it and kTop, while such sums are good to 2^-4; past that
-// mc itself and nothing, since fp16 has no room for their roundings (weights under
-// 2^-25 of the largest are then lost in fp16).
-template <typename T>
-__device__ __forceinline__ float reference_of(float mc) {
-  return kBelow<T> == 0.f || fabsf(mc) >= 1048576.f ? mc : mc - kBelow<T>;
-}
-template <typename T>
-__device__ __forceinline__ float top_of(float mc) {
-  return kBelow<T> != 0.f && fabsf(mc) >= 1048576.f ? 0.f : kTop<T>;
-}
-
 template <typename T, int G>
 __global__ void __launch_bounds__(kThreads, 1)
 shared_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kpage,

@@ -790,16 +790,21 @@ pa_status pa_rope_inv_freq(int32_t scaling, int32_t rotary_dim, double theta, do
   return PA_OK;
 }
 
-pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, const pa_rope *rope, const void *q_norm_weight,
-                           const void *k_norm_weight, float eps, const int32_t *positions,
-                           const int64_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads, void *q_out,
-                           const pa_kv_pool *pool, pa_stream_t stream) {
+pa_status pa_rope_kv_write_axes(const void *q, const void *k, const void *v, const pa_rope *rope,
+                                const uint8_t *pair_axes, int32_t num_axes, const void *q_norm_weight,
+                                const void *k_norm_weight, float eps, const int32_t *positions,
+                                const int64_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads, void *q_out,
+                                const pa_kv_pool *pool, pa_stream_t stream) {
   pa_status st = check_pool(pool);
   if (st != PA_OK) return st;
   if (!rope || !rope->inv_freq) return PA_ERR_NULL;
   if (rope->rotary_dim < 2 || rope->rotary_dim > kHeadDim || rope->rotary_dim % 2 != 0) return PA_ERR_SHAPE;
   if (rope->layout != PA_ROPE_HALF && rope->layout != PA_ROPE_INTERLEAVED) return PA_ERR_UNSUPPORTED;
   if (!isfinite(rope->attention_factor)) return PA_ERR_SHAPE;
+  if (!pair_axes) return PA_ERR_NULL;
+  if (num_axes < 1 || num_axes > PA_ROPE_MAX_AXES) return PA_ERR_SHAPE;
+  for (int i = 0; i < rope->rotary_dim / 2; ++i)
+    if (pair_axes[i] >= num_axes) return PA_ERR_SHAPE;
   if (num_tokens < 0) return PA_ERR_SHAPE;
   if (num_tokens == 0) return PA_OK;
   if (!q || !k || !v || !positions || !slot_mapping || !q_out ||
@@ -836,12 +841,23 @@ pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, const pa
   p.num_tokens = num_tokens;
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = pool->num_kv_heads;
+  p.num_axes = num_axes;
+  for (int i = 0; i < rope->rotary_dim / 2; ++i) p.pair_axis[i] = pair_axes[i];
   p.rotary_dim = rope->rotary_dim;
   p.interleaved = rope->layout == PA_ROPE_INTERLEAVED;
   p.attention_factor = rope->attention_factor;
   p.eps = eps;
   cudaError_t e = launch_rope_kv(p, pool->dtype, d->sm_count, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+pa_status pa_rope_kv_write(const void *q, const void *k, const void *v, const pa_rope *rope, const void *q_norm_weight,
+                           const void *k_norm_weight, float eps, const int32_t *positions,
+                           const int64_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads, void *q_out,
+                           const pa_kv_pool *pool, pa_stream_t stream) {
+  static constexpr uint8_t one_axis[kHeadDim / 2] = {};
+  return pa_rope_kv_write_axes(q, k, v, rope, one_axis, 1, q_norm_weight, k_norm_weight, eps, positions, slot_mapping,
+                               num_tokens, num_q_heads, q_out, pool, stream);
 }
 
 size_t pa_decode_shared_workspace_bytes(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
@@ -1040,6 +1056,155 @@ pa_status pa_kv_evict(const pa_kv_pool *pool, const int32_t *block_tables, int32
   return pa_kv_evict_ex(pool, block_tables, max_blocks_per_seq, context_lens, num_seqs, weights, weights_stride, budget,
                         recent, sinks, dst_block_tables, dst_max_blocks, weights_out, weights_out_stride, kept,
                         new_context_lens, 0, stream);
+}
+
+size_t pa_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads) {
+  if (num_seqs < 0 || num_seqs > kTreeMaxSeqs || num_kv_heads < 1 || num_q_heads < 1 || num_q_heads % num_kv_heads != 0)
+    return 0;
+  const int sms = sm_count();
+  return tree_workspace_bytes(sms > 0 ? sms : 1);
+}
+
+pa_status pa_paged_attn_tree(const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
+                             int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                             int32_t num_q_heads, int32_t max_context_len, float scale, const int32_t *tree_lens,
+                             const int32_t *parents, int32_t num_tokens, void *out, void *workspace,
+                             size_t workspace_bytes, pa_stream_t stream) {
+  if (num_tokens < 0) return PA_ERR_SHAPE;
+  // (a call without rows is one without sequences: its other arguments are checked no further)
+  pa_status st = decode_check_args(q, pool, block_tables, max_blocks_per_seq, context_lens, num_tokens ? num_seqs : 0,
+                                   num_q_heads, max_context_len, scale, out);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0) return PA_ERR_SHAPE;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!tree_lens || !parents) return PA_ERR_NULL;
+  if (num_seqs > kTreeMaxSeqs || num_tokens > (1 << 20) - 2) return PA_ERR_UNSUPPORTED;
+  const int group = num_q_heads / pool->num_kv_heads;
+  // the work is counted in 32 bits: (query tile, key tile) pairs
+  const int64_t tiles = (int64_t)pool->num_kv_heads * (num_seqs + (int64_t)num_tokens * group / 128);
+  if (tiles * (((int64_t)max_context_len + 127) / 128) > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (!aligned4(tree_lens) || !aligned4(parents)) return PA_ERR_ALIGN;
+  if (!workspace) return PA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return PA_ERR_ALIGN;
+  DeviceState *d = nullptr;
+  if ((st = device_state(&d)) != PA_OK) return st;  // also readies the tensor-map encoder
+  if (workspace_bytes < tree_workspace_bytes(d->sm_count)) return PA_ERR_WORKSPACE;
+  CUtensorMap maps[3];
+  if (!pool_map(&maps[0], pool, pool->k_cache, false) || !pool_map_vpages(&maps[1], pool, pool->v_cache) ||
+      !query_map(&maps[2], q, pool->dtype, num_q_heads, num_tokens, group))
+    return PA_ERR_CUDA;
+  TreeParams p{};
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.tree_lens = tree_lens;
+  p.parents = parents;
+  p.out = out;
+  p.err = d->err;
+  p.max_len = max_context_len;  // (at most the block table's capacity)
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.num_kv_heads = pool->num_kv_heads;
+  p.num_q_heads = num_q_heads;
+  p.num_blocks = pool->num_blocks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaError_t e = launch_attn_tree(p, workspace, maps, pool->dtype, group, d->sm_count,
+                                   static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+namespace {
+
+// The moves of pa_tree_accept and pa_tree_move, their other checks made (p holds
+// what differs between them).
+pa_status tree_move_call(TreeAcceptParams &p, const int32_t *tree_lens, const int32_t *context_lens, int32_t num_seqs,
+                         const pa_kv_pool *pools, int32_t num_layers, const int32_t *block_tables,
+                         int32_t max_blocks_per_seq, int32_t *new_context_lens, pa_stream_t stream) {
+  if (num_seqs < 0 || num_layers < 0 || p.path_stride < 1) return PA_ERR_SHAPE;
+  for (int32_t l = 0; l < num_layers; ++l) {
+    if (!pools) return PA_ERR_NULL;
+    pa_status st = check_pool(&pools[l]);
+    if (st != PA_OK) return st;
+    if (pools[l].num_blocks != pools[0].num_blocks || pools[l].num_kv_heads != pools[0].num_kv_heads ||
+        pools[l].dtype != pools[0].dtype)
+      return PA_ERR_SHAPE;
+  }
+  if (num_seqs == 0) return PA_OK;
+  if (!p.path || !p.path_lens || !tree_lens || !context_lens || !new_context_lens || (num_layers > 0 && !block_tables))
+    return PA_ERR_NULL;
+  if (num_layers > 0 && max_blocks_per_seq < 1) return PA_ERR_SHAPE;
+  if (num_seqs > 65536) return PA_ERR_UNSUPPORTED;
+  if (!aligned4(p.path) || !aligned4(p.path_lens) || !aligned4(tree_lens) || !aligned4(context_lens) ||
+      !aligned4(block_tables) || !aligned4(new_context_lens))
+    return PA_ERR_ALIGN;
+  const size_t lens_bytes = (size_t)num_seqs * sizeof(int32_t);
+  if (overlap(context_lens, lens_bytes, new_context_lens, lens_bytes)) return PA_ERR_SHAPE;
+  DeviceState *d = nullptr;
+  pa_status st = device_state(&d);
+  if (st != PA_OK) return st;
+  p.tree_lens = tree_lens;
+  p.context_lens = context_lens;
+  p.block_tables = num_layers > 0 ? block_tables : nullptr;
+  p.new_lens = new_context_lens;
+  p.err = d->err;
+  p.num_seqs = num_seqs;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_blocks = num_layers > 0 ? pools[0].num_blocks : 0;
+  p.row_vecs = num_layers > 0 ? pools[0].num_kv_heads * kHeadDim * 2 / 16 : 1;
+  p.first = 1;
+  int32_t l0 = 0;
+  do {  // up to kCopyLayers layers per launch; the later ones take the path that the first found
+    p.num_layers = num_layers - l0 < kCopyLayers ? num_layers - l0 : kCopyLayers;
+    for (int i = 0; i < p.num_layers; ++i) {
+      p.k[i] = pools[l0 + i].k_cache;
+      p.v[i] = pools[l0 + i].v_cache;
+    }
+    cudaError_t e = launch_tree_accept(p, d->sm_count, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e);
+    p.first = 0;
+    p.next_tokens = nullptr;
+    l0 += kCopyLayers;
+  } while (l0 < num_layers);
+  return PA_OK;
+}
+
+}  // namespace
+
+pa_status pa_tree_accept(const int64_t *draft_tokens, const int64_t *target_tokens, const int32_t *parents,
+                         int32_t num_tokens, const int32_t *tree_lens, const int32_t *context_lens, int32_t num_seqs,
+                         const pa_kv_pool *pools, int32_t num_layers, const int32_t *block_tables,
+                         int32_t max_blocks_per_seq, int32_t *path, int32_t path_stride, int32_t *path_lens,
+                         int64_t *next_tokens, int32_t *new_context_lens, pa_stream_t stream) {
+  if (num_tokens < 0) return PA_ERR_SHAPE;
+  if (num_seqs > 0) {
+    if (!next_tokens || (num_tokens > 0 && (!draft_tokens || !target_tokens || !parents))) return PA_ERR_NULL;
+    if (((reinterpret_cast<uintptr_t>(draft_tokens) | reinterpret_cast<uintptr_t>(target_tokens) |
+          reinterpret_cast<uintptr_t>(next_tokens)) & 7u) || !aligned4(parents))
+      return PA_ERR_ALIGN;
+  }
+  TreeAcceptParams p{};
+  p.draft = draft_tokens;
+  p.target = target_tokens;
+  p.parents = parents;
+  p.num_tokens = num_tokens;
+  p.path = path;
+  p.path_stride = path_stride;
+  p.path_lens = path_lens;
+  p.next_tokens = next_tokens;
+  return tree_move_call(p, tree_lens, context_lens, num_seqs, pools, num_layers, block_tables, max_blocks_per_seq,
+                        new_context_lens, stream);
+}
+
+pa_status pa_tree_move(const int32_t *path, int32_t path_stride, const int32_t *path_lens, const int32_t *tree_lens,
+                       const int32_t *context_lens, int32_t num_seqs, const pa_kv_pool *pools, int32_t num_layers,
+                       const int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *new_context_lens,
+                       pa_stream_t stream) {
+  TreeAcceptParams p{};
+  p.path = const_cast<int32_t *>(path);  // (read only without drafts)
+  p.path_stride = path_stride;
+  p.path_lens = const_cast<int32_t *>(path_lens);
+  return tree_move_call(p, tree_lens, context_lens, num_seqs, pools, num_layers, block_tables, max_blocks_per_seq,
+                        new_context_lens, stream);
 }
 
 pa_status pa_kv_block_copy(const pa_kv_pool *pools, int32_t num_layers, const int32_t *pairs, int32_t num_pairs,

@@ -83,7 +83,7 @@ struct RopeKvParams {
   const void *q_weight;      // [128], null: no RMSNorm
   const void *k_weight;
   const double *inv_freq;    // [rotary_dim / 2]
-  const int32_t *positions;  // [T]
+  const int32_t *positions;  // [num_axes][T]
   const int64_t *slots;      // [T]
   void *q_out;               // [T][Hq][128]
   void *k_cache;
@@ -93,6 +93,8 @@ struct RopeKvParams {
   int32_t num_tokens;
   int32_t num_q_heads;
   int32_t num_kv_heads;
+  int32_t num_axes;
+  uint8_t pair_axis[kHeadDim / 2];  // the axis whose position turns pair i
   int32_t rotary_dim;
   int32_t interleaved;
   float attention_factor;
@@ -284,6 +286,58 @@ size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int
 // maps: K in 2 KB half boxes (prefix), K in 4 KB pages (suffix), V in 4 KB pages, q.
 cudaError_t launch_decode_shared(SharedParams sp, const PrefillParams &pp, DecodeParams dp, void *workspace,
                                  const CUtensorMap *maps, int dtype, int group, int sms, cudaStream_t stream);
+
+// ---- attention of drafted tokens that form a tree (16-bit pools) -----------------------
+constexpr int kTreeMaxSeqs = 2048;  // their prefixes in shared memory
+struct TreeParams {
+  const int32_t *block_tables;
+  const int32_t *context_lens;  // drafted tokens included
+  const int32_t *tree_lens;
+  const int32_t *parents;       // [num_tokens]
+  void *out;                    // [num_tokens][Hq][128]
+  int *err;
+  int32_t *records;             // workspace: per CTA, what the join needs of its last run
+  float2 *ws_ml;                //   per piece and row: (max, sum)
+  float *ws_o;                  //   per piece: [dims / 4][128 rows][4] unnormalised outputs
+  int64_t max_len;              // the longest sequence that is computed
+  int32_t max_blocks_per_seq;
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t num_q_heads;
+  int32_t num_blocks;
+  float scale_log2;
+};
+size_t tree_workspace_bytes(int sms);
+// maps: K in 2 KB half boxes, V in 4 KB pages, q.
+cudaError_t launch_attn_tree(TreeParams p, void *workspace, const CUtensorMap *maps, int dtype, int group, int sms,
+                             cudaStream_t stream);
+
+// ---- the accepted path of such a tree, and the cache compacted to it ---------------------
+struct TreeAcceptParams {
+  const int64_t *draft;         // [num_tokens]
+  const int64_t *target;
+  const int32_t *parents;
+  const int32_t *tree_lens;     // [S]
+  const int32_t *context_lens;  // [S]
+  const int32_t *block_tables;  // [S][max_blocks_per_seq]
+  int32_t *path;                // [S][path_stride]
+  int32_t *path_lens;           // [S]
+  int64_t *next_tokens;         // [S], null: the paths are given
+  int32_t *new_lens;            // [S]
+  int *err;
+  void *k[kCopyLayers];         // pool base addresses of this launch's layers
+  void *v[kCopyLayers];
+  int32_t num_layers;           // of this launch
+  int32_t path_stride;
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t max_blocks_per_seq;
+  int32_t num_blocks;
+  int32_t row_vecs;             // 16-byte vectors per token row = Hkv * 128 * 2 / 16
+  int32_t first;                // 1: this launch writes the outputs and reports
+};
+cudaError_t launch_tree_accept(const TreeAcceptParams &p, int sms, cudaStream_t stream);
 
 // ---- one persistent launch for a mixed step (16-bit pools) ---------------------
 // The step's KV write (w), its chunks' prefill (pp: no window, no workspace)

@@ -80,7 +80,11 @@ __global__ void __launch_bounds__(kRopeKvThreads, 3) rope_kv_kernel(const RopeKv
   const int r_qk = w_qk + (lane >> 4), r_v = w_v + (lane >> 4);
   griddep_wait();  // q, k, v may be the previous kernel's output; the pool may be read by it
   long long turns = 0;
-  if (tid < TOK * 64 && (tid & 63) < d / 2) turns = turns_fixed(__ldg(p.inv_freq + (tid & 63)));
+  const int32_t *positions = p.positions;  // of this thread's pair
+  if (tid < TOK * 64 && (tid & 63) < d / 2) {
+    turns = turns_fixed(__ldg(p.inv_freq + (tid & 63)));
+    positions += (int64_t)p.pair_axis[tid & 63] * p.num_tokens;
+  }
   auto read = [&](const T *src, uint2 (&x)[2]) {
     if constexpr (MODE == kHalfPairs) {
       x[0] = *reinterpret_cast<const uint2 *>(src + d0);
@@ -106,7 +110,9 @@ __global__ void __launch_bounds__(kRopeKvThreads, 3) rope_kv_kernel(const RopeKv
   int buf = 0;
   for (int t0 = blockIdx.x * TOK; t0 < p.num_tokens; t0 += gridDim.x * TOK) {  // (block-uniform)
     const int t = t0 + tok;
-    const int pos = t < p.num_tokens ? __ldg(p.positions + t) : -1;
+    int pos = t < p.num_tokens ? __ldg(p.positions + t) : -1;
+    if (t < p.num_tokens)
+      for (int a = 1; a < p.num_axes; ++a) pos |= __ldg(p.positions + (int64_t)a * p.num_tokens + t);  // (the signs)
     const int64_t slot = t < p.num_tokens ? __ldg(p.slots + t) : -1;
     const bool ok = pos >= 0 && slot >= 0 && slot < p.num_slots;  // else nothing of the token is written
     if (!ok && t < p.num_tokens && tid % (32 * kWarps) == 0) set_error(p.err, PA_ERR_RANGE, t);
@@ -128,7 +134,7 @@ __global__ void __launch_bounds__(kRopeKvThreads, 3) rope_kv_kernel(const RopeKv
     // the step's angles, meanwhile
     if (tid < TOK * 64 && (tid & 63) < d / 2) {
       const int at = t0 + (tid >> 6);
-      const int pa = at < p.num_tokens ? __ldg(p.positions + at) : 0;
+      const int pa = at < p.num_tokens ? __ldg(positions + at) : 0;
       const long long turn = (long long)((unsigned long long)turns * (unsigned long long)(unsigned)pa);
       float s, c;
       sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
