@@ -1089,11 +1089,11 @@ pa_status pa_paged_attn_tree(const void *q, const pa_kv_pool *pool, const int32_
   DeviceState *d = nullptr;
   if ((st = device_state(&d)) != PA_OK) return st;  // also readies the tensor-map encoder
   if (workspace_bytes < tree_workspace_bytes(d->sm_count)) return PA_ERR_WORKSPACE;
-  CUtensorMap maps[3];
-  if (!pool_map(&maps[0], pool, pool->k_cache, false) || !pool_map_vpages(&maps[1], pool, pool->v_cache) ||
-      !query_map(&maps[2], q, pool->dtype, num_q_heads, num_tokens, group))
+  CUtensorMap maps[2];
+  if (!pool_map(&maps[0], pool, pool->k_cache, false) || !pool_map_vpages(&maps[1], pool, pool->v_cache))
     return PA_ERR_CUDA;
   TreeParams p{};
+  p.q = q;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.tree_lens = tree_lens;

@@ -288,15 +288,16 @@ cudaError_t launch_decode_shared(SharedParams sp, const PrefillParams &pp, Decod
                                  const CUtensorMap *maps, int dtype, int group, int sms, cudaStream_t stream);
 
 // ---- attention of drafted tokens that form a tree (16-bit pools) -----------------------
-constexpr int kTreeMaxSeqs = 2048;  // their prefixes in shared memory
+constexpr int kTreeMaxSeqs = PA_MAX_TREE_SEQS;  // their prefixes in shared memory
 struct TreeParams {
+  const void *q;                // [num_tokens][Hq][128]
   const int32_t *block_tables;
   const int32_t *context_lens;  // drafted tokens included
   const int32_t *tree_lens;
   const int32_t *parents;       // [num_tokens]
   void *out;                    // [num_tokens][Hq][128]
   int *err;
-  int32_t *records;             // workspace: per CTA, what the join needs of its last run
+  int32_t *records;             // workspace: per worker, what the join needs of its last run
   float2 *ws_ml;                //   per piece and row: (max, sum)
   float *ws_o;                  //   per piece: [dims / 4][128 rows][4] unnormalised outputs
   int64_t max_len;              // the longest sequence that is computed
@@ -309,7 +310,7 @@ struct TreeParams {
   float scale_log2;
 };
 size_t tree_workspace_bytes(int sms);
-// maps: K in 2 KB half boxes, V in 4 KB pages, q.
+// maps: K in 2 KB half boxes, V in 4 KB pages.
 cudaError_t launch_attn_tree(TreeParams p, void *workspace, const CUtensorMap *maps, int dtype, int group, int sms,
                              cudaStream_t stream);
 
