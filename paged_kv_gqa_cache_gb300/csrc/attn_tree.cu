@@ -39,23 +39,28 @@
 namespace pa {
 namespace {
 
-// Warps 0..3 softmax; 4..7 queries, masks, epilogue; 8 and 9 load K, 10 V, 11 issues the MMAs.
-constexpr int kTThreads = 384, kTWarpSide = 4, kTWarpLoad0 = 8, kTKLoad = 2, kTWarpMma = 11;
+// Warps 0..3 softmax; 4..7 drafted values and epilogue; 8 and 9 load K, 10 V, 11 issues the
+// MMAs; 12..15 queries and masks.
+constexpr int kTThreads = 512, kTWarpEpi = 4, kTWarpLoad0 = 8, kTKLoad = 2, kTWarpMma = 11, kTWarpPrep = 12;
+// Registers: 128 per thread at launch, given and taken by warpgroups (together what the
+// launch holds, so an increase never waits forever).
+constexpr int kTRegsSoftmax = 168, kTRegsEpi = 136, kTRegsLoad = 96, kTRegsPrep = 112;
+static_assert(128 * (kTRegsSoftmax + kTRegsEpi + kTRegsLoad + kTRegsPrep) <= 65536, "register split fits the launch");
 constexpr int kTStages = 3;  // of K, and of V
 constexpr int T_OFF_K = 0;
 constexpr int T_OFF_V = T_OFF_K + kTStages * 2 * kHalf;
 constexpr int kTMaskWords = PA_MAX_TREE_LEN / 32;
 constexpr int T_OFF_MASK = T_OFF_V + kTStages * 2 * kHalf;     // [run parity][token][kTMaskWords]
 constexpr int T_OFF_X = T_OFF_MASK + 2 * 128 * kTMaskWords * 4;  // (m, l) [run parity][128]
-constexpr int T_OFF_STAGE = T_OFF_X + 2 * 128 * 8;  // 1 KB per warp of 4..7: rows on their way in and out
-constexpr int T_OFF_BAR = T_OFF_STAGE + 4 * kStageBytes;
+constexpr int T_OFF_STAGE = T_OFF_X + 2 * 128 * 8;  // 1 KB per warp of 4..7 and 12..15: rows on their way out and in
+constexpr int T_OFF_BAR = T_OFF_STAGE + 8 * kStageBytes;
 // Tensor memory: two of S / P, O, two of Q (64 columns of packed pairs).
 constexpr uint32_t kTColO = 256, kTColQ = 384;
-// What the other roles want to know of a run: published by the first loader warp, which
-// finds the runs first (kb 0: no more).  8 of them: a key tile is loaded once S of the one
-// three before is done, so P V of the one five before was issued and, where that began a
-// run, O of the run before has been read.
-constexpr int kTRuns = 8;
+// What the other roles want to know of a run: published by the first loader warp a run
+// ahead of its own (kb 0: no more).  8 would do: when run u + 1 is published, of runs of one
+// key tile, tile u - 1 was loaded, so S of tile u - 4 is done, P V of tile u - 6 was issued
+// and O of run u - 7 has been read.
+constexpr int kTRuns = 10;
 struct TRunInfo {
   int32_t ka, kb, start, len;  // its key tiles; the sequence's first drafted key, and keys
   int32_t row, live_rows;      // row of the query tile's first token in q and out; rows of queries
@@ -77,10 +82,10 @@ struct TBars {
   uint32_t tmem_base;
   int32_t warp_tot[kTThreads / 32];
 };
-constexpr int T_BAR_BYTES = 1024;
+constexpr int T_BAR_BYTES = 960;
 static_assert(sizeof(TBars) <= T_BAR_BYTES, "barriers");
 constexpr int T_OFF_PLAN = T_OFF_BAR + T_BAR_BYTES;  // rows [num_seqs + 1], pairs [num_seqs + 1]
-static_assert(T_OFF_PLAN + 2 * (kTreeMaxSeqs + 1) * 4 + 1024 <= 232448, "shared memory");
+static_assert(T_OFF_PLAN + 2 * (kTreeMaxSeqs + 1) * 4 <= 232448, "shared memory");
 
 // The order of the work: sequence s has rows[s + 1] - rows[s] drafted tokens and
 // the pairs pairs[s] .. pairs[s + 1] - 1 (none for a sequence that is refused).
@@ -227,8 +232,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t IDESC_S = tc::idesc_f16(kBF16, 128, 128, false);
   constexpr uint32_t IDESC_O = tc::idesc_f16(kBF16, 128, 128, true);
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t tree_smem[];
+  uint8_t *smem = tree_smem;
   TBars &bars = *reinterpret_cast<TBars *>(smem + T_OFF_BAR);
   int32_t *rows = reinterpret_cast<int32_t *>(smem + T_OFF_PLAN), *pairs = rows + p.num_seqs + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -311,7 +316,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   int x = x0;
   bool begun = false;
 
-  if (warp < kTWarpSide) {
+  if (warp < kTWarpEpi) {
+    regs_inc<kTRegsSoftmax>();
     griddep_wait();
     // ---------------- softmax (warps 0..3) ----------------
     const int r = threadIdx.x;  // tile row = TMEM lane
@@ -411,88 +417,23 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       }
     }
   } else if (warp < kTWarpLoad0) {
+    regs_inc<kTRegsEpi>();
     griddep_wait();
-    // ---------------- queries and masks of the next run, drafted values, outputs (warps 4..7) ----------------
+    // ---------------- drafted values and outputs (warps 4..7) ----------------
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16), o_addr = lane_base + kTColO;
-    uint32_t *masks = reinterpret_cast<uint32_t *>(smem + T_OFF_MASK);
+    const uint32_t *masks = reinterpret_cast<const uint32_t *>(smem + T_OFF_MASK);
     const float2 *xm = reinterpret_cast<const float2 *>(smem + T_OFF_X);
     uint4 *stage = reinterpret_cast<uint4 *>(smem + T_OFF_STAGE + (warp & 3) * kStageBytes);
     int c0 = 0, sides = 0;
     uint32_t landed = 0;  // per stage the parity of its next drafted key tile
-    for (int ui = -1;; ++ui) {  // (the first time round only the first run is prepared)
-      // The next run, into the buffers of its parity, which the run before this one has left.
-      if (ui >= 0 && bars.info[ui % kTRuns].kb == 0) break;
-      const int un = ui + 1;
-      if (!wait_all(&bars.run_full[un % kTRuns], (un / kTRuns) & 1)) {
+    for (int ui = 0;; ++ui) {
+      if (!wait_all(&bars.q_full[ui & 1], (ui >> 1) & 1)) {
         timed_out = true;
         break;
       }
-      if (bars.info[un % kTRuns].kb != 0) {
-        const TRunInfo &I = bars.info[un % kTRuns];
-        const int par = un & 1;
-        // The queries: 64 bytes of 8 rows per load, all 32 rows of the warp (rows past the
-        // tree are zeros), turned so that a lane holds its row's on the way to tensor memory.
-        const T *q0 = static_cast<const T *>(p.q) + ((int64_t)I.row * p.num_q_heads + I.h * G) * kHeadDim;
-        const int live_rows = I.live_rows;
-        uint4 w[16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // row 8 i + lane / 4 of the warp
-          const int row = (warp & 3) * 32 + 8 * i + (lane >> 2);
-          const uint4 *src = reinterpret_cast<const uint4 *>(
-                                 q0 + ((int64_t)(row / G) * p.num_q_heads + row % G) * kHeadDim) + (lane & 3);
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) w[4 * cc + i] = row < live_rows ? __ldg(src + 4 * cc) : make_uint4(0, 0, 0, 0);
-        }
-        if (r < live_rows / G && I.kb * 128 > I.start) {  // (a run that ends in front of the tree needs no mask)
-          uint32_t *mask = masks + (par * 128 + r) * kTMaskWords;
-#pragma unroll
-          for (int k = 0; k < kTMaskWords; ++k) mask[k] = 0;
-          const int32_t *parents = p.parents + (I.row - I.tok0);
-          int a = I.tok0 + r;
-          while (true) {
-            mask[a >> 5] |= 1u << (a & 31);
-            const int up = __ldg(parents + a);
-            if (up < 0 || up >= a) {
-              if (up != -1) set_error(p.err, PA_ERR_RANGE, I.s);  // (the walk ends: as one without parent)
-              break;
-            }
-            a = up;
-          }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t v[16];
-#pragma unroll
-          for (int pass = 0; pass < 2; ++pass) {  // 16 rows at a time, the pieces swizzled against bank conflicts
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int row = 8 * i + (lane >> 2);
-              stage[row * 4 + ((lane & 3) ^ (row & 3))] = w[4 * cc + 2 * pass + i];
-            }
-            __syncwarp();
-            if ((lane >> 4) == pass) {
-              const int row = lane & 15;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint4 y = stage[row * 4 + (i ^ (row & 3))];
-                v[4 * i] = y.x;
-                v[4 * i + 1] = y.y;
-                v[4 * i + 2] = y.z;
-                v[4 * i + 3] = y.w;
-              }
-            }
-            __syncwarp();
-          }
-          tc::st_32x32b_x16(lane_base + kTColQ + par * 64 + cc * 16, v);
-        }
-        tc::wait_st();
-        tc::fence_before_sync();
-      }
-      mbar_arrive(&bars.q_full[un & 1]);
-      if (ui < 0) continue;
       const TRunInfo &I = bars.info[ui % kTRuns];
+      if (I.kb == 0) break;
 
       // Value rows from the first drafted one on, key tile by key tile: past the last key
       // they may hold anything and are zeroed; before it, what is not finite is (see above).
@@ -618,7 +559,89 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       }
       __syncwarp();
     }
+  } else if (warp >= kTWarpPrep) {
+    regs_dec<kTRegsPrep>();
+    griddep_wait();
+    // ---------------- queries and masks, a run ahead (warps 12..15) ----------------
+    const int r = threadIdx.x & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    uint32_t *masks = reinterpret_cast<uint32_t *>(smem + T_OFF_MASK);
+    uint4 *stage = reinterpret_cast<uint4 *>(smem + T_OFF_STAGE + (4 + (warp & 3)) * kStageBytes);
+    for (int un = 0;; ++un) {
+      // into the buffers of the run's parity, which the run two before has left
+      if (!wait_all(&bars.run_full[un % kTRuns], (un / kTRuns) & 1) ||
+          (un >= 2 && !wait_all(&bars.o_free, (un - 2) & 1))) {
+        timed_out = true;
+        break;
+      }
+      const TRunInfo &I = bars.info[un % kTRuns];
+      if (I.kb != 0) {
+        const int par = un & 1;
+        // The queries: 64 bytes of 8 rows per load, all 32 rows of the warp (rows past the
+        // tree are zeros), turned so that a lane holds its row's on the way to tensor memory.
+        const T *q0 = static_cast<const T *>(p.q) + ((int64_t)I.row * p.num_q_heads + I.h * G) * kHeadDim;
+        const int live_rows = I.live_rows;
+        uint4 w[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // row 8 i + lane / 4 of the warp
+          const int row = (warp & 3) * 32 + 8 * i + (lane >> 2);
+          const uint4 *src = reinterpret_cast<const uint4 *>(
+                                 q0 + ((int64_t)(row / G) * p.num_q_heads + row % G) * kHeadDim) + (lane & 3);
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) w[4 * cc + i] = row < live_rows ? __ldg(src + 4 * cc) : make_uint4(0, 0, 0, 0);
+        }
+        if (r < live_rows / G && I.kb * 128 > I.start) {  // (a run that ends in front of the tree needs no mask)
+          uint32_t *mask = masks + (par * 128 + r) * kTMaskWords;
+#pragma unroll
+          for (int k = 0; k < kTMaskWords; ++k) mask[k] = 0;
+          const int32_t *parents = p.parents + (I.row - I.tok0);
+          int a = I.tok0 + r;
+          while (true) {
+            mask[a >> 5] |= 1u << (a & 31);
+            const int up = __ldg(parents + a);
+            if (up < 0 || up >= a) {
+              if (up != -1) set_error(p.err, PA_ERR_RANGE, I.s);  // (the walk ends: as one without parent)
+              break;
+            }
+            a = up;
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t v[16];
+#pragma unroll
+          for (int pass = 0; pass < 2; ++pass) {  // 16 rows at a time, the pieces swizzled against bank conflicts
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int row = 8 * i + (lane >> 2);
+              stage[row * 4 + ((lane & 3) ^ (row & 3))] = w[4 * cc + 2 * pass + i];
+            }
+            __syncwarp();
+            if ((lane >> 4) == pass) {
+              const int row = lane & 15;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint4 y = stage[row * 4 + (i ^ (row & 3))];
+                v[4 * i] = y.x;
+                v[4 * i + 1] = y.y;
+                v[4 * i + 2] = y.z;
+                v[4 * i + 3] = y.w;
+              }
+            }
+            __syncwarp();
+          }
+          tc::st_32x32b_x16(lane_base + kTColQ + par * 64 + cc * 16, v);
+        }
+        tc::wait_st();
+        tc::fence_before_sync();
+      }
+      const bool more = I.kb != 0;  // (read before the arrival)
+      mbar_arrive(&bars.q_full[un & 1]);
+      if (!more) break;
+    }
   } else if (warp != kTWarpMma) {
+    regs_dec<kTRegsLoad>();
     // ---------------- loader warps: 8 boxes of a key tile each, from parallel lanes ----------------
     // The first two: K, the 64-dim half (box & 1) of page box / 2; the third: V, a page per
     // box.  The block ids of 4 key tiles sit one per lane, the next 4 tiles' already on
@@ -632,26 +655,30 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     int c = 0;
     uint32_t issued = 0;  // per barrier (8 bits per kind, 2 per stage) bit 1: any copy, bit 0: the last one's parity
     bool waited = false;
-    for (int ui = 0; !timed_out; ++ui) {
-      const bool more = next_run(U, x, begun);
-      if (lw == 0 && lane == 0) {
-        TRunInfo &I = bars.info[ui % kTRuns];
-        const int tok0 = first_token(U);
-        I.ka = U.ka;
-        I.kb = more ? U.kb : 0;
-        I.start = U.len - U.n;
-        I.len = U.len;
-        I.row = U.row0 + tok0;
-        I.live_rows = min(TQ, U.n - tok0) * G;
-        I.h = U.h;
-        I.s = U.s;
+    TRun N = {};
+    bool more = true;
+    for (int ui = -1; !timed_out; ++ui) {  // (the first time round only the first run is published)
+      if (!more) break;
+      U = N;
+      more = next_run(N, x, begun);
+      if (lw == 0 && lane == 0) {  // run ui + 1
+        TRunInfo &I = bars.info[(ui + 1) % kTRuns];
+        const int tok0 = first_token(N);
+        I.ka = N.ka;
+        I.kb = more ? N.kb : 0;
+        I.start = N.len - N.n;
+        I.len = N.len;
+        I.row = N.row0 + tok0;
+        I.live_rows = min(TQ, N.n - tok0) * G;
+        I.h = N.h;
+        I.s = N.s;
         I.tok0 = tok0;
-        I.whole = U.whole();
-        I.first = x - (U.kb - U.ka) == x0;
-        mbar_arrive(&bars.run_full[ui % kTRuns]);
+        I.whole = N.whole();
+        I.first = x - (N.kb - N.ka) == x0;
+        mbar_arrive(&bars.run_full[(ui + 1) % kTRuns]);
       }
       __syncwarp();
-      if (!more) break;
+      if (ui < 0) continue;
       const int32_t *bt = p.block_tables + (int64_t)U.s * p.max_blocks_per_seq;
       const int npages = (U.len + kBlock - 1) / kBlock;
       const int tail = for_k ? INT_MAX : (U.len - U.n) >> 7;  // the first key tile that reaches the drafted keys
@@ -702,8 +729,10 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           if (used & 2) mbar_wait((for_k ? bars.k_full : bars.v_full[k]) + i, used & 1, kWaitLimitNs / 8);
         }
   } else {
+    regs_dec<kTRegsLoad>();
     // ---------------- MMA issuer (warp-uniform loop, one elected lane issues) ----------------
     griddep_wait();
+    griddep_launch_dependents();  // (the join waits for this grid; its blocks start as CTAs leave)
     if (lane == 0 && sub == 0) {  // the join's record of this worker (after the wait: the previous call's join may still read)
       JoinRecord rec = {};
       if (x0 < x1) {
@@ -817,8 +846,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 }
 
 // ---- the join ----
-// Block (worker, part): the group of the worker's record, a thread per row and 4 dims.
-constexpr int kTJoinThreads = 256, kTJoinPieces = 4;  // pieces in flight
+// Block (worker, part): the group of the worker's record, per thread and round 4
+// items of a row's 4 dims each, so that their pieces are in flight together.
+constexpr int kTJoinThreads = 256, kTJoinParts = 4, kTJoinItems = 4, kTJoinPieces = 2;
 template <typename T, int G, int NT>
 __global__ void __launch_bounds__(kTJoinThreads) attn_tree_join_kernel(const __grid_constant__ TreeParams p) {
   griddep_wait();
@@ -831,48 +861,59 @@ __global__ void __launch_bounds__(kTJoinThreads) attn_tree_join_kernel(const __g
     dst[1] = __ldcg(src + 1);
     dst[2] = __ldcg(src + 2);
   }
-  // lanes: G neighbouring rows x 32 / G dim quads, so that pieces are read in runs and outputs are written so
-  for (int i = (int)blockIdx.y * kTJoinThreads + (int)threadIdx.x; i < rec.rows * 32; i += gridDim.y * kTJoinThreads) {
-    const int row = (i / 32) / G * G + i % G, quad = (i / G) % 32;
-    const int cta = cta_of_tile<NT>(rec.rows > 128 ? 2 : 1, row >> 7, rec.h), tr = row & 127;
-    JoinState js;
-    constexpr int U = kTJoinPieces;
+  const int items = rec.rows * 32, stride = gridDim.y * kTJoinThreads;
+  for (int i0 = (int)blockIdx.y * kTJoinThreads + (int)threadIdx.x; i0 < items; i0 += kTJoinItems * stride) {
+    JoinState js[kTJoinItems];
+    // lanes: G neighbouring rows x 32 / G dim quads, so that pieces are read in runs and outputs are written so
+    auto row_of = [&](int i) { return (i / 32) / G * G + i % G; };
+    auto quad_of = [&](int i) { return (i / G) % 32; };
     for (int j = 0; j < rec.blocks; ++j) {
       const int k0 = part_start(j, rec.kt, rec.blocks), bl = part_start(j + 1, rec.kt, rec.blocks) - k0;
       const int xa = rec.pairs0 + rec.groups * k0 + rec.g * bl;  // the unit's first pair
       const int ff = part_owner(xa, rec.total, rec.workers), fl = part_owner(xa + bl - 1, rec.total, rec.workers);
       const int second = part_start(ff, rec.total, rec.workers) < xa ? 1 : 0;  // worker ff's piece is not its first run
-      for (int f0 = ff; f0 <= fl; f0 += U) {
-        float2 ml[U];
-        float4 o[U];
+      for (int f0 = ff; f0 <= fl; f0 += kTJoinPieces) {
+        float2 ml[kTJoinItems][kTJoinPieces];
+        float4 o[kTJoinItems][kTJoinPieces];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          ml[u] = make_float2(-INFINITY, 0.f);
-          o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (f0 + u <= fl) {
-            const int64_t slot = 2 * ((f0 + u) * NT + cta) + (f0 + u == ff ? second : 0);
-            ml[u] = __ldcg(p.ws_ml + slot * 128 + tr);
-            o[u] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o) + (slot * 32 + quad) * 128 + tr);
+        for (int n = 0; n < kTJoinItems; ++n) {
+          const int i = i0 + n * stride, row = row_of(i), tr = row & 127;
+          const int cta = cta_of_tile<NT>(rec.rows > 128 ? 2 : 1, row >> 7, rec.h);
+#pragma unroll
+          for (int u = 0; u < kTJoinPieces; ++u) {
+            ml[n][u] = make_float2(-INFINITY, 0.f);
+            o[n][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < items && f0 + u <= fl) {
+              const int64_t slot = 2 * ((f0 + u) * NT + cta) + (f0 + u == ff ? second : 0);
+              ml[n][u] = __ldcg(p.ws_ml + slot * 128 + tr);
+              o[n][u] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o) + (slot * 32 + quad_of(i)) * 128 + tr);
+            }
           }
         }
-        js.add(ml, o);
+#pragma unroll
+        for (int n = 0; n < kTJoinItems; ++n) js[n].add(ml[n], o[n]);
       }
     }
-    js.store(reinterpret_cast<T *>(p.out) +
-             ((int64_t)(rec.row0 + row / G) * p.num_q_heads + rec.h * G + row % G) * kHeadDim + 4 * quad);
+#pragma unroll
+    for (int n = 0; n < kTJoinItems; ++n) {
+      const int i = i0 + n * stride, row = row_of(i);
+      if (i < items)
+        js[n].store(static_cast<T *>(p.out) +
+                    ((int64_t)(rec.row0 + row / G) * p.num_q_heads + rec.h * G + row % G) * kHeadDim + 4 * quad_of(i));
+    }
   }
 }
 
 template <typename T, int G, int NT>
 cudaError_t launch_tree_typed(const TreeParams &p, const CUtensorMap *maps, int sms, cudaStream_t stream) {
   static KernelSetup setup;
-  const int smem = 1024 + T_OFF_PLAN + 2 * (p.num_seqs + 1) * 4;
+  const int smem = T_OFF_PLAN + 2 * (p.num_seqs + 1) * 4;
   cudaError_t e = kernel_setup(setup, attn_tree_kernel<T, G, NT>, smem, kTThreads, nullptr);
   if (e != cudaSuccess) return e;
   const int workers = sms / NT > 0 ? sms / NT : 1;
   e = launch_pdl(attn_tree_kernel<T, G, NT>, dim3(workers * NT), dim3(kTThreads), smem, stream, maps[0], maps[1], p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_tree_join_kernel<T, G, NT>, dim3(workers, 16 * NT), dim3(kTJoinThreads), 0, stream, p);
+  return launch_pdl(attn_tree_join_kernel<T, G, NT>, dim3(workers, kTJoinParts * NT), dim3(kTJoinThreads), 0, stream, p);
 }
 
 struct TreeLayout {
