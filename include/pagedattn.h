@@ -807,7 +807,7 @@ PA_API pa_status pa_kv_evict_ex(const pa_kv_pool *pool, const int32_t *block_tab
  * range is recorded likewise and taken as -1.  A block id outside the pool is reported
  * (detail: the sequence); the outputs that needed that page are undefined.  16-bit pools;
  * num_seqs at most PA_MAX_TREE_SEQS, num_tokens at most 2^20 - 2, num_kv_heads * (num_seqs +
- * num_tokens * num_q_heads / num_kv_heads / 128) * ceil(max_context_len / 128) below 2^31
+ * num_tokens * num_q_heads / num_kv_heads / 128) * (ceil(max_context_len / 128) + 2) below 2^31
  * (else PA_ERR_UNSUPPORTED).  tree_lens is read before the dependency wait, as
  * context_lens and block_tables are; parents after it.  Other arguments and errors as
  * pa_paged_attn_decode.

@@ -91,7 +91,7 @@ static_assert(T_OFF_PLAN + 2 * (kTreeMaxSeqs + 1) * 4 <= 232448, "shared memory"
 // the pairs pairs[s] .. pairs[s + 1] - 1 (none for a sequence that is refused).
 struct TreePlan {
   const int32_t *rows, *pairs, *context_lens;
-  int32_t num_seqs, num_kv_heads, total, workers, share;
+  int32_t num_seqs, num_kv_heads, total, workers, share, cost;
 };
 
 // Part j of W things over n, [j W / n, (j + 1) W / n), and the part that holds thing y.
@@ -100,19 +100,24 @@ __device__ __forceinline__ int part_owner(int y, int W, int n) {
   return (int)((((int64_t)y + 1) * n + W - 1) / W - 1);
 }
 
-// A run of pairs: key tiles ka .. kb - 1 of group g of (sequence s, KV head h), within
-// the unit of that group and key block j (key tiles k0 .. k1 - 1).
+// A run of pairs: tiles va .. vb - 1 of group g of (sequence s, KV head h), within the unit
+// of that group and key block j (tiles k0 .. k1 - 1).  A run costs more than its key
+// tiles (queries, masks, epilogue): in the deal a group counts for `cost` tiles more,
+// which come first and hold no keys; all of these numbers count them.
 struct TRun {
-  int s, h, g, j, ka, kb, k0, k1;
-  int kt, groups, blocks;  // the sequence's key tiles, groups, key blocks
+  int s, h, g, j, va, vb, k0, k1;
+  int kt, groups, blocks;  // the sequence's tiles, groups, key blocks
   int n, len, row0;        // its drafted tokens, keys, and first row
-  __device__ __forceinline__ bool whole() const { return kb - ka == kt; }
+  // its key tiles
+  __device__ __forceinline__ int ka(int cost) const { return max(va - cost, 0); }
+  __device__ __forceinline__ int kb(int cost) const { return max(vb - cost, 0); }
+  __device__ __forceinline__ bool whole(int cost) const { return blocks == 1 && va <= cost && vb == kt; }
   template <int TG>
   __device__ __forceinline__ void open_sequence(const TreePlan &pl) {
     row0 = pl.rows[s];
     n = pl.rows[s + 1] - row0;
     len = __ldg(pl.context_lens + s);
-    kt = (len + 127) / 128;
+    kt = (len + 127) / 128 + pl.cost;
     groups = (n + TG - 1) / TG;
     blocks = groups > 1 ? max(kt / pl.share, 1) : 1;
   }
@@ -137,8 +142,8 @@ struct TRun {
     open_block();
     r -= groups * k0;
     g = r / (k1 - k0);
-    ka = k0 + r - g * (k1 - k0);
-    kb = min(k1, ka + (x_end - x));
+    va = k0 + r - g * (k1 - k0);
+    vb = min(k1, va + (x_end - x));
   }
   // The next one, from pair x on (the last ended with its unit).
   template <int TG>
@@ -156,8 +161,8 @@ struct TRun {
       }
       open_block();
     }
-    ka = k0;
-    kb = min(k1, ka + (x_end - x));
+    va = k0;
+    vb = min(k1, va + (x_end - x));
   }
 };
 
@@ -277,7 +282,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const int n = __ldg(p.tree_lens + s), len = __ldg(p.context_lens + s);
     if (n == 0) return 0;  // nothing drafted: no rows
     if (n > 0 && n <= PA_MAX_TREE_LEN && rows[s + 1] <= p.num_tokens && len >= n && len <= p.max_len)
-      return p.num_kv_heads * ((n + TG - 1) / TG) * ((len + 127) / 128);
+      return p.num_kv_heads * ((n + TG - 1) / TG) * ((len + 127) / 128 + p.run_cost);
     if (scribe) set_error(p.err, PA_ERR_RANGE, s);
     return 0;
   });
@@ -291,6 +296,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   pl.context_lens = p.context_lens;
   pl.num_seqs = p.num_seqs;
   pl.num_kv_heads = p.num_kv_heads;
+  pl.cost = p.run_cost;
   pl.total = pairs[p.num_seqs];
   pl.workers = min(pl.total, (int)gridDim.x / NT);  // so that no share is empty
   pl.share = pl.workers > 0 ? (pl.total + pl.workers - 1) / pl.workers : 1;
@@ -307,8 +313,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     while (x < x1) {
       if (!begun) U.at<TG>(pl, x, x1); else U.next<TG>(pl, x, x1);
       begun = true;
-      x += U.kb - U.ka;
-      if (mine(U)) return true;
+      x += U.vb - U.va;
+      if (U.vb > pl.cost && mine(U)) return true;  // (else there are none of the group's keys in it)
     }
     return false;
   };
@@ -653,6 +659,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     uint8_t *dst0 = smem + (for_k ? T_OFF_K + (box & 1) * kHalf + page * 2048 : T_OFF_V + page * kVPage);
     const uint32_t bytes = for_k ? 2048u : (uint32_t)kVPage;
     int c = 0;
+    // Keys that one CTA alone reads leave L2 to what is read again (pieces, queries).
+    const uint64_t once = policy_evict_first(), often = policy_evict_last();
     uint32_t issued = 0;  // per barrier (8 bits per kind, 2 per stage) bit 1: any copy, bit 0: the last one's parity
     bool waited = false;
     TRun N = {};
@@ -664,8 +672,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (lw == 0 && lane == 0) {  // run ui + 1
         TRunInfo &I = bars.info[(ui + 1) % kTRuns];
         const int tok0 = first_token(N);
-        I.ka = N.ka;
-        I.kb = more ? N.kb : 0;
+        I.ka = N.ka(pl.cost);
+        I.kb = more ? N.kb(pl.cost) : 0;
         I.start = N.len - N.n;
         I.len = N.len;
         I.row = N.row0 + tok0;
@@ -673,8 +681,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         I.h = N.h;
         I.s = N.s;
         I.tok0 = tok0;
-        I.whole = N.whole();
-        I.first = x - (N.kb - N.ka) == x0;
+        I.whole = N.whole(pl.cost);
+        I.first = x - (N.vb - N.va) == x0;
         mbar_arrive(&bars.run_full[(ui + 1) % kTRuns]);
       }
       __syncwarp();
@@ -682,12 +690,14 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const int32_t *bt = p.block_tables + (int64_t)U.s * p.max_blocks_per_seq;
       const int npages = (U.len + kBlock - 1) / kBlock;
       const int tail = for_k ? INT_MAX : (U.len - U.n) >> 7;  // the first key tile that reaches the drafted keys
-      int wbase = U.ka * 8;
+      const int ka = U.ka(pl.cost), kb = U.kb(pl.cost);
+      const uint64_t policy = U.n > TQ ? often : once;
+      int wbase = ka * 8;
       auto ids_from = [&](int base) { return base + lane < npages ? __ldg(bt + base + lane) : -1; };
       int32_t win = ids_from(wbase), win_next = ids_from(wbase + 32);
       if (!waited) griddep_wait();  // K and V may come from the kernels before
       waited = true;
-      for (int t = U.ka; t < U.kb; ++t, ++c) {
+      for (int t = ka; t < kb; ++t, ++c) {
         if (t * 8 >= wbase + 32) {
           wbase += 32;
           win = win_next;
@@ -716,9 +726,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         issued = issued >> bit & 2 ? issued ^ 1u << bit : issued | 2u << bit;
         if (ok) {
           if (for_k)
-            tma_load_4d(dst, &kmap, full, (box & 1) * 64, U.h, 0, id);
+            tma_load_4d_hint(dst, &kmap, full, (box & 1) * 64, U.h, 0, id, policy);
           else
-            tma_load_5d(dst, &vmap, full, 0, 0, 0, U.h, id);
+            tma_load_5d_hint(dst, &vmap, full, 0, 0, 0, U.h, id, policy);
         }
       }
     }
@@ -739,8 +749,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         // The group of the last pair: joined here if its first unit began in this share and others go on with it.
         TRun Z = {};
         Z.at<TG>(pl, x1 - 1, x1);
-        const int unit = x1 - 1 - (Z.ka - Z.k0);  // its unit's first pair
-        if (unit >= x0 && Z.k0 == 0 && (Z.blocks > 1 || unit + Z.k1 - Z.k0 > x1)) {
+        const int unit = x1 - 1 - (Z.va - Z.k0), end = unit + Z.k1 - Z.k0;  // its unit's pairs
+        const bool cut = part_owner(unit + pl.cost, pl.total, pl.workers) != part_owner(end - 1, pl.total, pl.workers);
+        if (unit >= x0 && Z.k0 == 0 && (Z.blocks > 1 || cut)) {  // (its keys, that is)
           rec.rows = min(TG, Z.n - Z.g * TG) * G;
           rec.row0 = Z.row0 + Z.g * TG;
           rec.h = Z.h;
@@ -883,7 +894,8 @@ __global__ void __launch_bounds__(kTJoinThreads) attn_tree_join_kernel(const __g
           for (int u = 0; u < kTJoinPieces; ++u) {
             ml[n][u] = make_float2(-INFINITY, 0.f);
             o[n][u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < items && f0 + u <= fl) {
+            // (a worker with no more than the group's cost has no piece)
+            if (i < items && f0 + u <= fl && k0 + min(part_start(f0 + u + 1, rec.total, rec.workers), xa + bl) - xa > p.run_cost) {
               const int64_t slot = 2 * ((f0 + u) * NT + cta) + (f0 + u == ff ? second : 0);
               ml[n][u] = __ldcg(p.ws_ml + slot * 128 + tr);
               o[n][u] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o) + (slot * 32 + quad_of(i)) * 128 + tr);
@@ -905,12 +917,15 @@ __global__ void __launch_bounds__(kTJoinThreads) attn_tree_join_kernel(const __g
 }
 
 template <typename T, int G, int NT>
-cudaError_t launch_tree_typed(const TreeParams &p, const CUtensorMap *maps, int sms, cudaStream_t stream) {
+cudaError_t launch_tree_typed(TreeParams p, const CUtensorMap *maps, int sms, cudaStream_t stream) {
   static KernelSetup setup;
   const int smem = T_OFF_PLAN + 2 * (p.num_seqs + 1) * 4;
   cudaError_t e = kernel_setup(setup, attn_tree_kernel<T, G, NT>, smem, kTThreads, nullptr);
   if (e != cudaSuccess) return e;
   const int workers = sms / NT > 0 ? sms / NT : 1;
+  // (calls of a few key tiles per worker are not dealt but spread: there the cost would leave workers without keys)
+  const int64_t groups = (int64_t)p.num_kv_heads * (p.num_seqs + (int64_t)p.num_tokens * G / (128 * NT));
+  p.run_cost = groups * ((p.max_len + 127) / 128) > 4 * workers ? kTreeRunCost : 0;
   e = launch_pdl(attn_tree_kernel<T, G, NT>, dim3(workers * NT), dim3(kTThreads), smem, stream, maps[0], maps[1], p);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_tree_join_kernel<T, G, NT>, dim3(workers, kTJoinParts * NT), dim3(kTJoinThreads), 0, stream, p);

@@ -1082,7 +1082,7 @@ pa_status pa_paged_attn_tree(const void *q, const pa_kv_pool *pool, const int32_
   const int group = num_q_heads / pool->num_kv_heads;
   // the work is counted in 32 bits: (query tile, key tile) pairs
   const int64_t tiles = (int64_t)pool->num_kv_heads * (num_seqs + (int64_t)num_tokens * group / 128);
-  if (tiles * (((int64_t)max_context_len + 127) / 128) > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (tiles * (((int64_t)max_context_len + 127) / 128 + kTreeRunCost) > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if (!aligned4(tree_lens) || !aligned4(parents)) return PA_ERR_ALIGN;
   if (!workspace) return PA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PA_ERR_ALIGN;

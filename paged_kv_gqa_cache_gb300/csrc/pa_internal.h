@@ -288,6 +288,7 @@ cudaError_t launch_decode_shared(SharedParams sp, const PrefillParams &pp, Decod
                                  const CUtensorMap *maps, int dtype, int group, int sms, cudaStream_t stream);
 
 // ---- attention of drafted tokens that form a tree (16-bit pools) -----------------------
+constexpr int kTreeRunCost = 2;     // what a group of queries costs beside its key tiles, in key tiles
 constexpr int kTreeMaxSeqs = PA_MAX_TREE_SEQS;  // their prefixes in shared memory
 struct TreeParams {
   const void *q;                // [num_tokens][Hq][128]
@@ -307,6 +308,7 @@ struct TreeParams {
   int32_t num_kv_heads;
   int32_t num_q_heads;
   int32_t num_blocks;
+  int32_t run_cost;             // 0 or kTreeRunCost
   float scale_log2;
 };
 size_t tree_workspace_bytes(int sms);
