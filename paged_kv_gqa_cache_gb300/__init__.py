@@ -285,8 +285,10 @@ def _fresh(stream, make, *args):
 def _result(stream, make, *args):
     """``_fresh`` for a tensor that the caller gets: it is used on the current
     stream, so its memory must not go back before that is done either."""
+    if stream is None:
+        return make(*args)
     t = _fresh(stream, make, *args)
-    if stream is not None and t.is_cuda:
+    if t.is_cuda:
         current = torch.cuda.current_stream()
         if stream != current:
             t.record_stream(current)
@@ -1196,6 +1198,15 @@ def _layer_args(dev: int, pools: Optional[LayerPools], block_tables: Optional[to
     return pools.array, pools.count, block_tables.data_ptr(), block_tables.shape[1]
 
 
+def _accept_outputs(stream, S: int, stride: int, device):
+    empty, i32 = torch.empty, torch.int32
+    if stream is None:
+        return (empty((S, stride), dtype=i32, device=device), empty((S,), dtype=i32, device=device),
+                empty((S,), dtype=torch.int64, device=device), empty((S,), dtype=i32, device=device))
+    make = lambda *shape, dtype=i32: _result(stream, lambda: empty(shape, dtype=dtype, device=device))
+    return make(S, stride), make(S), make(S, dtype=torch.int64), make(S)
+
+
 def tree_accept(draft_tokens: torch.Tensor, target_tokens: torch.Tensor, parents: torch.Tensor,
                 tree_lens: torch.Tensor, context_lens: torch.Tensor, pools: Optional[LayerPools] = None,
                 block_tables: Optional[torch.Tensor] = None, max_tree_len: int = MAX_TREE_LEN, stream=None):
@@ -1210,18 +1221,16 @@ def tree_accept(draft_tokens: torch.Tensor, target_tokens: torch.Tensor, parents
     if not (_fine(dev, i64, draft_tokens, target_tokens) and _fine(dev, i32, parents, tree_lens, context_lens)):
         _check_all(dev, (draft_tokens, "draft_tokens", i64), (target_tokens, "target_tokens", i64),
                    (parents, "parents", i32), (tree_lens, "tree_lens", i32), (context_lens, "context_lens", i32))
-    if draft_tokens.dim() != 1 or tree_lens.dim() != 1:
+    tokens, seqs = draft_tokens.shape, tree_lens.shape
+    if len(tokens) != 1 or len(seqs) != 1:
         raise ValueError("draft_tokens must be [T], tree_lens [S]")
-    T, S = draft_tokens.shape[0], tree_lens.shape[0]
-    if target_tokens.shape != (T,) or parents.shape != (T,) or context_lens.shape != (S,):
-        raise ValueError(f"target_tokens and parents must be [{T}], context_lens [{S}]")
+    if target_tokens.shape != tokens or parents.shape != tokens or context_lens.shape != seqs:
+        raise ValueError(f"target_tokens and parents must be {list(tokens)}, context_lens {list(seqs)}")
     if max_tree_len < 1:
         raise ValueError("max_tree_len must be at least 1")
+    T, S = tokens[0], seqs[0]
     array, layers, tables, mb = _layer_args(dev, pools, block_tables, S)
-    path = _result(stream, lambda: torch.empty((S, max_tree_len), dtype=i32, device=tree_lens.device))
-    path_lens = _result(stream, torch.empty_like, tree_lens)
-    next_tokens = _result(stream, lambda: torch.empty((S,), dtype=i64, device=tree_lens.device))
-    new_lens = _result(stream, torch.empty_like, tree_lens)
+    path, path_lens, next_tokens, new_lens = _accept_outputs(stream, S, max_tree_len, tree_lens.device)
     _check((_lib or load_library()).pa_tree_accept(
         draft_tokens.data_ptr(), target_tokens.data_ptr(), parents.data_ptr(), T, tree_lens.data_ptr(),
         context_lens.data_ptr(), S, array, layers, tables, mb, path.data_ptr(), max_tree_len, path_lens.data_ptr(),
