@@ -8,8 +8,8 @@
 // The n x G query rows of a sequence for one KV head against its keys are a
 // matrix product: query tiles of 128 rows (128 / G tokens x the G heads), key
 // tiles of 128 keys, on the tcgen05 tensor cores.  NT query tiles (1 or 2) form a
-// group, taken by NT CTAs at the same time, a worker, so that one of them reads the
-// keys from HBM and the other from L2.  All (group, key tile) pairs of the call are
+// group, taken by a cluster of NT CTAs in step, a worker: each fetches half of every
+// key tile for both (TMA multicast), so that HBM and L2 are read once per group.  All (group, key tile) pairs of the call are
 // dealt evenly to the workers (one CTA per SM), so one long sequence or many short
 // ones fill the GPU alike.  A worker's share is a row of runs: consecutive key tiles
 // of one group.  A run that holds all keys of its group writes the outputs; a group cut
@@ -70,8 +70,8 @@ struct TRunInfo {
 struct TBars {
   uint64_t k_full[kTStages], k_free[kTStages];
   uint64_t v_full[2][kTStages];  // [1]: a key tile that reaches the drafted keys (looked at before it is used)
-  uint64_t v_free[kTStages];   // P V of the key tile added to O
-  uint64_t s_full[2], p_full[2];
+  uint64_t v_free[kTStages];   // (k_free, v_free: in every CTA of the worker)
+  uint64_t s_full[2], p_full[2], o_done;  // o_done: P V of a key tile added to O
   uint64_t q_full[2];          // per run: its queries and masks are in place
   uint64_t look[kTStages];     // per key tile that reaches the drafted keys: its values are fit for P V
   uint64_t x_full[2], run_done, o_free;  // per run: (m, l) written; every P V done; O read
@@ -174,11 +174,33 @@ struct JoinRecord {
 };
 static_assert(sizeof(JoinRecord) == 48, "three 16-byte loads");
 
-// The CTA of a worker that takes query tile t of a run of KV head h: with one tile
-// the heads take turns.
-template <int NT>
-__device__ __forceinline__ int cta_of_tile(int tiles, int t, int h) {
-  return NT == 1 ? 0 : tiles == 2 ? t : h & 1;
+// Multicast to both CTAs of a cluster, at the same addresses in each: 4-D and 5-D tiled
+// loads, completing on each one's `bar`, and the arrival when every MMA issued so far by
+// this thread completes.
+__device__ __forceinline__ void tma_load_4d_both(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1,
+                                                 int c2, int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7, %8;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)),
+      "h"((uint16_t)3), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_both(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1,
+                                                 int c2, int c3, int c4, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8, %9;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar)),
+      "h"((uint16_t)3), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void commit_both(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
 }
 
 // Whether one of the two 16-bit values of u is infinite or NaN.
@@ -248,11 +270,11 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
     for (int i = 0; i < kTStages; ++i) {
-      mbar_init(&bars.k_full[i], kTKLoad);
-      mbar_init(&bars.k_free[i], 1);
+      mbar_init(&bars.k_full[i], NT == 1 ? kTKLoad : 1);
+      mbar_init(&bars.k_free[i], NT);
       mbar_init(&bars.v_full[0][i], 1);
       mbar_init(&bars.v_full[1][i], 1);
-      mbar_init(&bars.v_free[i], 1);
+      mbar_init(&bars.v_free[i], NT);
       mbar_init(&bars.look[i], 128);
     }
     for (int i = 0; i < 2; ++i) {
@@ -265,6 +287,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     mbar_init(&bars.run_done, 1);
     mbar_init(&bars.o_free, 128);
     mbar_init(&bars.side, 128);
+    mbar_init(&bars.o_done, 1);
     mbar_init(&bars.drain, 1);
     for (int i = 0; i < kTMaskWords; ++i) bars.bad[0][i] = bars.bad[1][i] = 0;
     fence_mbar_init();
@@ -288,6 +311,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   });
   tc::fence_before_sync();
   __syncthreads();
+  if constexpr (NT == 2) cluster_sync();  // (the other CTA's barriers are initialised)
   tc::fence_after_sync();
   const uint32_t tmem = bars.tmem_base;
   TreePlan pl;
@@ -304,17 +328,16 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   bool timed_out = false;
   // (the outcome of a wait is made warp-uniform: what follows is warp-wide)
   auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, mbar_wait(bar, parity)) != 0; };
-  // query tiles of a run (its group may be the last and not full), and whether this CTA has one of them
-  auto tiles_of = [&](const TRun &U) { return NT == 2 && U.n - U.g * TG > TQ ? 2 : 1; };
-  auto mine = [&](const TRun &U) { return NT == 1 || tiles_of(U) == 2 || cta_of_tile<NT>(1, 0, U.h) == sub; };
-  auto first_token = [&](const TRun &U) { return U.g * TG + (NT == 2 && tiles_of(U) == 2 ? sub * TQ : 0); };
-  // The CTA's next run from pair x on (x0: the first), x behind it; false: no more.
+  // the first token of this CTA's query tile (a group may be the last and not full: then the
+  // second tile has fewer rows or none, and its CTA only keeps step)
+  auto first_token = [&](const TRun &U) { return U.g * TG + sub * TQ; };
+  // The worker's next run from pair x on (x0: the first), x behind it; false: no more.
   auto next_run = [&](TRun &U, int &x, bool &begun) {
     while (x < x1) {
       if (!begun) U.at<TG>(pl, x, x1); else U.next<TG>(pl, x, x1);
       begun = true;
       x += U.vb - U.va;
-      if (U.vb > pl.cost && mine(U)) return true;  // (else there are none of the group's keys in it)
+      if (U.vb > pl.cost) return true;  // (else there are none of the group's keys in it)
     }
     return false;
   };
@@ -387,7 +410,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
               l *= f;
               m_ref = m_new;
             }
-            if (!wait_all(&bars.v_free[(c - 1) % kTStages], ((c - 1) / kTStages) & 1)) {
+            if (!wait_all(&bars.o_done, (c - 1) & 1)) {
               timed_out = true;
               break;
             }
@@ -654,17 +677,20 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     // their way: a table read per tile would hold up every copy by an L2 trip.
     const int lw = warp - kTWarpLoad0;
     const bool for_k = lw < kTKLoad;
-    const int box = for_k ? lw + kTKLoad * lane : lane, boxes = for_k ? 16 : 8, page = for_k ? box >> 1 : box;
+    // (With two CTAs the first K warp has all 16 boxes and issues every second one for both, and
+    // so does the V warp with its 8; what cannot be read each CTA zeroes for itself.)
+    const int box = for_k && NT == 1 ? lw + kTKLoad * lane : lane, boxes = for_k ? 16 : 8, page = for_k ? box >> 1 : box;
+    const bool issues = NT == 1 || (box & 1) == sub;
     uint64_t *free = for_k ? bars.k_free : bars.v_free;
     uint8_t *dst0 = smem + (for_k ? T_OFF_K + (box & 1) * kHalf + page * 2048 : T_OFF_V + page * kVPage);
     const uint32_t bytes = for_k ? 2048u : (uint32_t)kVPage;
     int c = 0;
-    // Keys that one CTA alone reads leave L2 to what is read again (pieces, queries).
+    // Keys that one worker alone reads leave L2 to what is read again (pieces, queries).
     const uint64_t once = policy_evict_first(), often = policy_evict_last();
     uint32_t issued = 0;  // per barrier (8 bits per kind, 2 per stage) bit 1: any copy, bit 0: the last one's parity
     bool waited = false;
     TRun N = {};
-    bool more = true;
+    bool more = NT == 1 || lw != 1;
     for (int ui = -1; !timed_out; ++ui) {  // (the first time round only the first run is published)
       if (!more) break;
       U = N;
@@ -677,7 +703,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         I.start = N.len - N.n;
         I.len = N.len;
         I.row = N.row0 + tok0;
-        I.live_rows = min(TQ, N.n - tok0) * G;
+        I.live_rows = max(min(TQ, N.n - tok0), 0) * G;
         I.h = N.h;
         I.s = N.s;
         I.tok0 = tok0;
@@ -691,7 +717,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const int npages = (U.len + kBlock - 1) / kBlock;
       const int tail = for_k ? INT_MAX : (U.len - U.n) >> 7;  // the first key tile that reaches the drafted keys
       const int ka = U.ka(pl.cost), kb = U.kb(pl.cost);
-      const uint64_t policy = U.n > TQ ? often : once;
+      const uint64_t policy = U.groups > 1 ? often : once;
       int wbase = ka * 8;
       auto ids_from = [&](int base) { return base + lane < npages ? __ldg(bt + base + lane) : -1; };
       int32_t win = ids_from(wbase), win_next = ids_from(wbase + 32);
@@ -724,8 +750,13 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         __syncwarp();
         const int bit = 2 * st + (t >= tail ? 8 : 0);
         issued = issued >> bit & 2 ? issued ^ 1u << bit : issued | 2u << bit;
-        if (ok) {
-          if (for_k)
+        if (ok && issues) {
+          if constexpr (NT == 2) {
+            if (for_k)
+              tma_load_4d_both(dst, &kmap, full, (box & 1) * 64, U.h, 0, id, policy);
+            else
+              tma_load_5d_both(dst, &vmap, full, 0, 0, 0, U.h, id, policy);
+          } else if (for_k)
             tma_load_4d_hint(dst, &kmap, full, (box & 1) * 64, U.h, 0, id, policy);
           else
             tma_load_5d_hint(dst, &vmap, full, 0, 0, 0, U.h, id, policy);
@@ -797,7 +828,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           tc::mma_f16_ts(tmem + kTColO, a_hi, bdesc, IDESC_O, kk > 0 || !p_first ? 1u : 0u);
           tc::mma_f16_ts(tmem + kTColO, a_hi + 16, bdesc, IDESC_O, 1u);
         }
-        tc::commit(&bars.v_free[st]);
+        tc::commit(&bars.o_done);
+        if constexpr (NT == 2) commit_both(&bars.v_free[st]); else tc::commit(&bars.v_free[st]);
         if (p_last) tc::commit(&bars.run_done);
       }
       __syncwarp();
@@ -826,7 +858,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             tc::mma_f16_ts(tmem + (c & 1) * 128, tmem + kTColQ + (ui & 1) * 64 + 8 * kk,
                            kdesc + (uint64_t)((kk >> 2) * kHalfStep + (kk & 3) * 2), IDESC_S, kk > 0 ? 1u : 0u);
           tc::commit(&bars.s_full[c & 1]);
-          tc::commit(&bars.k_free[st]);
+          if constexpr (NT == 2) commit_both(&bars.k_free[st]); else tc::commit(&bars.k_free[st]);
         }
         __syncwarp();
         if (pc >= 0 && !issue_pv()) {
@@ -850,6 +882,10 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   if (timed_out) set_error(p.err, PA_ERR_TIMEOUT, (int)blockIdx.x);
   tc::fence_before_sync();
   __syncthreads();
+  if constexpr (NT == 2) {  // (this CTA's copies and arrivals in the other's memory are over)
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == kTWarpMma) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
@@ -889,7 +925,7 @@ __global__ void __launch_bounds__(kTJoinThreads) attn_tree_join_kernel(const __g
 #pragma unroll
         for (int n = 0; n < kTJoinItems; ++n) {
           const int i = i0 + n * stride, row = row_of(i), tr = row & 127;
-          const int cta = cta_of_tile<NT>(rec.rows > 128 ? 2 : 1, row >> 7, rec.h);
+          const int cta = row >> 7;
 #pragma unroll
           for (int u = 0; u < kTJoinPieces; ++u) {
             ml[n][u] = make_float2(-INFINITY, 0.f);
@@ -922,11 +958,40 @@ cudaError_t launch_tree_typed(TreeParams p, const CUtensorMap *maps, int sms, cu
   const int smem = T_OFF_PLAN + 2 * (p.num_seqs + 1) * 4;
   cudaError_t e = kernel_setup(setup, attn_tree_kernel<T, G, NT>, smem, kTThreads, nullptr);
   if (e != cudaSuccess) return e;
-  const int workers = sms / NT > 0 ? sms / NT : 1;
+  int workers = sms;
+  if (NT == 2) {  // as many clusters as run at the same time
+    static std::mutex mutex;
+    static unsigned long long ctx = 0;
+    static int clusters = 0;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (ctx != launch_context_id()) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(sms / NT * NT);
+      cfg.blockDim = dim3(kTThreads);
+      cfg.dynamicSmemBytes = T_OFF_PLAN + 2 * (kTreeMaxSeqs + 1) * 4;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = NT;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      e = cudaFuncSetAttribute(attn_tree_kernel<T, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)cfg.dynamicSmemBytes);
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, attn_tree_kernel<T, G, NT>, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < 1) return cudaErrorInvalidConfiguration;
+      clusters = n < sms / NT ? n : sms / NT;
+      ctx = launch_context_id();
+    }
+    workers = clusters;
+  }
   // (calls of a few key tiles per worker are not dealt but spread: there the cost would leave workers without keys)
   const int64_t groups = (int64_t)p.num_kv_heads * (p.num_seqs + (int64_t)p.num_tokens * G / (128 * NT));
   p.run_cost = groups * ((p.max_len + 127) / 128) > 4 * workers ? kTreeRunCost : 0;
-  e = launch_pdl(attn_tree_kernel<T, G, NT>, dim3(workers * NT), dim3(kTThreads), smem, stream, maps[0], maps[1], p);
+  e = NT == 2 ? launch_pdl_cluster(attn_tree_kernel<T, G, NT>, dim3(workers * NT), dim3(kTThreads), smem, NT, stream,
+                                   maps[0], maps[1], p)
+              : launch_pdl(attn_tree_kernel<T, G, NT>, dim3(workers), dim3(kTThreads), smem, stream, maps[0], maps[1], p);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_tree_join_kernel<T, G, NT>, dim3(workers, kTJoinParts * NT), dim3(kTJoinThreads), 0, stream, p);
 }
