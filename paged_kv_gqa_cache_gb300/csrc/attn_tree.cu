@@ -345,6 +345,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   int x = x0;
   bool begun = false;
 
+  // (one instruction for the loader and MMA warps: setmaxnreg acts on whole warpgroups)
+  if (warp >= kTWarpLoad0 && warp < kTWarpPrep) regs_dec<kTRegsLoad>();
   if (warp < kTWarpEpi) {
     regs_inc<kTRegsSoftmax>();
     griddep_wait();
@@ -670,7 +672,6 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (!more) break;
     }
   } else if (warp != kTWarpMma) {
-    regs_dec<kTRegsLoad>();
     // ---------------- loader warps: 8 boxes of a key tile each, from parallel lanes ----------------
     // The first two: K, the 64-dim half (box & 1) of page box / 2; the third: V, a page per
     // box.  The block ids of 4 key tiles sit one per lane, the next 4 tiles' already on
@@ -770,7 +771,6 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           if (used & 2) mbar_wait((for_k ? bars.k_full : bars.v_full[k]) + i, used & 1, kWaitLimitNs / 8);
         }
   } else {
-    regs_dec<kTRegsLoad>();
     // ---------------- MMA issuer (warp-uniform loop, one elected lane issues) ----------------
     griddep_wait();
     griddep_launch_dependents();  // (the join waits for this grid; its blocks start as CTAs leave)

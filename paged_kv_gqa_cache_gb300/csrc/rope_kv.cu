@@ -61,7 +61,7 @@ __device__ __forceinline__ long long turns_fixed(double inv_freq) {
 __device__ __forceinline__ float2 twice(float a) { return make_float2(a, a); }
 
 // TOK tokens per CTA and step, 8 / TOK warps each.
-template <typename T, int MODE, bool NORM, int TOK>
+template <typename T, int MODE, bool NORM, int TOK, bool AXES>
 __global__ void __launch_bounds__(kRopeKvThreads, 3) rope_kv_kernel(const RopeKvParams p) {
   constexpr int kWarps = kRopeKvThreads / 32 / TOK;  // warps per token
   constexpr int kStep = 2 * kWarps;                  // rows per pass of them
@@ -80,10 +80,10 @@ __global__ void __launch_bounds__(kRopeKvThreads, 3) rope_kv_kernel(const RopeKv
   const int r_qk = w_qk + (lane >> 4), r_v = w_v + (lane >> 4);
   griddep_wait();  // q, k, v may be the previous kernel's output; the pool may be read by it
   long long turns = 0;
-  const int32_t *positions = p.positions;  // of this thread's pair
+  int64_t axis = 0;  // where the positions of this thread's pair begin
   if (tid < TOK * 64 && (tid & 63) < d / 2) {
     turns = turns_fixed(__ldg(p.inv_freq + (tid & 63)));
-    positions += (int64_t)p.pair_axis[tid & 63] * p.num_tokens;
+    if (AXES) axis = (int64_t)p.pair_axis[tid & 63] * p.num_tokens;
   }
   auto read = [&](const T *src, uint2 (&x)[2]) {
     if constexpr (MODE == kHalfPairs) {
@@ -111,8 +111,11 @@ __global__ void __launch_bounds__(kRopeKvThreads, 3) rope_kv_kernel(const RopeKv
   for (int t0 = blockIdx.x * TOK; t0 < p.num_tokens; t0 += gridDim.x * TOK) {  // (block-uniform)
     const int t = t0 + tok;
     int pos = t < p.num_tokens ? __ldg(p.positions + t) : -1;
-    if (t < p.num_tokens)
-      for (int a = 1; a < p.num_axes; ++a) pos |= __ldg(p.positions + (int64_t)a * p.num_tokens + t);  // (the signs)
+    if (AXES && t < p.num_tokens) {
+#pragma unroll
+      for (int a = 1; a < PA_ROPE_MAX_AXES; ++a)  // (their signs; all loads on their way together)
+        pos |= a < p.num_axes ? __ldg(p.positions + (int64_t)a * p.num_tokens + t) : 0;
+    }
     const int64_t slot = t < p.num_tokens ? __ldg(p.slots + t) : -1;
     const bool ok = pos >= 0 && slot >= 0 && slot < p.num_slots;  // else nothing of the token is written
     if (!ok && t < p.num_tokens && tid % (32 * kWarps) == 0) set_error(p.err, PA_ERR_RANGE, t);
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(kRopeKvThreads, 3) rope_kv_kernel(const RopeKv
     // the step's angles, meanwhile
     if (tid < TOK * 64 && (tid & 63) < d / 2) {
       const int at = t0 + (tid >> 6);
-      const int pa = at < p.num_tokens ? __ldg(positions + at) : 0;
+      const int pa = at < p.num_tokens ? __ldg(p.positions + axis + at) : 0;
       const long long turn = (long long)((unsigned long long)turns * (unsigned long long)(unsigned)pa);
       float s, c;
       sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
@@ -233,12 +236,12 @@ __global__ void __launch_bounds__(kRopeKvThreads, 3) rope_kv_kernel(const RopeKv
   griddep_launch_dependents();
 }
 
-template <typename T, int TOK>
+template <typename T, int TOK, bool AXES>
 cudaError_t launch_rope_kv_typed(const RopeKvParams &p, int grid, cudaStream_t stream) {
   const int mode = p.interleaved ? kInterleaved : p.rotary_dim % 8 == 0 ? kHalfPairs : kHalfExchange;
 #define PA_ROPE_CASE(M, N) \
   if (mode == M && (p.q_weight != nullptr) == N) \
-    return launch_pdl(rope_kv_kernel<T, M, N, TOK>, dim3(grid), dim3(kRopeKvThreads), 0, stream, p);
+    return launch_pdl(rope_kv_kernel<T, M, N, TOK, AXES>, dim3(grid), dim3(kRopeKvThreads), 0, stream, p);
   PA_ROPE_CASE(kInterleaved, false)
   PA_ROPE_CASE(kInterleaved, true)
   PA_ROPE_CASE(kHalfPairs, false)
@@ -249,17 +252,23 @@ cudaError_t launch_rope_kv_typed(const RopeKvParams &p, int grid, cudaStream_t s
   return cudaErrorInvalidValue;
 }
 
+template <bool AXES>
+cudaError_t launch_rope_kv_axes(const RopeKvParams &p, int dtype, int sms, cudaStream_t stream) {
+  const int cap = sms * 3;  // one wave: 3 CTAs fit on an SM
+  if (p.num_tokens <= cap) {  // a token per CTA
+    return dtype == PA_BF16 ? launch_rope_kv_typed<__nv_bfloat16, 1, AXES>(p, p.num_tokens, stream)
+                            : launch_rope_kv_typed<__half, 1, AXES>(p, p.num_tokens, stream);
+  }
+  const int want = (p.num_tokens + 3) / 4, grid = want < cap ? want : cap;
+  return dtype == PA_BF16 ? launch_rope_kv_typed<__nv_bfloat16, 4, AXES>(p, grid, stream)
+                          : launch_rope_kv_typed<__half, 4, AXES>(p, grid, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_rope_kv(const RopeKvParams &p, int dtype, int sms, cudaStream_t stream) {
-  const int cap = sms * 3;  // one wave: 3 CTAs fit on an SM
-  if (p.num_tokens <= cap) {  // a token per CTA
-    return dtype == PA_BF16 ? launch_rope_kv_typed<__nv_bfloat16, 1>(p, p.num_tokens, stream)
-                            : launch_rope_kv_typed<__half, 1>(p, p.num_tokens, stream);
-  }
-  const int want = (p.num_tokens + 3) / 4, grid = want < cap ? want : cap;
-  return dtype == PA_BF16 ? launch_rope_kv_typed<__nv_bfloat16, 4>(p, grid, stream)
-                          : launch_rope_kv_typed<__half, 4>(p, grid, stream);
+  return p.num_axes > 1 ? launch_rope_kv_axes<true>(p, dtype, sms, stream)
+                        : launch_rope_kv_axes<false>(p, dtype, sms, stream);
 }
 
 }  // namespace pa
