@@ -806,7 +806,8 @@ PA_API pa_status pa_kv_evict_ex(const pa_kv_pool *pool, const int32_t *block_tab
  * PA_ERR_RANGE (detail: the sequence) and its rows are left as they are.  A parent out of
  * range is recorded likewise and taken as -1.  A block id outside the pool is reported
  * (detail: the sequence); the outputs that needed that page are undefined.  16-bit pools;
- * num_seqs at most PA_MAX_TREE_SEQS, num_tokens at most 2^20 - 2, num_kv_heads * (num_seqs +
+ * num_seqs at most PA_MAX_TREE_SEQS, num_tokens at most 2^20 - 2, max_context_len at most 2^30,
+ * num_kv_heads * (num_seqs +
  * num_tokens * num_q_heads / num_kv_heads / 128) * (ceil(max_context_len / 128) + 2) below 2^31
  * (else PA_ERR_UNSUPPORTED).  tree_lens is read before the dependency wait, as
  * context_lens and block_tables are; parents after it.  Other arguments and errors as
@@ -836,7 +837,8 @@ PA_API pa_status pa_paged_attn_tree(const void *q, const pa_kv_pool *pool, const
  *                 moved (pools and block_tables are not read).
  *   path          int32 [num_seqs][path_stride], path_stride >= 1.
  *   path_lens     int32 [num_seqs]; next_tokens int64 [num_seqs]; new_context_lens int32
- *                 [num_seqs], apart from context_lens (PA_ERR_SHAPE).
+ *                 [num_seqs].  The four outputs lie apart from one another and from the
+ *                 inputs (else PA_ERR_SHAPE), the pools apart from one another.
  * The blocks of the drafted tokens must be the sequence's own (as reserved ones are).  With
  * the allocator, then: pa_sequence_commit of the drafted tokens and pa_sequence_truncate
  * to the new length.  A tree length outside [0, min(path_stride, PA_MAX_TREE_LEN)], a

@@ -1175,6 +1175,9 @@ class LayerPools:
         if len(devices) > 1:
             raise ValueError("the layers' pools must be on one device")
         self.device = devices.pop() if devices else None
+        ends = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for pair in self.tensors for t in pair)
+        if any(a[1] > b[0] for a, b in zip(ends, ends[1:])):
+            raise ValueError("the layers' pools must not overlap: each row is moved once")
 
 
 def layer_pools(pools) -> LayerPools:

@@ -1078,7 +1078,8 @@ pa_status pa_paged_attn_tree(const void *q, const pa_kv_pool *pool, const int32_
   if (num_seqs < 0) return PA_ERR_SHAPE;
   if (num_seqs == 0 || num_tokens == 0) return PA_OK;
   if (!tree_lens || !parents) return PA_ERR_NULL;
-  if (num_seqs > kTreeMaxSeqs || num_tokens > (1 << 20) - 2) return PA_ERR_UNSUPPORTED;
+  // (a length beyond 2^30 would not leave the key tiles' positions room in 32 bits)
+  if (num_seqs > kTreeMaxSeqs || num_tokens > (1 << 20) - 2 || max_context_len > (1 << 30)) return PA_ERR_UNSUPPORTED;
   const int group = num_q_heads / pool->num_kv_heads;
   // the work is counted in 32 bits: (query tile, key tile) pairs
   const int64_t tiles = (int64_t)pool->num_kv_heads * (num_seqs + (int64_t)num_tokens * group / 128);
@@ -1137,8 +1138,29 @@ pa_status tree_move_call(TreeAcceptParams &p, const int32_t *tree_lens, const in
   if (!aligned4(p.path) || !aligned4(p.path_lens) || !aligned4(tree_lens) || !aligned4(context_lens) ||
       !aligned4(block_tables) || !aligned4(new_context_lens))
     return PA_ERR_ALIGN;
-  const size_t lens_bytes = (size_t)num_seqs * sizeof(int32_t);
-  if (overlap(context_lens, lens_bytes, new_context_lens, lens_bytes)) return PA_ERR_SHAPE;
+  // every CTA of a sequence reads the inputs, and one writes the outputs meanwhile
+  struct Range {
+    const void *at;
+    size_t bytes;
+    bool out;
+  };
+  const size_t lens_bytes = (size_t)num_seqs * sizeof(int32_t), tokens = (size_t)p.num_tokens;
+  const bool greedy = p.next_tokens != nullptr;  // (else the paths are inputs, and there are no tokens)
+  const Range ranges[] = {{new_context_lens, lens_bytes, true},
+                          {p.path, lens_bytes * p.path_stride, greedy},
+                          {p.path_lens, lens_bytes, greedy},
+                          {p.next_tokens, greedy ? 2 * lens_bytes : 0, true},
+                          {tree_lens, lens_bytes, false},
+                          {context_lens, lens_bytes, false},
+                          {block_tables, num_layers > 0 ? lens_bytes * max_blocks_per_seq : 0, false},
+                          {p.draft, tokens * sizeof(int64_t), false},
+                          {p.target, tokens * sizeof(int64_t), false},
+                          {p.parents, tokens * sizeof(int32_t), false}};
+  constexpr int kRanges = sizeof(ranges) / sizeof(ranges[0]);
+  for (int a = 0; a < 4; ++a)
+    for (int b = a + 1; b < kRanges; ++b)
+      if ((ranges[a].out || ranges[b].out) && overlap(ranges[a].at, ranges[a].bytes, ranges[b].at, ranges[b].bytes))
+        return PA_ERR_SHAPE;
   DeviceState *d = nullptr;
   pa_status st = device_state(&d);
   if (st != PA_OK) return st;

@@ -34,6 +34,7 @@ def _pool(**kw):
     (dict(scale=float("nan")), "PA_ERR_SHAPE"), (dict(pool=_pool(dtype=9)), "PA_ERR_DTYPE"),
     (dict(pool=_pool(block_size=32)), "PA_ERR_UNSUPPORTED"), (dict(pool=None), "PA_ERR_NULL"),
     (dict(mb=1 << 26, mcl=1 << 30, S=40, T=100), "PA_ERR_UNSUPPORTED"),
+    (dict(mb=(1 << 26) + 1, mcl=(1 << 30) + 1, S=1, T=1), "PA_ERR_UNSUPPORTED"),
 ])
 def test_attn_tree_refusals(lib, kw, status):
     pool = kw.get("pool", _pool())
@@ -90,6 +91,28 @@ def test_accept_and_move_refusals(lib, kw, status, move):
 ])
 def test_accept_refusals(lib, kw, status):
     assert pa.STATUS[_accept(lib, kw, False)] == status
+
+
+def _apart(**kw):
+    """Addresses that no two arrays of a call share, but for those given."""
+    names = ["draft", "target", "parents", "n", "lens", "bt", "path", "plens", "next", "new"]
+    d = {name: P + (i << 16) for i, name in enumerate(names)}
+    d.update({a: d[b] + off for a, (b, off) in kw.items()})
+    return d
+
+
+@pytest.mark.parametrize("out,of,off", [  # 4 sequences, 20 tokens, paths of 8, tables of 16 blocks
+    *[(out, of, 0) for out in ("path", "plens", "next", "new")
+      for of in ("draft", "target", "parents", "n", "lens", "bt", "path", "plens", "next", "new") if of != out],
+    ("new", "n", 12), ("new", "path", 124), ("path", "parents", 76), ("next", "target", 152), ("plens", "bt", 252),
+])
+def test_accept_outputs_apart(lib, out, of, off):
+    assert pa.STATUS[_accept(lib, _apart(**{out: (of, off)}), False)] == "PA_ERR_SHAPE"
+
+
+@pytest.mark.parametrize("of,off", [("n", 0), ("lens", 12), ("bt", 252), ("path", 124), ("plens", 12)])
+def test_move_output_apart(lib, of, off):
+    assert pa.STATUS[_accept(lib, _apart(new=(of, off)), True)] == "PA_ERR_SHAPE"
 
 
 def _rope(**kw):
