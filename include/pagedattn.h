@@ -806,12 +806,11 @@ PA_API pa_status pa_kv_evict_ex(const pa_kv_pool *pool, const int32_t *block_tab
  * PA_ERR_RANGE (detail: the sequence) and its rows are left as they are.  A parent out of
  * range is recorded likewise and taken as -1.  A block id outside the pool is reported
  * (detail: the sequence); the outputs that needed that page are undefined.  16-bit pools;
- * num_seqs at most PA_MAX_TREE_SEQS, num_tokens at most 2^20 - 2, max_context_len at most 2^30,
- * num_kv_heads * (num_seqs +
- * num_tokens * num_q_heads / num_kv_heads / 128) * (ceil(max_context_len / 128) + 2) below 2^31
- * (else PA_ERR_UNSUPPORTED).  tree_lens is read before the dependency wait, as
- * context_lens and block_tables are; parents after it.  Other arguments and errors as
- * pa_paged_attn_decode.
+ * num_seqs at most PA_MAX_TREE_SEQS, num_tokens at most 2^20 - 2, max_context_len at most
+ * 2^30, num_kv_heads * (num_seqs + num_tokens * num_q_heads / num_kv_heads / 128) *
+ * (ceil(max_context_len / 128) + 2) below 2^31 (else PA_ERR_UNSUPPORTED).  tree_lens is
+ * read before the dependency wait, as context_lens and block_tables are; parents after
+ * it.  Other arguments and errors as pa_paged_attn_decode.
  */
 PA_API size_t pa_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads);
 PA_API pa_status pa_paged_attn_tree(const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
@@ -858,7 +857,8 @@ PA_API pa_status pa_tree_accept(const int64_t *draft_tokens, const int64_t *targ
  * tree_move — the cache compacted to paths found by other means (sampled
  * verification): the moves and new lengths of pa_tree_accept for the given path
  * and path_lens, which are read only (path_stride bounds the paths, not the trees).  A
- * path that is longer than its tree, not ascending or out of range records PA_ERR_RANGE (detail: the sequence) as above.
+ * path that is longer than its tree, not ascending or out of range records PA_ERR_RANGE
+ * (detail: the sequence) as above.
  */
 PA_API pa_status pa_tree_move(const int32_t *path, int32_t path_stride, const int32_t *path_lens,
                               const int32_t *tree_lens, const int32_t *context_lens, int32_t num_seqs,

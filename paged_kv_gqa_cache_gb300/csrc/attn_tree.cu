@@ -8,29 +8,47 @@
 // The n x G query rows of a sequence for one KV head against its keys are a
 // matrix product: query tiles of 128 rows (128 / G tokens x the G heads), key
 // tiles of 128 keys, on the tcgen05 tensor cores.  NT query tiles (1 or 2) form a
-// group, taken by a cluster of NT CTAs in step, a worker: each fetches half of every
-// key tile for both (TMA multicast), so that HBM and L2 are read once per group.  All (group, key tile) pairs of the call are
-// dealt evenly to the workers (one CTA per SM), so one long sequence or many short
-// ones fill the GPU alike.  A worker's share is a row of runs: consecutive key tiles
-// of one group.  A run that holds all keys of its group writes the outputs; a group cut
-// between workers leaves a piece (m, l, o) per CTA, joined by a second kernel.  Only a
-// worker's first and last run can be such pieces, so 2 slots per CTA hold them whatever
-// the batch.  With several groups to a sequence the key range is cut into blocks at
-// least as long as a share, the groups of a block next to each other in the order, so
-// that the workers that need the same keys run at the same time.
+// group, taken by a cluster of NT CTAs in step, a worker: each fetches half of
+// every key tile for both (TMA multicast), so that HBM and L2 are read once per
+// group.  All (group, key tile) pairs of the call are dealt evenly to the workers
+// (one CTA per SM), so one long sequence or many short ones fill the GPU alike.  A
+// worker's share is a row of runs: consecutive key tiles of one group.  A run that
+// holds all keys of its group writes the outputs; a group cut between workers
+// leaves a piece (m, l, o) per CTA, joined by a second kernel.  Only a worker's
+// first and last run can be such pieces, so 2 slots per CTA hold them whatever the
+// batch.  With several groups to a sequence the key range is cut into blocks at
+// least as long as a share, the groups of a block next to each other in the order,
+// so that the workers that need the same keys run at the same time.
 //
-// A pair is 64 KB of K and V, 1.47 us of an SM's share of HBM, beside 0.78 us of tensor
-// time (P in two terms).  To keep the copies running across a change of runs the
-// queries do not lie in shared memory but as the A operand in tensor memory, two tiles
-// of them, fetched a run ahead: all of shared memory is K and V.  One warpgroup
-// computes P; another prepares the next run's queries and masks, looks at the drafted
-// values and writes the outputs, while the next run is under way.
+// A pair is 64 KB of K and V, 1.47 us of an SM's share of HBM, beside 0.78 us of
+// tensor time (P in two terms).  To keep the copies running across a change of
+// runs the queries do not lie in shared memory but as the A operand in tensor
+// memory, two tiles of them, fetched a run ahead: the rings of K and V have three
+// key tiles each.  One warpgroup computes P, one prepares the next run's queries
+// and masks, one looks at the drafted values and writes the outputs, while the next
+// run is under way.  What a change of runs must not do: touch local memory (beside
+// 227 KB of shared memory the L1 is small; spills of 250 bytes cost 5 us a change),
+// read rows 16 bytes a lane (the queries: 124 against 101 us for 32 sequences of up
+// to 8192), or signal behind stores (an arrival waits until they are in L2).
 //
-// The mask: per token a bit for each drafted token that it sees, found by a walk up the
-// tree a run ahead; 128 bits of it per key tile that reaches the drafted keys.  A row
-// always sees itself.  A drafted value that is infinite or NaN must not reach the rows
-// that do not see it (0 x inf): such values are zeroed in shared memory and the rows
-// that see them made NaN.
+// The mask: per token a bit for each drafted token that it sees, found by a walk up
+// the tree a run ahead; 128 bits of it per key tile that reaches the drafted keys.
+// A row always sees itself.  A drafted value that is infinite or NaN must not reach
+// the rows that do not see it (0 x inf): such values are zeroed in shared memory and
+// the rows that see them made NaN.
+//
+// Measured (CUDA graphs): 192 sequences of up to 2900 tokens, chains of 1 to 8 drafts,
+// 16 / 8 heads, bf16: 189 us, 0.94 of the copy rate; 32 of 100 to 8192, 16 to 32 drafts,
+// 32 / 8: 96.6, 0.80; 5 of 40000 to 100001, 9 to 13 drafts, 32 / 4: 133.6, 0.85; 8 of
+// 8000 to 32768, 60 to 64 drafts (two query tiles), 32 / 8, fp16: 198, 0.54; one of 777,
+// 5 drafts: 11.3, a chain of latencies (plan, one key tile, join).  With one query tile
+// 152 equal contexts of 8192 run at 0.95; ragged batches lose what the SMs' unequal
+// speeds leave at the end.  With two a pair takes 1.3 us: P waits for S, S for the P V
+// that has left its columns, and tensor memory's loads and stores take turns with the
+// products (without the low term's product 170, without its stores 185, without the
+// maximum's pass 184, without exponentials 199).  Maxima found by the epilogue's warps
+// (203), and on top of that units of 64 keys, four of them in tensor memory (247), gain
+// nothing.
 #include <limits.h>
 
 #include "decode_mma.cuh"
@@ -46,7 +64,7 @@ constexpr int kTThreads = 512, kTWarpEpi = 4, kTWarpLoad0 = 8, kTKLoad = 2, kTWa
 // launch holds, so an increase never waits forever).
 constexpr int kTRegsSoftmax = 168, kTRegsEpi = 136, kTRegsLoad = 96, kTRegsPrep = 112;
 static_assert(128 * (kTRegsSoftmax + kTRegsEpi + kTRegsLoad + kTRegsPrep) <= 65536, "register split fits the launch");
-constexpr int kTStages = 3;  // of K, and of V
+constexpr int kTStages = 3;  // of K, and of V (two CTAs per SM of one stage each: 1.7 to 1.95 us a pair, not 1.55)
 constexpr int T_OFF_K = 0;
 constexpr int T_OFF_V = T_OFF_K + kTStages * 2 * kHalf;
 constexpr int kTMaskWords = PA_MAX_TREE_LEN / 32;
@@ -557,10 +575,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const int at = 8 * i + (lane >> 2), row = (warp & 3) * 32 + pass * 16 + at;
+                T *op = static_cast<T *>(p.out) + out0 + ((int64_t)(row / G) * p.num_q_heads + row % G) * kHeadDim;
                 if (row < live_rows)
-                  reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + out0 +
-                                            ((int64_t)(row / G) * p.num_q_heads + row % G) * kHeadDim)[4 * cc + (lane & 3)] =
-                      stage[at * 4 + ((lane & 3) ^ (at & 3))];
+                  reinterpret_cast<uint4 *>(op)[4 * cc + (lane & 3)] = stage[at * 4 + ((lane & 3) ^ (at & 3))];
               }
               __syncwarp();
             }
@@ -680,7 +697,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const bool for_k = lw < kTKLoad;
     // (With two CTAs the first K warp has all 16 boxes and issues every second one for both, and
     // so does the V warp with its 8; what cannot be read each CTA zeroes for itself.)
-    const int box = for_k && NT == 1 ? lw + kTKLoad * lane : lane, boxes = for_k ? 16 : 8, page = for_k ? box >> 1 : box;
+    const int box = for_k && NT == 1 ? lw + kTKLoad * lane : lane, boxes = for_k ? 16 : 8;
+    const int page = for_k ? box >> 1 : box;
     const bool issues = NT == 1 || (box & 1) == sub;
     uint64_t *free = for_k ? bars.k_free : bars.v_free;
     uint8_t *dst0 = smem + (for_k ? T_OFF_K + (box & 1) * kHalf + page * 2048 : T_OFF_V + page * kVPage);
@@ -774,7 +792,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     // ---------------- MMA issuer (warp-uniform loop, one elected lane issues) ----------------
     griddep_wait();
     griddep_launch_dependents();  // (the join waits for this grid; its blocks start as CTAs leave)
-    if (lane == 0 && sub == 0) {  // the join's record of this worker (after the wait: the previous call's join may still read)
+    if (lane == 0 && sub == 0) {  // the join's record (after the wait: the previous call's join may still read)
       JoinRecord rec = {};
       if (x0 < x1) {
         // The group of the last pair: joined here if its first unit began in this share and others go on with it.
@@ -931,7 +949,9 @@ __global__ void __launch_bounds__(kTJoinThreads) attn_tree_join_kernel(const __g
             ml[n][u] = make_float2(-INFINITY, 0.f);
             o[n][u] = make_float4(0.f, 0.f, 0.f, 0.f);
             // (a worker with no more than the group's cost has no piece)
-            if (i < items && f0 + u <= fl && k0 + min(part_start(f0 + u + 1, rec.total, rec.workers), xa + bl) - xa > p.run_cost) {
+            // (a piece without keys does not exist)
+            auto until = [&]() { return min(part_start(f0 + u + 1, rec.total, rec.workers), xa + bl); };
+            if (i < items && f0 + u <= fl && k0 + until() - xa > p.run_cost) {
               const int64_t slot = 2 * ((f0 + u) * NT + cta) + (f0 + u == ff ? second : 0);
               ml[n][u] = __ldcg(p.ws_ml + slot * 128 + tr);
               o[n][u] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o) + (slot * 32 + quad_of(i)) * 128 + tr);
@@ -989,11 +1009,12 @@ cudaError_t launch_tree_typed(TreeParams p, const CUtensorMap *maps, int sms, cu
   // (calls of a few key tiles per worker are not dealt but spread: there the cost would leave workers without keys)
   const int64_t groups = (int64_t)p.num_kv_heads * (p.num_seqs + (int64_t)p.num_tokens * G / (128 * NT));
   p.run_cost = groups * ((p.max_len + 127) / 128) > 4 * workers ? kTreeRunCost : 0;
-  e = NT == 2 ? launch_pdl_cluster(attn_tree_kernel<T, G, NT>, dim3(workers * NT), dim3(kTThreads), smem, NT, stream,
-                                   maps[0], maps[1], p)
-              : launch_pdl(attn_tree_kernel<T, G, NT>, dim3(workers), dim3(kTThreads), smem, stream, maps[0], maps[1], p);
+  const dim3 grid(workers * NT), block(kTThreads);
+  e = NT == 2 ? launch_pdl_cluster(attn_tree_kernel<T, G, NT>, grid, block, smem, NT, stream, maps[0], maps[1], p)
+              : launch_pdl(attn_tree_kernel<T, G, NT>, grid, block, smem, stream, maps[0], maps[1], p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_tree_join_kernel<T, G, NT>, dim3(workers, kTJoinParts * NT), dim3(kTJoinThreads), 0, stream, p);
+  const dim3 parts(workers, kTJoinParts * NT);
+  return launch_pdl(attn_tree_join_kernel<T, G, NT>, parts, dim3(kTJoinThreads), 0, stream, p);
 }
 
 struct TreeLayout {

@@ -65,7 +65,8 @@ def test_drafted_steps_leave_the_cache_of_single_steps(dtype, hq, hkv):
         s.commit(len(t))
     accepted = 0
     for step in range(steps):
-        trees = [make_tree(("random", "full", "chain", "forest")[(i + step) % 4], int(rng.integers(1, 14)), rng) for i in range(S)]
+        shapes = [("random", "full", "chain", "forest")[(i + step) % 4] for i in range(S)]
+        trees = [make_tree(shape, int(rng.integers(1, 14)), rng) for shape in shapes]
         drafts = [rng.integers(0, 3, len(t)) for t in trees]
         slots = [s.reserve(len(t)) for s, t in zip(seqs, trees)]
         bt, _, tree_lens, lens = pa.build_step_tables(seqs, 24)
@@ -74,7 +75,8 @@ def test_drafted_steps_leave_the_cache_of_single_steps(dtype, hq, hkv):
         pos = np.concatenate([s.length + _depths(t) for s, t in zip(seqs, trees)])
         queries = write(np.concatenate(slots), ids, pos)
         parents = cu(np.concatenate(trees))
-        outs = [pa.paged_attn_tree(queries[la], *pools[la], bt, lens, tree_lens, parents, SCALE) for la in range(layers)]
+        outs = [pa.paged_attn_tree(queries[la], *pools[la], bt, lens, tree_lens, parents, SCALE)
+                for la in range(layers)]
         # what the "model" chooses after each token: any function of the outputs that is the same below
         target = (outs[-1].float().sum((1, 2)).abs() * 64).long() % 3
         path, num, nxt, new_lens = pa.tree_accept(ids, target, parents, tree_lens, lens, handle, bt, max_tree_len=16)
@@ -145,10 +147,11 @@ def test_a_captured_step():
     def step():
         outs = []
         for la in range(2):
-            rq = pa.rope_kv_write_axes(q, k, v, inv, a["pos"], pa.rope_axes([64, 0, 0]), a["slots"], pool[la, 0], pool[la, 1])
-            outs.append(pa.paged_attn_tree(rq, pool[la, 0], pool[la, 1], a["bt"], a["lens"], a["n"], a["parents"], SCALE,
-                                           workspace=ws))
-        return outs + list(pa.tree_accept(draft, target, a["parents"], a["n"], a["lens"], handle, a["bt"], max_tree_len=n))
+            kc, vc = pool[la]
+            rq = pa.rope_kv_write_axes(q, k, v, inv, a["pos"], pa.rope_axes([64, 0, 0]), a["slots"], kc, vc)
+            outs.append(pa.paged_attn_tree(rq, kc, vc, a["bt"], a["lens"], a["n"], a["parents"], SCALE, workspace=ws))
+        return outs + list(pa.tree_accept(draft, target, a["parents"], a["n"], a["lens"], handle, a["bt"],
+                                          max_tree_len=n))
 
     step()
     torch.cuda.synchronize()
