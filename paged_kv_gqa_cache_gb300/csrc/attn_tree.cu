@@ -38,17 +38,19 @@
 // the rows that see them made NaN.
 //
 // Measured (CUDA graphs): 192 sequences of up to 2900 tokens, chains of 1 to 8 drafts,
-// 16 / 8 heads, bf16: 189 us, 0.94 of the copy rate; 32 of 100 to 8192, 16 to 32 drafts,
-// 32 / 8: 96.6, 0.80; 5 of 40000 to 100001, 9 to 13 drafts, 32 / 4: 133.6, 0.85; 8 of
-// 8000 to 32768, 60 to 64 drafts (two query tiles), 32 / 8, fp16: 198, 0.54; one of 777,
-// 5 drafts: 11.3, a chain of latencies (plan, one key tile, join).  With one query tile
+// 16 / 8 heads, bf16: 188 us, 0.94 of the copy rate; 32 of 100 to 8192, 16 to 32 drafts,
+// 32 / 8: 96.3, 0.80; 5 of 40000 to 100001, 9 to 13 drafts, 32 / 4: 133, 0.86; 8 of 8000
+// to 32768, 60 to 64 drafts (two query tiles), 32 / 8, fp16: 194, 0.55; one of 777, 5
+// drafts: 11.0, a chain of latencies (plan, one key tile, join).  With one query tile
 // 152 equal contexts of 8192 run at 0.95; ragged batches lose what the SMs' unequal
-// speeds leave at the end.  With two a pair takes 1.3 us: P waits for S, S for the P V
-// that has left its columns, and tensor memory's loads and stores take turns with the
-// products (without the low term's product 170, without its stores 185, without the
-// maximum's pass 184, without exponentials 199).  Maxima found by the epilogue's warps
-// (203), and on top of that units of 64 keys, four of them in tensor memory (247), gain
-// nothing.
+// speeds leave at the end.  With two a pair takes 1.3 us, the tensor pipe 67 % busy: P
+// waits for S, S for the P V that has left its columns, and tensor memory's loads and
+// stores take turns with the products (of 202, without the low term's product 170,
+// without its stores 185, without the maximum's pass 184, without exponentials 199).
+// P V goes in halves of 64 keys, the first as soon as its P is ready (199 to 193, and
+// 11.2 to 11.0).  More warps on the softmax gain nothing: the maxima found by the
+// epilogue's warps 195, half of the keys each with the maxima exchanged 213; units of
+// 64 keys, four of them in tensor memory: 247.
 #include <limits.h>
 
 #include "decode_mma.cuh"
@@ -89,7 +91,7 @@ struct TBars {
   uint64_t k_full[kTStages], k_free[kTStages];
   uint64_t v_full[2][kTStages];  // [1]: a key tile that reaches the drafted keys (looked at before it is used)
   uint64_t v_free[kTStages];   // (k_free, v_free: in every CTA of the worker)
-  uint64_t s_full[2], p_full[2], o_done;  // o_done: P V of a key tile added to O
+  uint64_t s_full[2], p_full[2][2], o_done;  // p_full: per half of the keys; o_done: P V of a key tile added to O
   uint64_t q_full[2];          // per run: its queries and masks are in place
   uint64_t look[kTStages];     // per key tile that reaches the drafted keys: its values are fit for P V
   uint64_t x_full[2], run_done, o_free;  // per run: (m, l) written; every P V done; O read
@@ -297,7 +299,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i], 128);
+      mbar_init(&bars.p_full[i][0], 128);
+      mbar_init(&bars.p_full[i][1], 128);
       mbar_init(&bars.q_full[i], 128);
       mbar_init(&bars.x_full[i], 128);
     }
@@ -453,16 +456,23 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             tc::wait_ld();
             if (cc < 3) tc::ld_32x32b_x32(s_addr + cc * 32 + 32, v[(cc + 1) & 1]);
             exp_pack_store32<T>(v[cc & 1], s_addr + cc * 32, sl2, m, ls);
+            if (cc == 1) {  // the first half's P V goes ahead
+              tc::wait_st();
+              tc::fence_before_sync();
+              mbar_arrive(&bars.p_full[st][0]);
+            }
           }
           l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
           tc::wait_st();
+        } else {
+          mbar_arrive(&bars.p_full[st][0]);
         }
         if (kt == kt_end - 1) {
           xm[(ui & 1) * 128 + r] = make_float2(m_ref, l);
           mbar_arrive(&bars.x_full[ui & 1]);
         }
         tc::fence_before_sync();
-        mbar_arrive(&bars.p_full[st]);
+        mbar_arrive(&bars.p_full[st][1]);
       }
     }
   } else if (warp < kTWarpLoad0) {
@@ -835,17 +845,23 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         landed ^= 1u << st;
       }
       if (p_first && p_run > 0 && !wait_all(&bars.o_free, (p_run - 1) & 1)) return false;
-      if (!wait_all(&bars.p_full[pc & 1], (pc >> 1) & 1)) return false;
-      tc::fence_after_sync();
-      if (leader) {
-        const uint64_t vdesc = vdesc0 + (uint64_t)st * kStageStep;
+      const uint64_t vdesc = vdesc0 + (uint64_t)st * kStageStep;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t a_hi = tmem + (pc & 1) * 128 + 32 * (kk >> 1) + 8 * (kk & 1);
-          const uint64_t bdesc = vdesc + (uint64_t)(kk * (kVPage >> 4));
-          tc::mma_f16_ts(tmem + kTColO, a_hi, bdesc, IDESC_O, kk > 0 || !p_first ? 1u : 0u);
-          tc::mma_f16_ts(tmem + kTColO, a_hi + 16, bdesc, IDESC_O, 1u);
+      for (int half = 0; half < 2; ++half) {  // (as soon as P of its 64 keys is ready)
+        if (!wait_all(&bars.p_full[pc & 1][half], (pc >> 1) & 1)) return false;
+        tc::fence_after_sync();
+        if (leader) {
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
+            const uint32_t a_hi = tmem + (pc & 1) * 128 + 32 * (kk >> 1) + 8 * (kk & 1);
+            const uint64_t bdesc = vdesc + (uint64_t)(kk * (kVPage >> 4));
+            tc::mma_f16_ts(tmem + kTColO, a_hi, bdesc, IDESC_O, kk > 0 || !p_first ? 1u : 0u);
+            tc::mma_f16_ts(tmem + kTColO, a_hi + 16, bdesc, IDESC_O, 1u);
+          }
         }
+        __syncwarp();
+      }
+      if (leader) {
         tc::commit(&bars.o_done);
         if constexpr (NT == 2) commit_both(&bars.v_free[st]); else tc::commit(&bars.v_free[st]);
         if (p_last) tc::commit(&bars.run_done);

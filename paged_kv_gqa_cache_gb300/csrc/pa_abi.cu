@@ -1138,6 +1138,7 @@ pa_status tree_move_call(TreeAcceptParams &p, const int32_t *tree_lens, const in
   if (!aligned4(p.path) || !aligned4(p.path_lens) || !aligned4(tree_lens) || !aligned4(context_lens) ||
       !aligned4(block_tables) || !aligned4(new_context_lens))
     return PA_ERR_ALIGN;
+  p.block_tables = num_layers > 0 ? block_tables : nullptr;
   // every CTA of a sequence reads the inputs, and one writes the outputs meanwhile
   struct Range {
     const void *at;
@@ -1152,7 +1153,7 @@ pa_status tree_move_call(TreeAcceptParams &p, const int32_t *tree_lens, const in
                           {p.next_tokens, greedy ? 2 * lens_bytes : 0, true},
                           {tree_lens, lens_bytes, false},
                           {context_lens, lens_bytes, false},
-                          {block_tables, num_layers > 0 ? lens_bytes * max_blocks_per_seq : 0, false},
+                          {p.block_tables, p.block_tables ? lens_bytes * max_blocks_per_seq : 0, false},
                           {p.draft, tokens * sizeof(int64_t), false},
                           {p.target, tokens * sizeof(int64_t), false},
                           {p.parents, tokens * sizeof(int32_t), false}};
@@ -1166,7 +1167,6 @@ pa_status tree_move_call(TreeAcceptParams &p, const int32_t *tree_lens, const in
   if (st != PA_OK) return st;
   p.tree_lens = tree_lens;
   p.context_lens = context_lens;
-  p.block_tables = num_layers > 0 ? block_tables : nullptr;
   p.new_lens = new_context_lens;
   p.err = d->err;
   p.num_seqs = num_seqs;

@@ -43,8 +43,8 @@
 // and width of images and video); a thread then multiplies each of its pairs by its own
 // axis's position, the rest is the same.  A variant of its own, because the choice in
 // the loop slowed the call with one axis (75 against 69.5 us of graph time, the 16383
-// tokens).  16383 tokens of 32 / 8 heads with the norm, three axes, bf16: 71 us, 0.84 of
-// the copy rate; 911 tokens without: 4.9; 8 of 16 / 8 heads: 2.3.  A step's positions
+// tokens).  16383 tokens of 32 / 8 heads with the norm, three axes, bf16: 71.5 us, 0.83 of
+// the copy rate; 911 tokens without: 4.6; 8 of 16 / 8 heads: 2.0.  A step's positions
 // loaded a step ahead: 76 (registers).
 #include "pa_device.cuh"
 
