@@ -264,4 +264,9 @@ def test_bindings_refuse():
         _run(c, max_tree_len=0)
     with pytest.raises(ValueError):
         pa.tree_move(c["parents"].view(1, 5), c["n"].repeat(2), c["n"], c["lens"], c["handle"], c["bt"])
+    k, v = c["pools"][0]
+    for pools in ([(k, v), (k, v)], [(k, k)], [(k[:2], v[:2]), (k[1:3], v[2:4])]):  # a row of them would move twice
+        with pytest.raises(ValueError):
+            pa.layer_pools(pools)
+    pa.layer_pools([(k[:2], v[:2]), (k[2:4], v[2:4])])
     assert TORCH["f16"] is c["pools"][0][0].dtype
