@@ -8,9 +8,9 @@
 // The n x G query rows of a sequence for one KV head against its keys are a
 // matrix product: query tiles of 128 rows (128 / G tokens x the G heads), key
 // tiles of 128 keys, on the tcgen05 tensor cores.  NT query tiles (1 or 2) form a
-// group, taken by a cluster of NT CTAs in step, a worker: each fetches half of
-// every key tile for both (TMA multicast), so that HBM and L2 are read once per
-// group.  All (group, key tile) pairs of the call are dealt evenly to the workers
+// group, taken by NT CTAs at the same time, a worker, so that one of them reads the
+// keys from HBM and the other from L2 (each on its own: nothing passes between
+// them).  All (group, key tile) pairs of the call are dealt evenly to the workers
 // (one CTA per SM), so one long sequence or many short ones fill the GPU alike.  A
 // worker's share is a row of runs: consecutive key tiles of one group.  A run that
 // holds all keys of its group writes the outputs; a group cut between workers
@@ -40,17 +40,17 @@
 // Measured (CUDA graphs): 192 sequences of up to 2900 tokens, chains of 1 to 8 drafts,
 // 16 / 8 heads, bf16: 188 us, 0.94 of the copy rate; 32 of 100 to 8192, 16 to 32 drafts,
 // 32 / 8: 96.3, 0.80; 5 of 40000 to 100001, 9 to 13 drafts, 32 / 4: 133, 0.86; 8 of 8000
-// to 32768, 60 to 64 drafts (two query tiles), 32 / 8, fp16: 194, 0.55; one of 777, 5
+// to 32768, 60 to 64 drafts (two query tiles), 32 / 8, fp16: 201, 0.53; one of 777, 5
 // drafts: 11.0, a chain of latencies (plan, one key tile, join).  With one query tile
 // 152 equal contexts of 8192 run at 0.95; ragged batches lose what the SMs' unequal
 // speeds leave at the end.  With two a pair takes 1.3 us, the tensor pipe 67 % busy: P
 // waits for S, S for the P V that has left its columns, and tensor memory's loads and
 // stores take turns with the products (of 202, without the low term's product 170,
 // without its stores 185, without the maximum's pass 184, without exponentials 199).
-// P V goes in halves of 64 keys, the first as soon as its P is ready (199 to 193, and
-// 11.2 to 11.0).  More warps on the softmax gain nothing: the maxima found by the
-// epilogue's warps 195, half of the keys each with the maxima exchanged 213; units of
-// 64 keys, four of them in tensor memory: 247.
+// P V goes in halves of 64 keys, the first as soon as its P is ready (3 %, and 11.2 to
+// 11.0).  More warps on the softmax gain nothing: the maxima found by the epilogue's
+// warps cost 1 %, half of the keys each with the maxima exchanged 10; units of 64 keys,
+// four of them in tensor memory, 28.
 #include <limits.h>
 
 #include "decode_mma.cuh"
@@ -90,7 +90,7 @@ struct TRunInfo {
 struct TBars {
   uint64_t k_full[kTStages], k_free[kTStages];
   uint64_t v_full[2][kTStages];  // [1]: a key tile that reaches the drafted keys (looked at before it is used)
-  uint64_t v_free[kTStages];   // (k_free, v_free: in every CTA of the worker)
+  uint64_t v_free[kTStages];
   uint64_t s_full[2], p_full[2][2], o_done;  // p_full: per half of the keys; o_done: P V of a key tile added to O
   uint64_t q_full[2];          // per run: its queries and masks are in place
   uint64_t look[kTStages];     // per key tile that reaches the drafted keys: its values are fit for P V
@@ -194,35 +194,6 @@ struct JoinRecord {
 };
 static_assert(sizeof(JoinRecord) == 48, "three 16-byte loads");
 
-// Multicast to both CTAs of a cluster, at the same addresses in each: 4-D and 5-D tiled
-// loads, completing on each one's `bar`, and the arrival when every MMA issued so far by
-// this thread completes.
-__device__ __forceinline__ void tma_load_4d_both(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1,
-                                                 int c2, int c3, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7, %8;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)),
-      "h"((uint16_t)3), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_5d_both(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1,
-                                                 int c2, int c3, int c4, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8, %9;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar)),
-      "h"((uint16_t)3), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ void commit_both(uint64_t *bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-
 // Whether one of the two 16-bit values of u is infinite or NaN.
 template <typename T>
 __device__ __forceinline__ bool not_finite2(uint32_t u) {
@@ -290,11 +261,11 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
     for (int i = 0; i < kTStages; ++i) {
-      mbar_init(&bars.k_full[i], NT == 1 ? kTKLoad : 1);
-      mbar_init(&bars.k_free[i], NT);
+      mbar_init(&bars.k_full[i], kTKLoad);
+      mbar_init(&bars.k_free[i], 1);
       mbar_init(&bars.v_full[0][i], 1);
       mbar_init(&bars.v_full[1][i], 1);
-      mbar_init(&bars.v_free[i], NT);
+      mbar_init(&bars.v_free[i], 1);
       mbar_init(&bars.look[i], 128);
     }
     for (int i = 0; i < 2; ++i) {
@@ -332,7 +303,6 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   });
   tc::fence_before_sync();
   __syncthreads();
-  if constexpr (NT == 2) cluster_sync();  // (the other CTA's barriers are initialised)
   tc::fence_after_sync();
   const uint32_t tmem = bars.tmem_base;
   TreePlan pl;
@@ -350,15 +320,16 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   // (the outcome of a wait is made warp-uniform: what follows is warp-wide)
   auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL, mbar_wait(bar, parity)) != 0; };
   // the first token of this CTA's query tile (a group may be the last and not full: then the
-  // second tile has fewer rows or none, and its CTA only keeps step)
+  // second tile has fewer rows or none)
   auto first_token = [&](const TRun &U) { return U.g * TG + sub * TQ; };
-  // The worker's next run from pair x on (x0: the first), x behind it; false: no more.
+  // This CTA's next run from pair x on (x0: the first), x behind it; false: no more.
   auto next_run = [&](TRun &U, int &x, bool &begun) {
     while (x < x1) {
       if (!begun) U.at<TG>(pl, x, x1); else U.next<TG>(pl, x, x1);
       begun = true;
       x += U.vb - U.va;
-      if (U.vb > pl.cost) return true;  // (else there are none of the group's keys in it)
+      // (else there are none of the group's keys in it, or no rows of this CTA)
+      if (U.vb > pl.cost && first_token(U) < U.n) return true;
     }
     return false;
   };
@@ -705,11 +676,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     // their way: a table read per tile would hold up every copy by an L2 trip.
     const int lw = warp - kTWarpLoad0;
     const bool for_k = lw < kTKLoad;
-    // (With two CTAs the first K warp has all 16 boxes and issues every second one for both, and
-    // so does the V warp with its 8; what cannot be read each CTA zeroes for itself.)
-    const int box = for_k && NT == 1 ? lw + kTKLoad * lane : lane, boxes = for_k ? 16 : 8;
+    const int box = for_k ? lw + kTKLoad * lane : lane, boxes = for_k ? 16 : 8;
     const int page = for_k ? box >> 1 : box;
-    const bool issues = NT == 1 || (box & 1) == sub;
     uint64_t *free = for_k ? bars.k_free : bars.v_free;
     uint8_t *dst0 = smem + (for_k ? T_OFF_K + (box & 1) * kHalf + page * 2048 : T_OFF_V + page * kVPage);
     const uint32_t bytes = for_k ? 2048u : (uint32_t)kVPage;
@@ -719,7 +687,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     uint32_t issued = 0;  // per barrier (8 bits per kind, 2 per stage) bit 1: any copy, bit 0: the last one's parity
     bool waited = false;
     TRun N = {};
-    bool more = NT == 1 || lw != 1;
+    bool more = true;
     for (int ui = -1; !timed_out; ++ui) {  // (the first time round only the first run is published)
       if (!more) break;
       U = N;
@@ -732,7 +700,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         I.start = N.len - N.n;
         I.len = N.len;
         I.row = N.row0 + tok0;
-        I.live_rows = max(min(TQ, N.n - tok0), 0) * G;
+        I.live_rows = min(TQ, N.n - tok0) * G;
         I.h = N.h;
         I.s = N.s;
         I.tok0 = tok0;
@@ -779,13 +747,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         __syncwarp();
         const int bit = 2 * st + (t >= tail ? 8 : 0);
         issued = issued >> bit & 2 ? issued ^ 1u << bit : issued | 2u << bit;
-        if (ok && issues) {
-          if constexpr (NT == 2) {
-            if (for_k)
-              tma_load_4d_both(dst, &kmap, full, (box & 1) * 64, U.h, 0, id, policy);
-            else
-              tma_load_5d_both(dst, &vmap, full, 0, 0, 0, U.h, id, policy);
-          } else if (for_k)
+        if (ok) {
+          if (for_k)
             tma_load_4d_hint(dst, &kmap, full, (box & 1) * 64, U.h, 0, id, policy);
           else
             tma_load_5d_hint(dst, &vmap, full, 0, 0, 0, U.h, id, policy);
@@ -863,7 +826,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       }
       if (leader) {
         tc::commit(&bars.o_done);
-        if constexpr (NT == 2) commit_both(&bars.v_free[st]); else tc::commit(&bars.v_free[st]);
+        tc::commit(&bars.v_free[st]);
         if (p_last) tc::commit(&bars.run_done);
       }
       __syncwarp();
@@ -892,7 +855,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             tc::mma_f16_ts(tmem + (c & 1) * 128, tmem + kTColQ + (ui & 1) * 64 + 8 * kk,
                            kdesc + (uint64_t)((kk >> 2) * kHalfStep + (kk & 3) * 2), IDESC_S, kk > 0 ? 1u : 0u);
           tc::commit(&bars.s_full[c & 1]);
-          if constexpr (NT == 2) commit_both(&bars.k_free[st]); else tc::commit(&bars.k_free[st]);
+          tc::commit(&bars.k_free[st]);
         }
         __syncwarp();
         if (pc >= 0 && !issue_pv()) {
@@ -916,10 +879,6 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   if (timed_out) set_error(p.err, PA_ERR_TIMEOUT, (int)blockIdx.x);
   tc::fence_before_sync();
   __syncthreads();
-  if constexpr (NT == 2) {  // (this CTA's copies and arrivals in the other's memory are over)
-    __syncwarp();
-    cluster_sync();
-  }
   if (warp == kTWarpMma) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
@@ -994,40 +953,12 @@ cudaError_t launch_tree_typed(TreeParams p, const CUtensorMap *maps, int sms, cu
   const int smem = T_OFF_PLAN + 2 * (p.num_seqs + 1) * 4;
   cudaError_t e = kernel_setup(setup, attn_tree_kernel<T, G, NT>, smem, kTThreads, nullptr);
   if (e != cudaSuccess) return e;
-  int workers = sms;
-  if (NT == 2) {  // as many clusters as run at the same time
-    static std::mutex mutex;
-    static unsigned long long ctx = 0;
-    static int clusters = 0;
-    std::lock_guard<std::mutex> lock(mutex);
-    if (ctx != launch_context_id()) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(sms / NT * NT);
-      cfg.blockDim = dim3(kTThreads);
-      cfg.dynamicSmemBytes = T_OFF_PLAN + 2 * (kTreeMaxSeqs + 1) * 4;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = NT;
-      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      int n = 0;
-      e = cudaFuncSetAttribute(attn_tree_kernel<T, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)cfg.dynamicSmemBytes);
-      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, attn_tree_kernel<T, G, NT>, &cfg);
-      if (e != cudaSuccess) return e;
-      if (n < 1) return cudaErrorInvalidConfiguration;
-      clusters = n < sms / NT ? n : sms / NT;
-      ctx = launch_context_id();
-    }
-    workers = clusters;
-  }
+  const int workers = sms / NT > 0 ? sms / NT : 1;
   // (calls of a few key tiles per worker are not dealt but spread: there the cost would leave workers without keys)
   const int64_t groups = (int64_t)p.num_kv_heads * (p.num_seqs + (int64_t)p.num_tokens * G / (128 * NT));
   p.run_cost = groups * ((p.max_len + 127) / 128) > 4 * workers ? kTreeRunCost : 0;
   const dim3 grid(workers * NT), block(kTThreads);
-  e = NT == 2 ? launch_pdl_cluster(attn_tree_kernel<T, G, NT>, grid, block, smem, NT, stream, maps[0], maps[1], p)
-              : launch_pdl(attn_tree_kernel<T, G, NT>, grid, block, smem, stream, maps[0], maps[1], p);
+  e = launch_pdl(attn_tree_kernel<T, G, NT>, grid, block, smem, stream, maps[0], maps[1], p);
   if (e != cudaSuccess) return e;
   const dim3 parts(workers, kTJoinParts * NT);
   return launch_pdl(attn_tree_join_kernel<T, G, NT>, parts, dim3(kTJoinThreads), 0, stream, p);
@@ -1057,7 +988,10 @@ cudaError_t launch_attn_tree(TreeParams p, void *workspace, const CUtensorMap *m
   p.records = reinterpret_cast<int32_t *>(ws);
   p.ws_ml = reinterpret_cast<float2 *>(ws + l.ml);
   p.ws_o = reinterpret_cast<float *>(ws + l.o);
-  // Two query tiles per group where the average tree fills more than one.
+  // Two query tiles per group where the average tree fills more than one.  Two against one,
+  // 32 / 8 heads, bf16: 19 sequences of 8192 with 33 drafts 171 us against 188, with 64 165
+  // against 195; 64 of 1024 with 33 87 against 96; one of 20000 with 33 40 against 64.  With
+  // 96 drafts, three tiles, a CTA in four has none: 325 against 283.
   const bool two = (int64_t)p.num_tokens * group > (int64_t)p.num_seqs * 128;
 #define PA_TREE_CASE(T, G) \
   if (group == G) \
