@@ -244,7 +244,11 @@ struct JoinState {
     float mx = M;
 #pragma unroll
     for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
-    if (mx == -INFINITY) return;
+    if (mx == -INFINITY) {  // no scores, or NaN alone (a maximum skips them): such a sum stays
+#pragma unroll
+      for (int u = 0; u < U; ++u) L += ml[u].y;
+      return;
+    }
     const float f = ex2(M - mx);
     L *= f;
     O.x *= f, O.y *= f, O.z *= f, O.w *= f;
