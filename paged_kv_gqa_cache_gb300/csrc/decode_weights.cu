@@ -144,14 +144,14 @@ decode_weights_kernel(const DecodeParams p, const float *scores, const float *we
     for (int f = lane; f < nf; f += 32) {
       const float2 ml = *reinterpret_cast<const float2 *>(p.ws_ml + ((slot0 + f) * G + warp) * 2);
       const float mn = fmaxf(m, ml.x);
-      if (mn > -INFINITY) l = l * exp2f(m - mn) + ml.y * exp2f(ml.x - mn);
+      l = mn > -INFINITY ? l * exp2f(m - mn) + ml.y * exp2f(ml.x - mn) : l + ml.y;  // (NaN scores alone: a NaN)
       m = mn;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       const float m2 = __shfl_xor_sync(FULL, m, off), l2 = __shfl_xor_sync(FULL, l, off);
       const float mn = fmaxf(m, m2);
-      if (mn > -INFINITY) l = l * exp2f(m - mn) + l2 * exp2f(m2 - mn);
+      l = mn > -INFINITY ? l * exp2f(m - mn) + l2 * exp2f(m2 - mn) : l + l2;
       m = mn;
     }
     if (lane == 0) {

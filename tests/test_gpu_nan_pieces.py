@@ -85,3 +85,14 @@ def test_outputs_of_the_decode_with_weights():
         _spoil(c, 0, lo, lo + 16, 1)
         mine, rest = _heads(weights._run(c, None, torch.zeros_like(c["w"]))[0], 1, 2)
         assert bool(mine[0].isnan().all()) and not bool(rest.isnan().any()) and not bool(mine[1].isnan().any()), lo
+
+
+def test_weights_of_the_decode_with_weights():
+    """The head's row sum is NaN, and so is the weight of every token."""
+    c = weights._case([9000, 40], 16, 8, "bf16", seed=4)
+    rest = [h for h in range(8) if h != 1]
+    for lo in range(0, 2048, 16):
+        _spoil(c, 0, lo, lo + 16, 1)
+        _, w = weights._run(c, None, torch.zeros_like(c["w"]))
+        assert bool(w[0, 1, :9000].isnan().all()) and not bool(w[0, 1, 9000:].isnan().any()), lo
+        assert not bool(w[0, rest].isnan().any()) and not bool(w[1].isnan().any()), lo
