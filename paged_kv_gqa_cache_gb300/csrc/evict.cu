@@ -151,7 +151,10 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv_evict_kernel(const EvictPara
       n > p.out_stride) {  // uniform over the cluster
     if (h == 0 && rank == 0 && tid == 0) {
       set_error(p.err, PA_ERR_RANGE, s);
-      if (p.flags & PA_EVICT_MARK_LENGTHS) p.new_lens[s] = -1;
+      if (p.flags & PA_EVICT_MARK_LENGTHS) {
+        p.new_lens[s] = -1;
+        __threadfence();  // (as at the end)
+      }
     }
     if (p.flags & PA_EVICT_MARK_KEPT) {
       int32_t *row = p.kept + ((int64_t)s * hkv + h) * p.budget;

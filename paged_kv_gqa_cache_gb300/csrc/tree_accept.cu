@@ -122,7 +122,10 @@ tree_accept_kernel(const __grid_constant__ TreeAcceptParams p, int layers_per_ct
     if (!ok) dep = 0;
   }
   if (scribe && i == 0) {
+    // An attention call enqueued next reads the lengths before its dependency wait, so this
+    // kernel never releases its dependents early and makes them visible before it ends.
     p.new_lens[s] = ok ? start + dep : -1;
+    __threadfence();
     if (!ok) set_error(p.err, PA_ERR_RANGE, s);
   }
   if (p.num_layers == 0) return;

@@ -15,3 +15,14 @@ def test_nothing_is_multicast_in_a_cluster(name):
     with open(os.path.join(CSRC, name)) as f:
         text = f.read()
     assert not re.search(r"multicast\s*::\s*cluster", text)
+
+
+@pytest.mark.parametrize("name", ["evict.cu", "tree_accept.cu"])
+def test_new_lengths_are_visible_before_their_kernel_ends(name):
+    """The attention calls read the lengths before their dependency wait: a kernel that writes
+    them fences behind the store and lets nothing start early."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = f.read()
+    stores = re.findall(r"p\.new_lens\[s\] = [^;]*;(\s*__threadfence\(\);)?", text)
+    assert stores and all(stores)
+    assert "griddep_launch_dependents" not in text
