@@ -686,12 +686,7 @@ __device__ __forceinline__ void merge_fragments(const DecodeParams &p, int s, in
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mc = fmaxf(mc, __shfl_xor_sync(FULL, mc, off));
     const float Mn = fmaxf(M, mc);
-    if (Mn == -INFINITY) {  // (uniform) no scores yet, or NaN alone (a maximum skips them): such a sum stays
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) lf += __shfl_xor_sync(FULL, lf, off);
-      L += lf;
-      continue;
-    }
+    if (Mn == -INFINITY) continue;  // no valid fragment yet (uniform)
     const float so = exp2f(M - Mn);
     const float wgt = (mf > -INFINITY) ? exp2f(mf - Mn) : 0.f;
     float lw = lf * wgt;

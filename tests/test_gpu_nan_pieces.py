@@ -96,24 +96,3 @@ def test_weights_of_the_decode_with_weights():
         _, w = weights._run(c, None, torch.zeros_like(c["w"]))
         assert bool(w[0, 1, :9000].isnan().all()) and not bool(w[0, 1, 9000:].isnan().any()), lo
         assert not bool(w[0, rest].isnan().any()) and not bool(w[1].isnan().any()), lo
-
-
-def _plain(c):
-    return pa.paged_attn_decode(c["q"], c["kc"], c["vc"], c["bt"], c["lens"], weights.SCALE)
-
-
-@pytest.mark.parametrize("n", [40, 1000, 9000])
-def test_outputs_of_the_plain_decode(n):
-    c = weights._case([n, 40], 16, 8, "f16", seed=5)
-    for lo in range(0, min(n, 2048), 16):
-        _spoil(c, 0, lo, min(lo + 16, n), 3)
-        mine, rest = _heads(_plain(c), 3, 2)
-        assert bool(mine[0].isnan().all()) and not bool(rest.isnan().any()) and not bool(mine[1].isnan().any()), lo
-
-
-def test_outputs_of_the_plain_decode_of_a_batch():
-    c = weights._case([9000] * 40, 16, 8, "f16", seed=5)
-    for lo in range(0, 4096, 16):
-        _spoil(c, 39, lo, lo + 16, 3)
-        mine, rest = _heads(_plain(c), 3, 2)
-        assert bool(mine[39].isnan().all()) and not bool(rest.isnan().any()) and not bool(mine[:39].isnan().any()), lo
