@@ -822,7 +822,9 @@ PA_API pa_status pa_paged_attn_tree(const void *q, const pa_kv_pool *pool, const
 /*
  * tree_accept — the drafted tokens that the model confirms, and the cache compacted
  * to them.  A token is accepted if it has no parent, or if its parent is accepted and
- * draft_tokens[i] == target_tokens[parent].  The deepest accepted token (of equally deep
+ * draft_tokens[i] == target_tokens[parent].  (One without parent stands for a token that
+ * the model has chosen, the last one sampled.  Nothing here decides between several: where
+ * they are drafts too, pa_tree_accept_ex.)  The deepest accepted token (of equally deep
  * ones the lowest index) ends sequence s's path: path[s][0 .. len) its ancestors from
  * the top down and itself, path[s][len .. path_stride) = -1, path_lens[s] = len,
  * next_tokens[s] its target, new_context_lens[s] = context_lens[s] - n + len.  In each
@@ -853,6 +855,20 @@ PA_API pa_status pa_tree_accept(const int64_t *draft_tokens, const int64_t *targ
                                 const int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *path,
                                 int32_t path_stride, int32_t *path_lens, int64_t *next_tokens,
                                 int32_t *new_context_lens, pa_stream_t stream);
+/*
+ * tree_accept_ex — pa_tree_accept for trees whose tokens without parent are drafts like
+ * the others:
+ *   context_targets  int64 [num_seqs], apart from the outputs: the model's choice after
+ *                 the committed context.  A token without parent is accepted only if
+ *                 it is that one.  Where nothing is accepted (an empty tree also), len 0,
+ *                 the choice is the next token.  NULL: as pa_tree_accept.
+ */
+PA_API pa_status pa_tree_accept_ex(const int64_t *draft_tokens, const int64_t *target_tokens,
+                                   const int64_t *context_targets, const int32_t *parents, int32_t num_tokens,
+                                   const int32_t *tree_lens, const int32_t *context_lens, int32_t num_seqs,
+                                   const pa_kv_pool *pools, int32_t num_layers, const int32_t *block_tables,
+                                   int32_t max_blocks_per_seq, int32_t *path, int32_t path_stride, int32_t *path_lens,
+                                   int64_t *next_tokens, int32_t *new_context_lens, pa_stream_t stream);
 /*
  * tree_move — the cache compacted to paths found by other means (sampled
  * verification): the moves and new lengths of pa_tree_accept for the given path

@@ -61,7 +61,7 @@ EXPORTS = ("pa_kv_cache_write", "pa_decode_workspace_bytes", "pa_paged_attn_deco
            "pa_decode_shared_workspace_bytes", "pa_paged_attn_decode_shared",
            "pa_decode_weights_workspace_bytes", "pa_paged_attn_decode_weights",
            "pa_sequence_unshare", "pa_sequence_truncate", "pa_rope_kv_write_axes", "pa_tree_workspace_bytes",
-           "pa_paged_attn_tree", "pa_tree_accept", "pa_tree_move",
+           "pa_paged_attn_tree", "pa_tree_accept", "pa_tree_accept_ex", "pa_tree_move",
            "pa_allocator_create", "pa_allocator_destroy", "pa_allocator_allocate", "pa_allocator_retain",
            "pa_allocator_release", "pa_allocator_refcount", "pa_allocator_stats_get", "pa_allocator_take_copies",
            "pa_sequence_create", "pa_sequence_destroy", "pa_sequence_reserve", "pa_sequence_commit",
@@ -183,6 +183,8 @@ def load_library(path: str = LIB_PATH):
         lib.pa_paged_attn_tree.restype = i32
         lib.pa_tree_accept.argtypes = [P, P, P, i32, P, P, i32, pool_p, i32, P, i32, P, i32, P, P, P, P]
         lib.pa_tree_accept.restype = i32
+        lib.pa_tree_accept_ex.argtypes = [P, P] + lib.pa_tree_accept.argtypes[1:]
+        lib.pa_tree_accept_ex.restype = i32
         lib.pa_tree_move.argtypes = [P, i32, P, P, P, i32, pool_p, i32, P, i32, P, P]
         lib.pa_tree_move.restype = i32
         lib.pa_decode_shared_workspace_bytes.argtypes = [i32, i32, i32, i32]
@@ -1212,13 +1214,17 @@ def _accept_outputs(stream, S: int, stride: int, device):
 
 def tree_accept(draft_tokens: torch.Tensor, target_tokens: torch.Tensor, parents: torch.Tensor,
                 tree_lens: torch.Tensor, context_lens: torch.Tensor, pools: Optional[LayerPools] = None,
-                block_tables: Optional[torch.Tensor] = None, max_tree_len: int = MAX_TREE_LEN, stream=None):
+                block_tables: Optional[torch.Tensor] = None, max_tree_len: int = MAX_TREE_LEN, stream=None,
+                context_targets: Optional[torch.Tensor] = None):
     """The drafted tokens (packed int64 [T], trees as in :func:`paged_attn_tree`) that
     the model's choices ``target_tokens`` (int64 [T], after each of them) confirm, and
     every layer's cache compacted to them in place (``pools`` from
     :func:`layer_pools`; None: nothing is moved).  Returns (path int32 [S, max_tree_len],
     -1 past its end; path lengths int32 [S]; the next tokens int64 [S]; new context
-    lengths int32 [S]); a refused sequence gets an empty path, and -1 in the others."""
+    lengths int32 [S]); a refused sequence gets an empty path, and -1 in the others.
+    A token without parent is taken as chosen by the model already (the last one
+    sampled), unless ``context_targets`` (int64 [S]), the model's choice after each
+    committed context, is given to judge those too."""
     dev = _device()
     i32, i64 = torch.int32, torch.int64
     if not (_fine(dev, i64, draft_tokens, target_tokens) and _fine(dev, i32, parents, tree_lens, context_lens)):
@@ -1232,12 +1238,19 @@ def tree_accept(draft_tokens: torch.Tensor, target_tokens: torch.Tensor, parents
     if max_tree_len < 1:
         raise ValueError("max_tree_len must be at least 1")
     T, S = tokens[0], seqs[0]
+    choice = None
+    if context_targets is not None:
+        if not _fine(dev, i64, context_targets):
+            _check_all(dev, (context_targets, "context_targets", i64))
+        if context_targets.shape != seqs:
+            raise ValueError(f"context_targets must be {list(seqs)}")
+        choice = context_targets.data_ptr()
     array, layers, tables, mb = _layer_args(dev, pools, block_tables, S)
     path, path_lens, next_tokens, new_lens = _accept_outputs(stream, S, max_tree_len, tree_lens.device)
-    _check((_lib or load_library()).pa_tree_accept(
-        draft_tokens.data_ptr(), target_tokens.data_ptr(), parents.data_ptr(), T, tree_lens.data_ptr(),
+    _check((_lib or load_library()).pa_tree_accept_ex(
+        draft_tokens.data_ptr(), target_tokens.data_ptr(), choice, parents.data_ptr(), T, tree_lens.data_ptr(),
         context_lens.data_ptr(), S, array, layers, tables, mb, path.data_ptr(), max_tree_len, path_lens.data_ptr(),
-        next_tokens.data_ptr(), new_lens.data_ptr(), _stream_of(stream, dev)), "pa_tree_accept")
+        next_tokens.data_ptr(), new_lens.data_ptr(), _stream_of(stream, dev)), "pa_tree_accept_ex")
     return path, path_lens, next_tokens, new_lens
 
 

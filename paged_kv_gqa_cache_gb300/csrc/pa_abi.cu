@@ -1156,6 +1156,7 @@ pa_status tree_move_call(TreeAcceptParams &p, const int32_t *tree_lens, const in
                           {p.block_tables, p.block_tables ? lens_bytes * max_blocks_per_seq : 0, false},
                           {p.draft, tokens * sizeof(int64_t), false},
                           {p.target, tokens * sizeof(int64_t), false},
+                          {p.context_targets, p.context_targets ? 2 * lens_bytes : 0, false},
                           {p.parents, tokens * sizeof(int32_t), false}};
   constexpr int kRanges = sizeof(ranges) / sizeof(ranges[0]);
   for (int a = 0; a < 4; ++a)
@@ -1192,21 +1193,24 @@ pa_status tree_move_call(TreeAcceptParams &p, const int32_t *tree_lens, const in
 
 }  // namespace
 
-pa_status pa_tree_accept(const int64_t *draft_tokens, const int64_t *target_tokens, const int32_t *parents,
-                         int32_t num_tokens, const int32_t *tree_lens, const int32_t *context_lens, int32_t num_seqs,
-                         const pa_kv_pool *pools, int32_t num_layers, const int32_t *block_tables,
-                         int32_t max_blocks_per_seq, int32_t *path, int32_t path_stride, int32_t *path_lens,
-                         int64_t *next_tokens, int32_t *new_context_lens, pa_stream_t stream) {
+pa_status pa_tree_accept_ex(const int64_t *draft_tokens, const int64_t *target_tokens, const int64_t *context_targets,
+                            const int32_t *parents, int32_t num_tokens, const int32_t *tree_lens,
+                            const int32_t *context_lens, int32_t num_seqs, const pa_kv_pool *pools, int32_t num_layers,
+                            const int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *path,
+                            int32_t path_stride, int32_t *path_lens, int64_t *next_tokens, int32_t *new_context_lens,
+                            pa_stream_t stream) {
   if (num_tokens < 0) return PA_ERR_SHAPE;
   if (num_seqs > 0) {
     if (!next_tokens || (num_tokens > 0 && (!draft_tokens || !target_tokens || !parents))) return PA_ERR_NULL;
     if (((reinterpret_cast<uintptr_t>(draft_tokens) | reinterpret_cast<uintptr_t>(target_tokens) |
-          reinterpret_cast<uintptr_t>(next_tokens)) & 7u) || !aligned4(parents))
+          reinterpret_cast<uintptr_t>(next_tokens) | reinterpret_cast<uintptr_t>(context_targets)) & 7u) ||
+        !aligned4(parents))
       return PA_ERR_ALIGN;
   }
   TreeAcceptParams p{};
   p.draft = draft_tokens;
   p.target = target_tokens;
+  p.context_targets = context_targets;
   p.parents = parents;
   p.num_tokens = num_tokens;
   p.path = path;
@@ -1215,6 +1219,16 @@ pa_status pa_tree_accept(const int64_t *draft_tokens, const int64_t *target_toke
   p.next_tokens = next_tokens;
   return tree_move_call(p, tree_lens, context_lens, num_seqs, pools, num_layers, block_tables, max_blocks_per_seq,
                         new_context_lens, stream);
+}
+
+pa_status pa_tree_accept(const int64_t *draft_tokens, const int64_t *target_tokens, const int32_t *parents,
+                         int32_t num_tokens, const int32_t *tree_lens, const int32_t *context_lens, int32_t num_seqs,
+                         const pa_kv_pool *pools, int32_t num_layers, const int32_t *block_tables,
+                         int32_t max_blocks_per_seq, int32_t *path, int32_t path_stride, int32_t *path_lens,
+                         int64_t *next_tokens, int32_t *new_context_lens, pa_stream_t stream) {
+  return pa_tree_accept_ex(draft_tokens, target_tokens, nullptr, parents, num_tokens, tree_lens, context_lens, num_seqs,
+                           pools, num_layers, block_tables, max_blocks_per_seq, path, path_stride, path_lens,
+                           next_tokens, new_context_lens, stream);
 }
 
 pa_status pa_tree_move(const int32_t *path, int32_t path_stride, const int32_t *path_lens, const int32_t *tree_lens,

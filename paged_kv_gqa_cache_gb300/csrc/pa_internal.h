@@ -320,6 +320,7 @@ cudaError_t launch_attn_tree(TreeParams p, void *workspace, const CUtensorMap *m
 struct TreeAcceptParams {
   const int64_t *draft;         // [num_tokens]
   const int64_t *target;
+  const int64_t *context_targets;  // [S], null: tokens without parent are accepted
   const int32_t *parents;
   const int32_t *tree_lens;     // [S]
   const int32_t *context_lens;  // [S]

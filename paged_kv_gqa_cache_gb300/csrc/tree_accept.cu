@@ -2,11 +2,12 @@
 // compacted to them, for sm_103a.
 //
 // Sequence s has n drafted tokens at cache positions L - n .. L - 1, a tree by
-// parents.  Token i is accepted when it has no parent, or when its parent is
-// accepted and draft[i] equals target[parent], what the model chose after the
-// parent.  Of the accepted tokens the deepest (of these the lowest index) ends the
-// path; the path's rows move, in every layer and in place, to positions L - n ..:
-// row L - n + path[i] to row L - n + i, so that the cache is a line again.
+// parents.  Token i is accepted when its parent is accepted and draft[i] equals
+// target[parent], what the model chose after the parent; one without parent when it
+// equals the choice after the committed context, or always where that is not given.
+// Of the accepted tokens the deepest (of these the lowest index) ends the path; the
+// path's rows move, in every layer and in place, to positions L - n ..: row L - n +
+// path[i] to row L - n + i, so that the cache is a line again.
 //
 // One launch: every CTA of a sequence finds the path itself (a few hundred bytes
 // from L2; waiting for one that does would cost another launch) and moves it in
@@ -17,8 +18,8 @@
 // barrier, no second buffer.
 // Bound by a chain of round trips (lengths, drafts, block ids, rows) where little
 // moves, by bytes where much does (8 rows of 16 bytes in flight per thread).  36 layers
-// of 8 heads, bf16: 32 sequences of 16 to 32 drafts 7.2 us (the bytes' own 4.5), 192 of
-// 33 to 64 26.5 us (22.6, 0.86 of the copy rate); one of 5 drafts, 28 layers: 2.2 us.
+// of 8 heads, bf16: 32 sequences of 16 to 32 drafts 7.4 us (the bytes' own 4.5), 192 of
+// 33 to 64 26.5 us (22.6, 0.86 of the copy rate); one of 5 drafts, 28 layers: 2.6 us.
 #include "pa_device.cuh"
 
 namespace pa {
@@ -59,6 +60,8 @@ tree_accept_kernel(const __grid_constant__ TreeAcceptParams p, int layers_per_ct
   int dep = 0;          // the path's length
   int64_t next = -1;
   if constexpr (GREEDY) {
+    const bool judged = p.context_targets != nullptr;  // (the tokens without parent, that is)
+    const int64_t choice = judged ? __ldg(p.context_targets + s) : -1;
     int64_t before = 0;  // rows of the sequences in front
     for (int j = i; j < s; j += kAcceptThreads) before += max(__ldg(p.tree_lens + j), 0);
     const int64_t row0 = block_sum(before, s_part);
@@ -74,7 +77,7 @@ tree_accept_kernel(const __grid_constant__ TreeAcceptParams p, int layers_per_ct
     ok = !__syncthreads_or(!ok || (i < n && (par < -1 || par >= i)));
     // hop: the ancestor reached, -1 above a root, -2 not accepted; depth: tokens from here to it
     int hop = -2, depth = 1;
-    if (ok && i < n && (par < 0 || draft == s_tgt[par])) hop = par;
+    if (ok && i < n && (par < 0 ? !judged || draft == choice : draft == s_tgt[par])) hop = par;
     while (true) {
       s_hop[i] = hop;
       s_dep[i] = depth;
@@ -94,6 +97,7 @@ tree_accept_kernel(const __grid_constant__ TreeAcceptParams p, int layers_per_ct
     for (int w = 0; w < kAcceptThreads / 32; ++w) best = max(best, s_best[w]);
     dep = best >> 16;
     const int node = kAcceptThreads - 1 - (best & 0xffff);
+    if (ok) next = choice;  // (nothing accepted)
     if (dep > 0) {
       next = s_tgt[node];
       if (i == 0)
