@@ -865,12 +865,18 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
                   positions: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   interleaved: bool = False, attention_factor: float = 1.0,
                   q_norm_weight: Optional[torch.Tensor] = None, k_norm_weight: Optional[torch.Tensor] = None,
-                  eps: float = 1e-6, q_out: Optional[torch.Tensor] = None, stream=None,
-                  _axes: Optional[bytes] = None) -> torch.Tensor:
+                  eps: float = 1e-6, q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rotate q [T, Hq, 128] (returned; ``q_out=q`` works in place) and k
     [T, Hkv, 128] to ``positions``, after an RMSNorm where the weights are given,
     and write the rotated k and the unchanged v into their slots.
     ``inv_freq`` (float64 [rotary_dim / 2]) sets how much of the head turns."""
+    return _rope_kv_write(q, k, v, inv_freq, positions, None, slot_mapping, k_cache, v_cache, interleaved,
+                          attention_factor, q_norm_weight, k_norm_weight, eps, q_out, stream)
+
+
+def _rope_kv_write(q, k, v, inv_freq, positions, axes: Optional[bytes], slot_mapping, k_cache, v_cache, interleaved,
+                   attention_factor, q_norm_weight, k_norm_weight, eps, q_out, stream) -> torch.Tensor:
+    """``rope_kv_write``, or with ``axes`` ``rope_kv_write_axes``."""
     dev = _device()
     pool = _pool_of(k_cache, v_cache, dev)
     dt, hkv, d = k_cache.dtype, pool.num_kv_heads, pool.head_dim
@@ -885,11 +891,11 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
     qshape = q.shape
     T, hq = qshape[:2] if len(qshape) == 3 else (0, 0)
     rows, each = (T, hkv, d), (T,)
-    if _axes is not None:
+    if axes is not None:
         if positions.dim() != 2 or positions.shape[1] != T:
             raise ValueError(f"positions must be [axes, {T}]")
-        if len(_axes) != inv_freq.numel():
-            raise ValueError(f"pair_axes names {len(_axes)} pairs, inv_freq holds {inv_freq.numel()}")
+        if len(axes) != inv_freq.numel():
+            raise ValueError(f"pair_axes names {len(axes)} pairs, inv_freq holds {inv_freq.numel()}")
     elif positions.shape != each:
         raise ValueError(f"positions must be [{T}]")
     if qshape != (T, hq, d) or k.shape != rows or v.shape != rows or slot_mapping.shape != each or inv_freq.dim() != 1:
@@ -907,9 +913,9 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: t
         wk = None if k_norm_weight is None else k_norm_weight.data_ptr()
     rope = Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], ROPE_INTERLEAVED if interleaved else ROPE_HALF,
                 attention_factor)
-    if _axes is not None:
+    if axes is not None:
         _check((_lib or load_library()).pa_rope_kv_write_axes(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(rope), _axes, positions.shape[0], wq, wk, eps,
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(rope), axes, positions.shape[0], wq, wk, eps,
             positions.data_ptr(), slot_mapping.data_ptr(), T, hq, q_out.data_ptr(), ctypes.byref(pool),
             _stream_of(stream, dev)), "pa_rope_kv_write_axes")
         return q_out
@@ -945,8 +951,8 @@ def rope_kv_write_axes(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_fr
     ``pair_axes[i]`` (bytes [rotary_dim / 2], see :func:`rope_axes`)."""
     if not isinstance(pair_axes, bytes):
         raise TypeError("pair_axes must be bytes (see rope_axes)")
-    return rope_kv_write(q, k, v, inv_freq, positions, slot_mapping, k_cache, v_cache, interleaved, attention_factor,
-                         q_norm_weight, k_norm_weight, eps, q_out, stream, _axes=pair_axes)
+    return _rope_kv_write(q, k, v, inv_freq, positions, pair_axes, slot_mapping, k_cache, v_cache, interleaved,
+                          attention_factor, q_norm_weight, k_norm_weight, eps, q_out, stream)
 
 
 def decode_shared_workspace_bytes(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int) -> int:
