@@ -790,7 +790,8 @@ PA_API pa_status pa_kv_evict_ex(const pa_kv_pool *pool, const int32_t *block_tab
  *   out[i][g] = softmax_j(scale * q[i][g] . K_j) V_j over those.
  *   q, out        [num_tokens][num_q_heads][128], pool dtype, packed as parents.
  *   context_lens  the whole lengths, drafted tokens included; at least tree_lens[s].
- *   max_context_len  also the longest sequence that is computed.
+ *   max_context_len  also the longest sequence that is computed, and what the deal of
+ *                 small calls goes by: one near the longest length is up to 15 % faster.
  *   num_tokens    rows of q, parents and out; rows behind the last tree are left as
  *                 they are.
  *   workspace     pa_tree_workspace_bytes() bytes (for the current device: it
@@ -800,8 +801,9 @@ PA_API pa_status pa_kv_evict_ex(const pa_kv_pool *pool, const int32_t *block_tab
  * The query-key and probability-value products run on the tensor cores with fp32
  * accumulation, the probabilities in two terms of the pool dtype (as
  * pa_paged_attn_decode_shared).  Keys and values of drafted tokens that a row does not
- * see have no effect on it, infinities and NaN among them; one that it sees with such
- * a value makes its output NaN.  A tree length out of range, a context shorter than
+ * see have no effect on it, infinities and NaN among them.  A value that it sees and that
+ * is one of them, and a NaN in such a key, make its output NaN; an infinite key is a score
+ * of +inf (NaN), -inf (no weight) or NaN.  A tree length out of range, a context shorter than
  * the tree or longer than max_context_len, and a tree that runs past num_tokens record
  * PA_ERR_RANGE (detail: the sequence) and its rows are left as they are.  A parent out of
  * range is recorded likewise and taken as -1.  A block id outside the pool is reported

@@ -1138,7 +1138,8 @@ def paged_attn_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     ``context_lens[s]`` cached tokens are its drafts; ``parents`` (int32 [T]) gives each
     token's parent as an index within its tree (less than its own; -1: none).  A token
     sees the committed context, its ancestors and itself.  ``max_context_len`` (default:
-    the block table's capacity) is also the longest sequence that is computed."""
+    the block table's capacity) is also the longest sequence that is computed; small
+    calls gain from one near the longest length."""
     dev = _device()
     pool = _pool_of(k_cache, v_cache, dev)
     dt, i32 = k_cache.dtype, torch.int32

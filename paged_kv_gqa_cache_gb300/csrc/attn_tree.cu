@@ -40,8 +40,9 @@
 // Measured (CUDA graphs): 192 sequences of up to 2900 tokens, chains of 1 to 8 drafts,
 // 16 / 8 heads, bf16: 188 us, 0.94 of the copy rate; 32 of 100 to 8192, 16 to 32 drafts,
 // 32 / 8: 96.3, 0.80; 5 of 40000 to 100001, 9 to 13 drafts, 32 / 4: 133, 0.86; 8 of 8000
-// to 32768, 60 to 64 drafts (two query tiles), 32 / 8, fp16: 201, 0.53; one of 777, 5
-// drafts: 11.0, a chain of latencies (plan, one key tile, join).  With one query tile
+// to 32768, 60 to 64 drafts (two query tiles), 32 / 8, fp16: 198, 0.54 (in bursts at 2
+// GHz; 232 where thousands of calls in a row bring the SMs to 1.5 GHz under the power
+// cap, which the calls that HBM bounds do not feel); one of 777, 5 drafts: 11.0, a chain of latencies (plan, one key tile, join).  With one query tile
 // 152 equal contexts of 8192 run at 0.95; ragged batches lose what the SMs' unequal
 // speeds leave at the end.  With two a pair takes 1.3 us, the tensor pipe 67 % busy: P
 // waits for S, S for the P V that has left its columns, and tensor memory's loads and
@@ -954,7 +955,11 @@ cudaError_t launch_tree_typed(TreeParams p, const CUtensorMap *maps, int sms, cu
   cudaError_t e = kernel_setup(setup, attn_tree_kernel<T, G, NT>, smem, kTThreads, nullptr);
   if (e != cudaSuccess) return e;
   const int workers = sms / NT > 0 ? sms / NT : 1;
-  // (calls of a few key tiles per worker are not dealt but spread: there the cost would leave workers without keys)
+  // A call of a few key tiles per worker, by the bound on its lengths, is spread as evenly as its
+  // key tiles go, without the runs' cost, which would leave workers without keys: 4 sequences of
+  // 300 with 8 drafts, 32 / 8 heads, 12.7 us against 14.6, one of 777, 16 / 8, 11.2 against 12.4;
+  // 16 of 500, 16 / 8, 18.3 against 17.6, and 4 of 600 with 60 drafts, 32 / 8, 20.3 against 18.7.
+  // The lengths themselves are not known here: a bound far above them has the second figures.
   const int64_t groups = (int64_t)p.num_kv_heads * (p.num_seqs + (int64_t)p.num_tokens * G / (128 * NT));
   p.run_cost = groups * ((p.max_len + 127) / 128) > 4 * workers ? kTreeRunCost : 0;
   const dim3 grid(workers * NT), block(kTThreads);

@@ -19,7 +19,7 @@
 // Bound by a chain of round trips (lengths, drafts, block ids, rows) where little
 // moves, by bytes where much does (8 rows of 16 bytes in flight per thread).  36 layers
 // of 8 heads, bf16: 32 sequences of 16 to 32 drafts 7.4 us (the bytes' own 4.5), 192 of
-// 33 to 64 26.5 us (22.6, 0.86 of the copy rate); one of 5 drafts, 28 layers: 2.6 us.
+// 33 to 64 26.6 us (22.6, 0.85 of the copy rate); one of 5 drafts, 28 layers: 2.6 us.
 #include "pa_device.cuh"
 
 namespace pa {
